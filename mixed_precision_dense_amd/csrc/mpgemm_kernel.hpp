@@ -881,11 +881,14 @@ constexpr int tile_lds_bytes() {
 }
 
 // ---------------------------------------------------------------------------------------
-// One BM x BN tile of D (tile row tm, tile column tn) by one workgroup; smem holds at least
-// tile_lds_bytes() of LDS.
+// The product op(A) op(B) of one BM x BN tile (first row m0, first column n0) by one workgroup,
+// into acc; smem holds at least tile_lds_bytes() of LDS.  When it returns, this wave's loads have
+// landed and its accumulators can be read; other waves may still be reading fragments, so the
+// LDS is free for the epilogue only after a barrier.
 // ---------------------------------------------------------------------------------------
-template <int IN, int OUT, bool TA, bool TB, int BM, int BN, int NW>
-__device__ __forceinline__ void gemm_tile(const Params &p, int tm, int tn, lds_char *smem) {
+template <int IN, bool TA, bool TB, int BM, int BN, int NW>
+__device__ __forceinline__ void tile_product(const Params &p, int m0, int n0, lds_char *smem,
+                                             typename MmaAcc<IN>::type (&acc)[BM / 32][BN / (8 * NW)]) {
     constexpr bool kF8 = is_fp8(IN);
     static_assert(NW == 4 || (NW == 8 && !kF8), "4 waves, or 8 for 2-byte and INT8 inputs");
     constexpr int EB = (IN == IN_I8 || kF8) ? 1 : 2;
@@ -911,9 +914,7 @@ __device__ __forceinline__ void gemm_tile(const Params &p, int tm, int tn, lds_c
     const int wm = wave / (NW / 2), wn = wave % (NW / 2);
     const int vq = wave & 3, hi = wave >> 2;    // the quarter and position group it loads
 
-    const int m0 = tm * BM, n0 = tn * BN;
     const int m_left = p.m - m0, n_left = p.n - n0;
-    const bool full_mn = (m_left >= BM) && (n_left >= BN);
 
     OpA opa;
     OpB opb;
@@ -944,7 +945,6 @@ __device__ __forceinline__ void gemm_tile(const Params &p, int tm, int tn, lds_c
         cb.last_records = (int)(lb < 0 ? 0 : (lb > kNumRecords ? kNumRecords : lb));
     }
 
-    acc_t acc[FM][FN];
 #pragma unroll
     for (int i = 0; i < FM; ++i)
 #pragma unroll
@@ -1294,8 +1294,27 @@ __device__ __forceinline__ void gemm_tile(const Params &p, int tm, int tn, lds_c
     }
     wait_vmem<0>();  // no direct load into LDS is left in flight when the workgroup ends
     drain_mfma(acc);
+}
 
-    // ---- epilogue
+// ---------------------------------------------------------------------------------------
+// One BM x BN tile of D (tile row tm, tile column tn) by one workgroup; smem holds at least
+// tile_lds_bytes() of LDS.
+// ---------------------------------------------------------------------------------------
+template <int IN, int OUT, bool TA, bool TB, int BM, int BN, int NW>
+__device__ __forceinline__ void gemm_tile(const Params &p, int tm, int tn, lds_char *smem) {
+    constexpr int EB = (IN == IN_I8 || is_fp8(IN)) ? 1 : 2;
+    constexpr int FM = BM / 32, FN = BN / (8 * NW);
+    constexpr int A_BYTES = Operand<EB, !TA, BM / 32, NW / 4>::kStageBytes;
+    constexpr int B_BYTES = Operand<EB, TB, BN / 32, NW / 4>::kStageBytes;
+    const int m0 = tm * BM, n0 = tn * BN;
+    const int m_left = p.m - m0, n_left = p.n - n0;
+    const bool full_mn = (m_left >= BM) && (n_left >= BN);
+    const int wave = threadIdx.x / 64, lane = threadIdx.x % 64;
+    const int wm = wave / (NW / 2), wn = wave % (NW / 2);
+
+    typename MmaAcc<IN>::type acc[FM][FN];
+    tile_product<IN, TA, TB, BM, BN, NW>(p, m0, n0, smem, acc);
+
     // (full_mn, p.read_c and the wave index are uniform across a wave)
     // The lane index passes through an empty statement here, so that the epilogue's per-lane
     // addresses are computed after the loop rather than held in registers across it.
