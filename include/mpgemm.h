@@ -281,6 +281,192 @@ const char *mpgemm_status_string(mpgemm_status_t status);
 mpgemm_status_t mpgemm_tile_shape(int64_t m, int64_t n, mpgemm_dtype_t a_type, int *tile_m,
                                   int *tile_n);
 
+/* ---------------------------------------------------------------------------------------
+ * Products of language models: a product with its bias, activation and residual, the same for
+ * rows divided among experts, and the cross entropy of a linear layer; each with its gradients.
+ *
+ * Types: the inputs of a product are both MPGEMM_R_16F or both MPGEMM_R_16BF, the output (and a C
+ * that is read) that type or MPGEMM_R_32F, scalars are FP32.  Products are accumulated as
+ * mpgemm_run's; everything after them is computed in FP32 and rounded once, to nearest even,
+ * where it is stored.  Storage, alignment (16-byte pointers, row strides that are multiples of
+ * 16 bytes and below the same limit), ownership, ordering and errors are mpgemm_run's; C, aux
+ * and Z are, like A and B, read in whole aligned 16-byte blocks.  Sizes go up to 2^31 - 256.
+ * The results of a call do not depend on other calls and are the same each time.
+ * A workspace is device memory of the size that the named function gives, 256-byte aligned, owned
+ * by the caller, overwritten, and in use until the queued work finishes: NULL or too small
+ * returns MPGEMM_STATUS_INVALID_VALUE, misaligned MPGEMM_STATUS_NOT_SUPPORTED.  Nothing is
+ * allocated and no call waits for the device, so all of them can be captured into a graph.
+ * --------------------------------------------------------------------------------------- */
+typedef enum {
+    MPGEMM_ACT_NONE = 0,
+    MPGEMM_ACT_RELU = 1,      /* max(z, 0); slope 0 at 0 */
+    MPGEMM_ACT_GELU = 2,      /* z Phi(z) */
+    MPGEMM_ACT_GELU_TANH = 3, /* z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) / 2 */
+    MPGEMM_ACT_SILU = 4       /* z / (1 + exp(-z)) */
+} mpgemm_act_t;
+
+typedef struct {
+    int act;                  /* an mpgemm_act_t */
+    const void *bias;         /* n values, added to every row; NULL: none */
+    int bias_type;            /* an mpgemm_dtype_t: the inputs' type or MPGEMM_R_32F */
+    int64_t bias_stride;      /* grouped products: elements between two experts' biases (0: one
+                                 bias for all); otherwise ignored */
+    void *aux;                /* receives Z (m x n, the inputs' type); NULL: not kept */
+    int64_t ld_aux;           /* elements, >= n */
+} mpgemm_epilogue_t;
+
+/* Queue  Z = alpha * op(A) * op(B) + bias,  D = act(Z) + beta * C.
+ *   C is read only when *beta != 0 and may have another type and leading dimension than D; D == C
+ *   is allowed when they are alike in both.  Z, when kept, must not overlap any other argument.
+ *   The activation is taken from Z before its rounding.  k == 0 gives Z = bias. */
+mpgemm_status_t mpgemm_run_epilogue(mpgemm_handle_t handle, mpgemm_op_t transa, mpgemm_op_t transb,
+                                    int64_t m, int64_t n, int64_t k, const float *alpha,
+                                    const void *A, mpgemm_dtype_t a_type, int64_t lda,
+                                    const void *B, mpgemm_dtype_t b_type, int64_t ldb,
+                                    const mpgemm_epilogue_t *epilogue, const float *beta,
+                                    const void *C, mpgemm_dtype_t c_type, int64_t ldc, void *D,
+                                    mpgemm_dtype_t d_type, int64_t ldd, void *stream);
+
+/* Queue the gradient that comes through an activation:
+ *   D(i, j) = alpha * (op(A) op(B))(i, j) * act'(Z(i, j)),   dbias(j) = sum over i of D(i, j)
+ * with Z as mpgemm_run_epilogue kept it (the inputs' type; not read for MPGEMM_ACT_NONE), and dbias
+ * n FP32 values, summed in FP32 before D's rounding in a fixed order; NULL: not computed, and
+ * no workspace is needed.  m == 0 gives dbias = 0.
+ *   workspace: mpgemm_epilogue_grad_workspace_size(1, m, n) bytes. */
+mpgemm_status_t mpgemm_run_epilogue_grad(mpgemm_handle_t handle, mpgemm_op_t transa,
+                                         mpgemm_op_t transb, int64_t m, int64_t n, int64_t k,
+                                         const float *alpha, const void *A, mpgemm_dtype_t a_type,
+                                         int64_t lda, const void *B, mpgemm_dtype_t b_type,
+                                         int64_t ldb, mpgemm_act_t act, const void *Z, int64_t ldz,
+                                         void *D, mpgemm_dtype_t d_type, int64_t ldd, float *dbias,
+                                         void *workspace, uint64_t workspace_bytes, void *stream);
+
+/* Queue one product for each expert's rows: row r of expert e, offsets[e] <= r < offsets[e + 1],
+ *   Z(r, :) = alpha * A(r, :) * op(B_e) + bias_e,   D(r, :) = act(Z(r, :)).
+ *   A: rows x k (ld lda), D: rows x n, Z (epilogue->aux): rows x n.
+ *   B_e: k x n (transb == N) or n x k (transb == T) at B + e * stride_b elements; stride_b is a
+ *        multiple of 8, and 0 gives all experts the same one.
+ *   offsets: groups + 1 non-decreasing device integers from 0 to rows; an expert may have no
+ *        rows, and rows of no expert keep what D and Z held.  They are read by the queued kernels,
+ *        never by the host; values outside the contract are clamped, so that no memory outside
+ *        the operands is touched, but the results are then unspecified.
+ *   groups goes up to 65535. */
+mpgemm_status_t mpgemm_run_grouped(mpgemm_handle_t handle, mpgemm_op_t transb, int64_t groups,
+                                   int64_t rows, int64_t n, int64_t k, const float *alpha,
+                                   const void *A, mpgemm_dtype_t a_type, int64_t lda,
+                                   const int32_t *offsets, const void *B, mpgemm_dtype_t b_type,
+                                   int64_t ldb, int64_t stride_b, const mpgemm_epilogue_t *epilogue,
+                                   void *D, mpgemm_dtype_t d_type, int64_t ldd, void *stream);
+
+/* mpgemm_run_epilogue_grad for experts' rows: D(r, :) = alpha * A(r, :) op(B_e) * act'(Z(r, :)),
+ * dbias(e, :) = sum of expert e's rows of D (groups x n FP32 values, 0 for an expert without rows).
+ *   workspace: mpgemm_epilogue_grad_workspace_size(groups, rows, n) bytes (none without dbias). */
+mpgemm_status_t mpgemm_run_grouped_grad(mpgemm_handle_t handle, mpgemm_op_t transb, int64_t groups,
+                                        int64_t rows, int64_t n, int64_t k, const float *alpha,
+                                        const void *A, mpgemm_dtype_t a_type, int64_t lda,
+                                        const int32_t *offsets, const void *B,
+                                        mpgemm_dtype_t b_type, int64_t ldb, int64_t stride_b,
+                                        mpgemm_act_t act, const void *Z, int64_t ldz, void *D,
+                                        mpgemm_dtype_t d_type, int64_t ldd, float *dbias,
+                                        void *workspace, uint64_t workspace_bytes, void *stream);
+
+/* Queue the gradients of the experts' weights: for each expert
+ *   D_e = alpha * A_e^T X_e + beta * D_e          (m x n at D + e * stride_d elements)
+ * where A_e (rows x m as a whole, ld lda) and X_e (rows x n, ld ldx) are expert e's rows.  An
+ * expert without rows gets beta * D_e.  D is read only when *beta != 0.  The experts' D must not
+ * overlap: stride_d >= (m - 1) * ldd + n, a multiple of 16 bytes. */
+mpgemm_status_t mpgemm_run_grouped_wgrad(mpgemm_handle_t handle, int64_t groups, int64_t rows,
+                                         int64_t m, int64_t n, const float *alpha, const void *A,
+                                         mpgemm_dtype_t a_type, int64_t lda, const void *X,
+                                         mpgemm_dtype_t x_type, int64_t ldx, const int32_t *offsets,
+                                         const float *beta, void *D, mpgemm_dtype_t d_type,
+                                         int64_t ldd, int64_t stride_d, void *stream);
+
+/* Queue the softmax cross entropy of a linear layer, without storing its logits:
+ *   z(i, v) = alpha * X(i, :) . W(v, :),   lse(i) = log(sum over v of exp(z(i, v))),
+ *   loss(i) = lse(i) - z(i, target(i)),  0 where the target does not count.
+ *   X: m x k, W: n x k (type MPGEMM_R_16F or MPGEMM_R_16BF both), n >= 1.
+ *   target: m device integers; one outside 0 .. n - 1 (-1 or -100, as a rule) does not count.
+ *   loss, lse: m FP32 values each (lse of every row).
+ *   workspace: mpgemm_linear_ce_workspace_size(m, n, k, type, 0) bytes. */
+mpgemm_status_t mpgemm_run_linear_ce(mpgemm_handle_t handle, int64_t m, int64_t n, int64_t k,
+                                     const float *alpha, const void *X, mpgemm_dtype_t type,
+                                     int64_t ldx, const void *W, int64_t ldw, const int64_t *target,
+                                     float *loss, float *lse, void *workspace,
+                                     uint64_t workspace_bytes, void *stream);
+
+/* Queue its gradients: with P(i, v) = (exp(z(i, v) - lse(i)) - [v == target(i)]) * grad(i), and 0 in
+ * rows whose target does not count,
+ *   dX = alpha * P W,   dW = alpha * P^T X      (type's; either may be NULL and is then skipped).
+ *   lse: as mpgemm_run_linear_ce wrote it.  grad: m FP32 values, the gradient of each row's loss.
+ *   P is computed in pieces of the vocabulary and rounded to the inputs' type for the products
+ *   (FP16: scaled by a power of two first, so that small probabilities stay normal).
+ *   workspace: mpgemm_linear_ce_workspace_size(m, n, k, type, 1) bytes, which is also enough for
+ *   mpgemm_run_linear_ce. */
+mpgemm_status_t mpgemm_run_linear_ce_grad(mpgemm_handle_t handle, int64_t m, int64_t n, int64_t k,
+                                          const float *alpha, const void *X, mpgemm_dtype_t type,
+                                          int64_t ldx, const void *W, int64_t ldw,
+                                          const int64_t *target, const float *lse,
+                                          const float *grad, void *dX, int64_t lddx, void *dW,
+                                          int64_t lddw, void *workspace, uint64_t workspace_bytes,
+                                          void *stream);
+
+/* Workspace bytes of the gradients above for dbias (groups == 1 for mpgemm_run_epilogue_grad), and
+ * of the cross entropy (train != 0: of its gradients too).  0 for sizes or types outside the
+ * contract and where no workspace is needed.  Host-only. */
+uint64_t mpgemm_epilogue_grad_workspace_size(int64_t groups, int64_t m, int64_t n);
+uint64_t mpgemm_linear_ce_workspace_size(int64_t m, int64_t n, int64_t k, mpgemm_dtype_t type,
+                                         int train);
+
+/* Host-only argument checks of the entry points above (as mpgemm_check is for mpgemm_run). */
+mpgemm_status_t mpgemm_check_epilogue(mpgemm_op_t transa, mpgemm_op_t transb, int64_t m, int64_t n,
+                                      int64_t k, const float *alpha, const void *A,
+                                      mpgemm_dtype_t a_type, int64_t lda, const void *B,
+                                      mpgemm_dtype_t b_type, int64_t ldb,
+                                      const mpgemm_epilogue_t *epilogue, const float *beta,
+                                      const void *C, mpgemm_dtype_t c_type, int64_t ldc,
+                                      const void *D, mpgemm_dtype_t d_type, int64_t ldd);
+mpgemm_status_t mpgemm_check_epilogue_grad(mpgemm_op_t transa, mpgemm_op_t transb, int64_t m,
+                                           int64_t n, int64_t k, const float *alpha, const void *A,
+                                           mpgemm_dtype_t a_type, int64_t lda, const void *B,
+                                           mpgemm_dtype_t b_type, int64_t ldb, mpgemm_act_t act,
+                                           const void *Z, int64_t ldz, const void *D,
+                                           mpgemm_dtype_t d_type, int64_t ldd, const float *dbias,
+                                           const void *workspace, uint64_t workspace_bytes);
+mpgemm_status_t mpgemm_check_grouped(mpgemm_op_t transb, int64_t groups, int64_t rows, int64_t n,
+                                     int64_t k, const float *alpha, const void *A,
+                                     mpgemm_dtype_t a_type, int64_t lda, const int32_t *offsets,
+                                     const void *B, mpgemm_dtype_t b_type, int64_t ldb,
+                                     int64_t stride_b, const mpgemm_epilogue_t *epilogue,
+                                     const void *D, mpgemm_dtype_t d_type, int64_t ldd);
+mpgemm_status_t mpgemm_check_grouped_grad(mpgemm_op_t transb, int64_t groups, int64_t rows,
+                                          int64_t n, int64_t k, const float *alpha, const void *A,
+                                          mpgemm_dtype_t a_type, int64_t lda,
+                                          const int32_t *offsets, const void *B,
+                                          mpgemm_dtype_t b_type, int64_t ldb, int64_t stride_b,
+                                          mpgemm_act_t act, const void *Z, int64_t ldz,
+                                          const void *D, mpgemm_dtype_t d_type, int64_t ldd,
+                                          const float *dbias, const void *workspace,
+                                          uint64_t workspace_bytes);
+mpgemm_status_t mpgemm_check_grouped_wgrad(int64_t groups, int64_t rows, int64_t m, int64_t n,
+                                           const float *alpha, const void *A,
+                                           mpgemm_dtype_t a_type, int64_t lda, const void *X,
+                                           mpgemm_dtype_t x_type, int64_t ldx,
+                                           const int32_t *offsets, const float *beta,
+                                           const void *D, mpgemm_dtype_t d_type, int64_t ldd,
+                                           int64_t stride_d);
+mpgemm_status_t mpgemm_check_linear_ce(int64_t m, int64_t n, int64_t k, const float *alpha,
+                                       const void *X, mpgemm_dtype_t type, int64_t ldx,
+                                       const void *W, int64_t ldw, const int64_t *target,
+                                       const float *loss, const float *lse, const void *workspace,
+                                       uint64_t workspace_bytes);
+mpgemm_status_t mpgemm_check_linear_ce_grad(int64_t m, int64_t n, int64_t k, const float *alpha,
+                                            const void *X, mpgemm_dtype_t type, int64_t ldx,
+                                            const void *W, int64_t ldw, const int64_t *target,
+                                            const float *lse, const float *grad, const void *dX,
+                                            int64_t lddx, const void *dW, int64_t lddw,
+                                            const void *workspace, uint64_t workspace_bytes);
+
 #ifdef __cplusplus
 }
 #endif

@@ -29,6 +29,7 @@ STATUS = {0: "SUCCESS", 1: "NOT_INITIALIZED", 2: "INVALID_VALUE", 3: "NOT_SUPPOR
           8: "WRONG_DEVICE", 9: "SCRATCH_TOO_SMALL"}
 SUCCESS = 0
 NOALLOC_SCRATCH_BYTES = 64 << 20   # MPGEMM_NOALLOC_SCRATCH_BYTES
+ACTS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}   # mpgemm_act_t
 
 _lib: Optional[ctypes.CDLL] = None
 
@@ -61,7 +62,29 @@ SIGNATURES = {
     "mpgemm_check_bf16x3": (_i32, [_i32, _i32, _i64, _i64, _i64, _vp, _vp, _i64, _vp, _i64, _vp,
                                    _vp, _i64, _vp, _vp, _u64]),
     "mpgemm_bf16x3_workspace_size": (_u64, [_i32, _i32, _i64, _i64, _i64]),
+    "mpgemm_epilogue_grad_workspace_size": (_u64, [_i64, _i64, _i64]),
+    "mpgemm_linear_ce_workspace_size": (_u64, [_i64, _i64, _i64, _i32, _i32]),
 }
+# Arguments of the products of language models: the check's, and the run's with the handle before
+# and the stream after them.
+_OPS = {
+    "epilogue": [_i32, _i32, _i64, _i64, _i64, _vp, _vp, _i32, _i64, _vp, _i32, _i64, _vp, _vp, _vp,
+                 _i32, _i64, _vp, _i32, _i64],
+    "epilogue_grad": [_i32, _i32, _i64, _i64, _i64, _vp, _vp, _i32, _i64, _vp, _i32, _i64, _i32, _vp,
+                      _i64, _vp, _i32, _i64, _vp, _vp, _u64],
+    "grouped": [_i32, _i64, _i64, _i64, _i64, _vp, _vp, _i32, _i64, _vp, _vp, _i32, _i64, _i64, _vp,
+                _vp, _i32, _i64],
+    "grouped_grad": [_i32, _i64, _i64, _i64, _i64, _vp, _vp, _i32, _i64, _vp, _vp, _i32, _i64, _i64,
+                     _i32, _vp, _i64, _vp, _i32, _i64, _vp, _vp, _u64],
+    "grouped_wgrad": [_i64, _i64, _i64, _i64, _vp, _vp, _i32, _i64, _vp, _i32, _i64, _vp, _vp, _vp,
+                      _i32, _i64, _i64],
+    "linear_ce": [_i64, _i64, _i64, _vp, _vp, _i32, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _u64],
+    "linear_ce_grad": [_i64, _i64, _i64, _vp, _vp, _i32, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _i64,
+                       _vp, _i64, _vp, _u64],
+}
+for _name, _args in _OPS.items():
+    SIGNATURES["mpgemm_run_" + _name] = (_i32, [_vp, *_args, _vp])
+    SIGNATURES["mpgemm_check_" + _name] = (_i32, _args)
 
 
 def declare(lib: ctypes.CDLL) -> ctypes.CDLL:
@@ -244,6 +267,191 @@ def mpgemm_tile_shape(m: int, n: int, a_type="f16") -> tuple:
     if st != SUCCESS:
         raise MpgemmError(st, "mpgemm_tile_shape")
     return tm.value, tn.value
+
+
+# ------------------------------------------------------------------- products of language models
+# Arguments in the C ABI's order; alpha, beta and the activation as Python values, pointers as
+# tensors or integers, types as names or enum values.  Each run has a host-only check beside it
+# with the same arguments but the handle and the stream.
+class _EpilogueStruct(ctypes.Structure):
+    _fields_ = [("act", _i32), ("bias", _vp), ("bias_type", _i32), ("bias_stride", _i64),
+                ("aux", _vp), ("ld_aux", _i64)]
+
+
+class Epilogue:
+    """mpgemm_epilogue_t: activation, bias (of ``bias_type``, ``bias_stride`` elements from one
+    expert's to the next's) and where the value before the activation is kept.  Holds its tensors."""
+
+    __slots__ = ("struct", "held")
+
+    def __init__(self, act="none", bias=None, bias_type="f32", aux=None, ld_aux=0, bias_stride=0):
+        self.held = (bias, aux)
+        self.struct = _EpilogueStruct(_act(act), _ptr(bias), _dtype(bias_type), bias_stride, _ptr(aux),
+                                      ld_aux)
+
+
+def _act(act: Union[str, int]) -> int:
+    return ACTS[act] if isinstance(act, str) else int(act)
+
+
+def _f32(v):
+    return ctypes.byref(ctypes.c_float(v))
+
+
+def _epi(e: Optional[Epilogue]):
+    return None if e is None else ctypes.byref(e.struct)
+
+
+def _run(name: str, handle, args, stream, check: bool) -> int:
+    st = getattr(load(), name)(handle, *args, _stream(stream))
+    if check and st != SUCCESS:
+        raise MpgemmError(st, name)
+    return st
+
+
+def _epilogue_args(transa, transb, m, n, k, alpha, A, a_type, lda, B, b_type, ldb, epilogue, beta, C,
+                   c_type, ldc, D, d_type, ldd):
+    return (_op(transa), _op(transb), m, n, k, _f32(alpha), _ptr(A), _dtype(a_type), lda, _ptr(B),
+            _dtype(b_type), ldb, _epi(epilogue), _f32(beta), _ptr(C), _dtype(c_type), ldc, _ptr(D),
+            _dtype(d_type), ldd)
+
+
+def mpgemm_run_epilogue(handle, transa, transb, m, n, k, alpha, A, a_type, lda, B, b_type, ldb,
+                        epilogue, beta, C, c_type, ldc, D, d_type, ldd, stream=None,
+                        check: bool = True) -> int:
+    """Queue D = act(alpha op(A) op(B) + bias) + beta C."""
+    return _run("mpgemm_run_epilogue", handle,
+                _epilogue_args(transa, transb, m, n, k, alpha, A, a_type, lda, B, b_type, ldb, epilogue,
+                               beta, C, c_type, ldc, D, d_type, ldd), stream, check)
+
+
+def mpgemm_check_epilogue(*args) -> int:
+    return load().mpgemm_check_epilogue(*_epilogue_args(*args))
+
+
+def _epilogue_grad_args(transa, transb, m, n, k, alpha, A, a_type, lda, B, b_type, ldb, act, Z, ldz, D,
+                        d_type, ldd, dbias, workspace, workspace_bytes):
+    return (_op(transa), _op(transb), m, n, k, _f32(alpha), _ptr(A), _dtype(a_type), lda, _ptr(B),
+            _dtype(b_type), ldb, _act(act), _ptr(Z), ldz, _ptr(D), _dtype(d_type), ldd, _ptr(dbias),
+            _ptr(workspace), workspace_bytes)
+
+
+def mpgemm_run_epilogue_grad(handle, transa, transb, m, n, k, alpha, A, a_type, lda, B, b_type, ldb,
+                             act, Z, ldz, D, d_type, ldd, dbias, workspace, workspace_bytes,
+                             stream=None, check: bool = True) -> int:
+    """Queue D = alpha op(A) op(B) act'(Z) and dbias, the column sums of D."""
+    return _run("mpgemm_run_epilogue_grad", handle,
+                _epilogue_grad_args(transa, transb, m, n, k, alpha, A, a_type, lda, B, b_type, ldb, act,
+                                    Z, ldz, D, d_type, ldd, dbias, workspace, workspace_bytes),
+                stream, check)
+
+
+def mpgemm_check_epilogue_grad(*args) -> int:
+    return load().mpgemm_check_epilogue_grad(*_epilogue_grad_args(*args))
+
+
+def _grouped_args(transb, groups, rows, n, k, alpha, A, a_type, lda, offsets, B, b_type, ldb, stride_b,
+                  epilogue, D, d_type, ldd):
+    return (_op(transb), groups, rows, n, k, _f32(alpha), _ptr(A), _dtype(a_type), lda, _ptr(offsets),
+            _ptr(B), _dtype(b_type), ldb, stride_b, _epi(epilogue), _ptr(D), _dtype(d_type), ldd)
+
+
+def mpgemm_run_grouped(handle, transb, groups, rows, n, k, alpha, A, a_type, lda, offsets, B, b_type,
+                       ldb, stride_b, epilogue, D, d_type, ldd, stream=None, check: bool = True) -> int:
+    """Queue D(r) = act(alpha A(r) op(B_e) + bias_e) for the rows r of every expert e."""
+    return _run("mpgemm_run_grouped", handle,
+                _grouped_args(transb, groups, rows, n, k, alpha, A, a_type, lda, offsets, B, b_type, ldb,
+                              stride_b, epilogue, D, d_type, ldd), stream, check)
+
+
+def mpgemm_check_grouped(*args) -> int:
+    return load().mpgemm_check_grouped(*_grouped_args(*args))
+
+
+def _grouped_grad_args(transb, groups, rows, n, k, alpha, A, a_type, lda, offsets, B, b_type, ldb,
+                       stride_b, act, Z, ldz, D, d_type, ldd, dbias, workspace, workspace_bytes):
+    return (_op(transb), groups, rows, n, k, _f32(alpha), _ptr(A), _dtype(a_type), lda, _ptr(offsets),
+            _ptr(B), _dtype(b_type), ldb, stride_b, _act(act), _ptr(Z), ldz, _ptr(D), _dtype(d_type), ldd,
+            _ptr(dbias), _ptr(workspace), workspace_bytes)
+
+
+def mpgemm_run_grouped_grad(handle, transb, groups, rows, n, k, alpha, A, a_type, lda, offsets, B,
+                            b_type, ldb, stride_b, act, Z, ldz, D, d_type, ldd, dbias, workspace,
+                            workspace_bytes, stream=None, check: bool = True) -> int:
+    """Queue D(r) = alpha A(r) op(B_e) act'(Z(r)) and dbias(e), the sum of expert e's rows of D."""
+    return _run("mpgemm_run_grouped_grad", handle,
+                _grouped_grad_args(transb, groups, rows, n, k, alpha, A, a_type, lda, offsets, B, b_type,
+                                   ldb, stride_b, act, Z, ldz, D, d_type, ldd, dbias, workspace,
+                                   workspace_bytes), stream, check)
+
+
+def mpgemm_check_grouped_grad(*args) -> int:
+    return load().mpgemm_check_grouped_grad(*_grouped_grad_args(*args))
+
+
+def _grouped_wgrad_args(groups, rows, m, n, alpha, A, a_type, lda, X, x_type, ldx, offsets, beta, D,
+                        d_type, ldd, stride_d):
+    return (groups, rows, m, n, _f32(alpha), _ptr(A), _dtype(a_type), lda, _ptr(X), _dtype(x_type), ldx,
+            _ptr(offsets), _f32(beta), _ptr(D), _dtype(d_type), ldd, stride_d)
+
+
+def mpgemm_run_grouped_wgrad(handle, groups, rows, m, n, alpha, A, a_type, lda, X, x_type, ldx, offsets,
+                             beta, D, d_type, ldd, stride_d, stream=None, check: bool = True) -> int:
+    """Queue D_e = alpha A_e^T X_e + beta D_e for every expert e."""
+    return _run("mpgemm_run_grouped_wgrad", handle,
+                _grouped_wgrad_args(groups, rows, m, n, alpha, A, a_type, lda, X, x_type, ldx, offsets,
+                                    beta, D, d_type, ldd, stride_d), stream, check)
+
+
+def mpgemm_check_grouped_wgrad(*args) -> int:
+    return load().mpgemm_check_grouped_wgrad(*_grouped_wgrad_args(*args))
+
+
+def _linear_ce_args(m, n, k, alpha, X, dtype, ldx, W, ldw, target, loss, lse, workspace,
+                    workspace_bytes):
+    return (m, n, k, _f32(alpha), _ptr(X), _dtype(dtype), ldx, _ptr(W), ldw, _ptr(target), _ptr(loss),
+            _ptr(lse), _ptr(workspace), workspace_bytes)
+
+
+def mpgemm_run_linear_ce(handle, m, n, k, alpha, X, dtype, ldx, W, ldw, target, loss, lse, workspace,
+                         workspace_bytes, stream=None, check: bool = True) -> int:
+    """Queue each row's softmax cross entropy (and log-sum-exp) of the logits alpha X W^T."""
+    return _run("mpgemm_run_linear_ce", handle,
+                _linear_ce_args(m, n, k, alpha, X, dtype, ldx, W, ldw, target, loss, lse, workspace,
+                                workspace_bytes), stream, check)
+
+
+def mpgemm_check_linear_ce(*args) -> int:
+    return load().mpgemm_check_linear_ce(*_linear_ce_args(*args))
+
+
+def _linear_ce_grad_args(m, n, k, alpha, X, dtype, ldx, W, ldw, target, lse, grad, dX, lddx, dW, lddw,
+                         workspace, workspace_bytes):
+    return (m, n, k, _f32(alpha), _ptr(X), _dtype(dtype), ldx, _ptr(W), ldw, _ptr(target), _ptr(lse),
+            _ptr(grad), _ptr(dX), lddx, _ptr(dW), lddw, _ptr(workspace), workspace_bytes)
+
+
+def mpgemm_run_linear_ce_grad(handle, m, n, k, alpha, X, dtype, ldx, W, ldw, target, lse, grad, dX,
+                              lddx, dW, lddw, workspace, workspace_bytes, stream=None,
+                              check: bool = True) -> int:
+    """Queue the gradients dX and dW (either may be None) of the rows' losses weighted by grad."""
+    return _run("mpgemm_run_linear_ce_grad", handle,
+                _linear_ce_grad_args(m, n, k, alpha, X, dtype, ldx, W, ldw, target, lse, grad, dX, lddx,
+                                     dW, lddw, workspace, workspace_bytes), stream, check)
+
+
+def mpgemm_check_linear_ce_grad(*args) -> int:
+    return load().mpgemm_check_linear_ce_grad(*_linear_ce_grad_args(*args))
+
+
+def mpgemm_epilogue_grad_workspace_size(groups: int, m: int, n: int) -> int:
+    """Workspace bytes of mpgemm_run_epilogue_grad (groups = 1) and mpgemm_run_grouped_grad for dbias."""
+    return load().mpgemm_epilogue_grad_workspace_size(groups, m, n)
+
+
+def mpgemm_linear_ce_workspace_size(m: int, n: int, k: int, dtype, train: bool) -> int:
+    """Workspace bytes of mpgemm_run_linear_ce, with train of its gradients too."""
+    return load().mpgemm_linear_ce_workspace_size(m, n, k, _dtype(dtype), 1 if train else 0)
 
 
 class Handle:

@@ -10,16 +10,11 @@
 #include <string.h>
 
 #include "mpgemm.h"
+#include "mpgemm_handle.hpp"
 #include "mpgemm_host.hpp"
 #include "mpgemm_kernel.hpp"
 
 using namespace mpg_host;
-
-struct mpgemm_handle_s {
-    int device;
-    int num_cus;
-    void *scratch;   // this device's address of `scratch` (below), or nullptr
-};
 
 // Fixed scratch buffer of mpgemm_run_bf16x3_noalloc, for callers that cannot allocate: it
 // holds the BF16 pieces of the split operands, laid out as mpgemm_run_bf16x3's workspace.
@@ -33,11 +28,6 @@ namespace {
 
 std::mutex g_handles_mu;
 std::set<mpgemm_handle_t> g_handles;  // live handles; lets destroyed ones be recognised
-
-bool handle_live(mpgemm_handle_t h) {
-    std::lock_guard<std::mutex> lock(g_handles_mu);
-    return g_handles.count(h) != 0;
-}
 
 std::mutex g_scratch_mu;
 std::map<int, void *> g_scratch_addr;   // device -> address of `scratch` on that device
@@ -58,6 +48,21 @@ void *scratch_address(int dev) {
 }
 
 }  // namespace
+
+namespace mpg_host {
+
+bool handle_live(mpgemm_handle_t h) {
+    std::lock_guard<std::mutex> lock(g_handles_mu);
+    return g_handles.count(h) != 0;
+}
+
+mpgemm_status_t handle_on_device(mpgemm_handle_t handle) {
+    int dev = -1;
+    if (hipGetDevice(&dev) != hipSuccess) return MPGEMM_STATUS_INTERNAL_ERROR;
+    return dev == handle->device ? MPGEMM_STATUS_SUCCESS : MPGEMM_STATUS_WRONG_DEVICE;
+}
+
+}  // namespace mpg_host
 
 namespace mpg {
 hipError_t launch_fp8(int in, int out, bool ta, bool tb, int tile, const Params &p, hipStream_t s) {

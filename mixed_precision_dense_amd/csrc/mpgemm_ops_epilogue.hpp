@@ -1,0 +1,419 @@
+// mpgemm_ops_epilogue.hpp -- what the op kernels do with a product's FP32 values: activations
+// and their slopes, and the epilogue of eight consecutive columns of one row.
+//
+// Everything is computed in FP32; a result is rounded once, to nearest even, where it is stored.
+#pragma once
+
+#include "mpgemm_kernel.hpp"
+#include "mpgemm_ops.hpp"
+
+namespace mpg {
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+__device__ __forceinline__ float fast_exp2(float x) { return __builtin_amdgcn_exp2f(x); }
+__device__ __forceinline__ float fast_rcp(float x) { return __builtin_amdgcn_rcpf(x); }
+
+// 1 / (1 + exp(-x)) from the hardware's exp2 and reciprocal (1 ulp each): exp(-x) overflows to
+// infinity for very negative x, whose reciprocal is the 0 that the sigmoid rounds to.
+__device__ __forceinline__ float sigmoid(float x) { return fast_rcp(1.0f + fast_exp2(-kLog2e * x)); }
+
+// Slopes are those of a point within +-30, where every activation's slope has reached 0 or 1 in
+// FP32: an infinite (or huge) value kept from the forward pass gives that limit, and no 0 * inf.
+// NaN stays NaN.
+__device__ __forceinline__ float near_zero(float z) { return z > 30.0f ? 30.0f : (z < -30.0f ? -30.0f : z); }
+
+// The normal distribution's Phi(z) and exp(-z^2 / 2).  With x = |z| / sqrt(2) and
+// t = 1 / (1 + 0.43 x), erfc(x) = exp(-x^2) t q(t), q a polynomial of degree 7 fitted to erfcx(x)
+// in relative minimax over x in [0, 12] (2e-7, 5e-7 as evaluated in FP32): the lower tail keeps its
+// relative accuracy, as 1 + erf would not.
+__device__ __forceinline__ float normal_cdf(float z, float &bell) {
+    const float a = __builtin_fabsf(z);
+    const float t = fast_rcp(__builtin_fmaf(a, 0.43f * 0.70710678118654752f, 1.0f));
+    bell = fast_exp2(z * z * (-0.5f * kLog2e));
+    float q = 0.07090955117377087f;
+    q = __builtin_fmaf(q, t, -0.2990298556651683f);
+    q = __builtin_fmaf(q, t, 0.36473237500049616f);
+    q = __builtin_fmaf(q, t, -0.06881683436104556f);
+    q = __builtin_fmaf(q, t, 0.2382076128012132f);
+    q = __builtin_fmaf(q, t, 0.20746980043114047f);
+    q = __builtin_fmaf(q, t, 0.24398845434153432f);
+    q = __builtin_fmaf(q, t, 0.2425387182165695f);
+    const float tail = 0.5f * bell * (q * t);   // Phi(-|z|)
+    return z > 0.0f ? 1.0f - tail : tail;
+}
+
+constexpr float kGeluC = 0.79788456080286536f;   // sqrt(2 / pi)
+constexpr float kGeluA = 0.044715f;
+
+template <int ACT>
+__device__ __forceinline__ float act_value(float z) {
+    if constexpr (ACT == ACT_RELU) return z <= 0.0f ? 0.0f : z;   // NaN stays NaN
+    if constexpr (ACT == ACT_GELU) {
+        float bell;
+        return z * normal_cdf(z, bell);
+    }
+    // 0.5 z (1 + tanh u) = z / (1 + exp(-2u))
+    if constexpr (ACT == ACT_GELU_TANH)
+        return z * sigmoid(2.0f * kGeluC * z * __builtin_fmaf(kGeluA * z, z, 1.0f));
+    if constexpr (ACT == ACT_SILU) return z * sigmoid(z);
+    return z;
+}
+
+template <int ACT>
+__device__ __forceinline__ float act_slope(float z) {
+    if constexpr (ACT == ACT_RELU) return z > 0.0f ? 1.0f : 0.0f;
+    if constexpr (ACT == ACT_NONE) return 1.0f;
+    z = near_zero(z);
+    if constexpr (ACT == ACT_GELU) {
+        float bell;
+        const float phi = normal_cdf(z, bell);
+        return __builtin_fmaf(z * 0.39894228040143268f, bell, phi);
+    }
+    if constexpr (ACT == ACT_GELU_TANH) {
+        const float z2 = z * z;
+        const float g = sigmoid(2.0f * kGeluC * z * __builtin_fmaf(kGeluA, z2, 1.0f));
+        // d(2u)/dz = 2 c (1 + 3 a z^2)
+        return __builtin_fmaf(z * g * (1.0f - g), 2.0f * kGeluC * __builtin_fmaf(3.0f * kGeluA, z2, 1.0f), g);
+    }
+    const float g = sigmoid(z);   // ACT_SILU
+    return g * __builtin_fmaf(z, 1.0f - g, 1.0f);
+}
+
+// Calls f(std::integral_constant<int, ACT>) for the activation named at run time (uniform).
+template <typename F>
+__device__ __forceinline__ void with_act(int act, F &&f) {
+    switch (act) {
+    case ACT_RELU: f(std::integral_constant<int, ACT_RELU>{}); break;
+    case ACT_GELU: f(std::integral_constant<int, ACT_GELU>{}); break;
+    case ACT_GELU_TANH: f(std::integral_constant<int, ACT_GELU_TANH>{}); break;
+    case ACT_SILU: f(std::integral_constant<int, ACT_SILU>{}); break;
+    default: f(std::integral_constant<int, ACT_NONE>{}); break;
+    }
+}
+
+// ------------------------------------------------------------------------------- eight columns
+template <int IN>
+__device__ __forceinline__ float widen(uint32_t bits16) {
+    if constexpr (IN == IN_F16)
+        return (float)__builtin_bit_cast(_Float16, (unsigned short)bits16);
+    else
+        return __builtin_bit_cast(float, bits16 << 16);
+}
+template <int IN>
+__device__ __forceinline__ unsigned short narrow(float v) {
+    if constexpr (IN == IN_F16) {
+        asm("" : "+v"(v));   // the FP32 value first, then one rounding (no fused fma and conversion)
+        return __builtin_bit_cast(unsigned short, (_Float16)v);
+    } else {
+        return __builtin_bit_cast(unsigned short, (__bf16)v);
+    }
+}
+template <int IN>
+__device__ __forceinline__ void widen8(u32x4 x, float (&v)[8]) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        v[2 * q] = widen<IN>(x[q] & 0xFFFFu);
+        v[2 * q + 1] = widen<IN>(x[q] >> 16);
+    }
+}
+template <int IN>
+__device__ __forceinline__ u32x4 narrow8(const float (&v)[8]) {
+    u32x4 x;
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+        x[q] = (uint32_t)narrow<IN>(v[2 * q]) | ((uint32_t)narrow<IN>(v[2 * q + 1]) << 16);
+    return x;
+}
+
+// Where a workgroup's tile lies.
+struct OpTile {
+    int tm, tn;          // tile of its product
+    int tile;            // GROUPS_ROWS: number of the row tile over all experts, else tm
+    int expert, split;
+    int row0;            // first row of A and D of its product
+    int m, k;            // rows and summed length of its product
+    int64_t d_off;       // element offset of its D
+};
+
+// What an epilogue reads besides the product: eight columns of C and aux, as stored.
+struct ChunkIn {
+    u32x4 c0, c1, z;
+};
+
+// The eight columns col .. col + 7 of row `row` of D (ncol >= 1 of them exist).  C and aux are read
+// in whole 16-byte blocks that hold a column that exists.
+__device__ __forceinline__ void chunk_load(const OpParams &p, const OpTile &w, int64_t row, int col, int ncol,
+                                           ChunkIn &in) {
+    if (p.C != nullptr) {
+        const int64_t at = w.d_off + row * p.ldc + col;
+        if (p.c_f32) {
+            const float *c = (const float *)p.C + at;
+            in.c0 = *(const u32x4 *)c;
+            if (ncol > 4) in.c1 = *(const u32x4 *)(c + 4);
+        } else {
+            in.c0 = *(const u32x4 *)((const uint16_t *)p.C + at);
+        }
+    }
+    if (p.mode == OP_SLOPE && p.aux != nullptr) in.z = *(const u32x4 *)((const uint16_t *)p.aux + row * p.ld_aux + col);
+}
+
+template <int IN>
+__device__ __forceinline__ void store8(void *base, int f32, int64_t at, int ncol, const float (&v)[8]) {
+    if (f32) {
+        float *d = (float *)base + at;
+        if (ncol >= 8) {
+            *(f32x4 *)d = f32x4{v[0], v[1], v[2], v[3]};
+            *(f32x4 *)(d + 4) = f32x4{v[4], v[5], v[6], v[7]};
+        } else {
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+                if (q < ncol) d[q] = v[q];
+        }
+    } else {
+        uint16_t *d = (uint16_t *)base + at;
+        const u32x4 x = narrow8<IN>(v);
+        if (ncol >= 8) {
+            *(u32x4 *)d = x;
+        } else {
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+                if (q < ncol) d[q] = (uint16_t)(q & 1 ? x[q / 2] >> 16 : x[q / 2]);
+        }
+    }
+}
+
+// The bias of columns col .. col + 7 (zeros where there is none).
+template <int IN>
+__device__ __forceinline__ void bias_load(const OpParams &p, int expert, int col, float (&b)[8]) {
+#pragma unroll
+    for (int q = 0; q < 8; ++q) b[q] = 0.0f;
+    if (p.bias == nullptr || p.mode != OP_FORWARD) return;
+    const int64_t at = (int64_t)expert * p.bias_stride + col;
+#pragma unroll
+    for (int q = 0; q < 8; ++q)
+        if (col + q < p.n)
+            b[q] = p.bias_f32 ? ((const float *)p.bias)[at + q] : widen<IN>(((const uint16_t *)p.bias)[at + q]);
+}
+
+// alpha, times the device factor where there is one.
+__device__ __forceinline__ float op_alpha(const OpParams &p) {
+    return p.scale != nullptr ? p.alpha * p.scale[0] : p.alpha;
+}
+
+// Turns the products v of eight columns into what is stored, and stores it; sums adds up what
+// OP_SLOPE stores (before its rounding).  `drow` is the row of D, C and aux.
+template <int IN>
+__device__ __forceinline__ void chunk_finish(const OpParams &p, float alpha, const OpTile &w, int64_t drow, int col,
+                                             int ncol, const ChunkIn &in, const float (&bias)[8], float (&v)[8],
+                                             float (&sums)[8]) {
+    const int64_t at = w.d_off + drow * p.ldd + col;
+    if (p.mode == OP_SLOPE) {
+        float z[8];
+        widen8<IN>(in.z, z);
+        with_act(p.act, [&](auto a) {
+#pragma unroll
+            for (int q = 0; q < 8; ++q) v[q] = alpha * v[q] * act_slope<decltype(a)::value>(z[q]);
+        });
+#pragma unroll
+        for (int q = 0; q < 8; ++q) sums[q] += v[q];
+    } else if (p.mode == OP_CE_PROBS) {
+        // A row that does not count has weight 0: nothing of its product may reach D.
+        const float wt = p.weight[drow], lse = p.lse[drow];
+        const int64_t t = p.target[drow] - p.col0 - col;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+            const float e = fast_exp2(kLog2e * __builtin_fmaf(alpha, v[q], -lse));
+            v[q] = wt == 0.0f ? 0.0f : (e - (t == q ? 1.0f : 0.0f)) * wt;
+        }
+    } else {
+#pragma unroll
+        for (int q = 0; q < 8; ++q) v[q] = __builtin_fmaf(alpha, v[q], bias[q]);
+        if (p.aux != nullptr) store8<IN>(p.aux, 0, drow * p.ld_aux + col, ncol, v);
+        with_act(p.act, [&](auto a) {
+#pragma unroll
+            for (int q = 0; q < 8; ++q) v[q] = act_value<decltype(a)::value>(v[q]);
+        });
+        if (p.C != nullptr) {
+            float c[8];
+            if (p.c_f32) {
+                const f32x4 lo = __builtin_bit_cast(f32x4, in.c0), hi = __builtin_bit_cast(f32x4, in.c1);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    c[q] = lo[q];
+                    c[q + 4] = hi[q];
+                }
+            } else {
+                widen8<IN>(in.c0, c);
+            }
+#pragma unroll
+            for (int q = 0; q < 8; ++q) v[q] = __builtin_fmaf(p.beta, c[q], v[q]);
+        }
+    }
+    store8<IN>(p.D, p.d_f32, at, ncol, v);
+}
+
+// ------------------------------------------------------------------------------- experts' rows
+// Rows [lo, hi) of expert e.  Offsets outside 0 .. rows or decreasing ones are clamped, so that no
+// value on the device makes a kernel touch memory outside the operands.
+__device__ __forceinline__ void expert_rows(const int *offsets, int e, int rows, int &lo, int &hi) {
+    lo = min(max(offsets[e], 0), rows);
+    hi = max(lo, min(max(offsets[e + 1], 0), rows));
+}
+
+// A value that every lane of a wave holds alike, in scalar registers.
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+__device__ __forceinline__ int64_t uniform64(int64_t v) {
+    const uint32_t lo = (uint32_t)uniform((int)(uint32_t)v), hi = (uint32_t)uniform((int)(uint32_t)((uint64_t)v >> 32));
+    return (int64_t)(((uint64_t)hi << 32) | lo);
+}
+
+// Inclusive prefix sum over a wave's 64 lanes.
+__device__ __forceinline__ int64_t wave_scan(int64_t v, int lane) {
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+        const int64_t o = __shfl_up(v, d, 64);
+        if (lane >= d) v += o;
+    }
+    return v;
+}
+
+// Row tiles of `tile_rows` rows before expert e and of expert e itself, by one whole wave.
+__device__ __forceinline__ void expert_tiles(const OpParams &p, int tile_rows, int expert, int lane, int64_t &before,
+                                             int &own, int &lo, int &hi) {
+    before = 0;
+    for (int base = 0; base <= expert; base += 64) {
+        int l = 0, h = 0;
+        if (base + lane < p.groups) expert_rows(p.offsets, base + lane, p.m, l, h);
+        const int t = (h - l + tile_rows - 1) / tile_rows;
+        const int64_t incl = wave_scan(t, lane);
+        if (expert < base + 64) {
+            const int src = expert - base;
+            before += __shfl(incl - t, src, 64);
+            own = __shfl(t, src, 64);
+            lo = __shfl(l, src, 64);
+            hi = __shfl(h, src, 64);
+        } else {
+            before += __shfl(incl, 63, 64);
+        }
+    }
+}
+
+// The tile of workgroup `wg`; false: none is left for it.  Every wave of a workgroup finds it for
+// itself.  The experts' tiles follow each other, an expert's own by columns of tiles (which share
+// its weights); each XCD gets a contiguous run of them.
+template <int BM>
+__device__ __forceinline__ bool locate(const OpParams &p, int wg, int split, int lane, OpTile &w) {
+    w.split = split;
+    w.expert = 0;
+    w.row0 = 0;
+    w.m = p.m;
+    w.k = p.k;
+    w.d_off = 0;
+    if (p.groups_kind == GROUPS_ROWS) {
+        int64_t total = 0;
+        for (int base = 0; base < p.groups; base += 64) {
+            int lo = 0, hi = 0;
+            if (base + lane < p.groups) expert_rows(p.offsets, base + lane, p.m, lo, hi);
+            total += __shfl(wave_scan((hi - lo + BM - 1) / BM, lane), 63, 64);
+        }
+        total = uniform64(total) * p.tiles_n;
+        if (wg >= total) return false;
+        const int64_t run = min(total, (int64_t)p.tiles_m * p.tiles_n) / 8;
+        const int64_t id = wg < run * 8 ? (wg % 8) * run + wg / 8 : wg;
+        int64_t before = 0;
+        for (int base = 0; base < p.groups; base += 64) {
+            int lo = 0, hi = 0;
+            if (base + lane < p.groups) expert_rows(p.offsets, base + lane, p.m, lo, hi);
+            const int t = (hi - lo + BM - 1) / BM;
+            const int64_t incl = before + wave_scan(t, lane);
+            const uint64_t hit = (uint64_t)uniform64((int64_t)__ballot(t > 0 && id < incl * p.tiles_n && id >= (incl - t) * p.tiles_n));
+            if (hit != 0) {
+                const int src = __builtin_ctzll(hit);
+                const int own = uniform(__shfl(t, src, 64));
+                const int first = uniform((int)__shfl(incl - t, src, 64));
+                w.expert = base + src;
+                w.row0 = uniform(__shfl(lo, src, 64));
+                w.m = uniform(__shfl(hi, src, 64)) - w.row0;
+                const int local = uniform((int)(id - (int64_t)first * p.tiles_n));
+                w.tm = local % own;
+                w.tn = local / own;
+                w.tile = first + w.tm;
+                return true;
+            }
+            before = uniform64(__shfl(incl, 63, 64));
+        }
+        return false;
+    }
+    if (p.groups_kind == GROUPS_K) {
+        const int per = p.tiles_m * p.tiles_n;
+        const int total = per * p.groups, run = total / 8;
+        const int id = wg < run * 8 ? (wg % 8) * run + wg / 8 : wg;
+        w.expert = id / per;
+        const int local = id - w.expert * per;
+        w.tm = local % p.tiles_m;
+        w.tn = local / p.tiles_m;
+        w.tile = w.tm;
+        int lo, hi;
+        expert_rows(p.offsets, w.expert, p.k, lo, hi);
+        w.row0 = 0;
+        w.k = uniform(hi) - uniform(lo);
+        w.d_off = (int64_t)w.expert * p.stride_d;
+        return true;
+    }
+    tile_coords(wg, p.tiles_m, p.tiles_n, w.tm, w.tn);
+    w.tile = w.tm;
+    if (p.splits > 1) {
+        w.k = min(p.k_split, p.k - split * p.k_split);
+        w.d_off = (int64_t)split * p.stride_split;
+    }
+    return true;
+}
+
+// The operands of a tile's product.
+template <bool TA, bool TB>
+__device__ __forceinline__ Params op_operands(const OpParams &p, const OpTile &w) {
+    Params q = {};
+    int64_t ka = 0, kb = 0;   // first summed index in A and in B
+    if (p.groups_kind == GROUPS_K) {
+        int lo, hi;
+        expert_rows(p.offsets, w.expert, p.k, lo, hi);
+        ka = kb = uniform(lo);
+    } else if (p.splits > 1) {
+        ka = kb = (int64_t)w.split * p.k_split;
+    }
+    const int64_t a = (int64_t)w.row0 * (TA ? 1 : p.lda) + ka * (TA ? p.lda : 1);
+    const int64_t b = kb * (TB ? 1 : p.ldb) + (p.groups_kind == GROUPS_ROWS ? (int64_t)w.expert * p.stride_b : 0);
+    q.A = (const char *)p.A + 2 * a;
+    q.B = (const char *)p.B + 2 * b;
+    q.lda = p.lda;
+    q.ldb = p.ldb;
+    q.m = w.m;
+    q.n = p.n;
+    q.k = w.k;
+    return q;
+}
+
+// ------------------------------------------------------------------------------- row statistics
+// Reductions over the 16 lanes of a DPP row (every lane gets the result).
+template <int R>
+__device__ __forceinline__ float row_rotate(float v) {
+    return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), 0x120 + R, 0xF, 0xF, false));
+}
+__device__ __forceinline__ float row_max16(float v) {
+    v = fmaxf(v, row_rotate<8>(v));
+    v = fmaxf(v, row_rotate<4>(v));
+    v = fmaxf(v, row_rotate<2>(v));
+    return fmaxf(v, row_rotate<1>(v));
+}
+__device__ __forceinline__ float row_sum16(float v) {
+    v += row_rotate<8>(v);
+    v += row_rotate<4>(v);
+    v += row_rotate<2>(v);
+    return v + row_rotate<1>(v);
+}
+// What exponentials are taken from: the maximum, or 0 where there is no finite one below +inf
+// (a range without columns, or of -inf alone, then sums to 0 and not to NaN).
+__device__ __forceinline__ float stat_base(float top) { return top == -__builtin_inff() ? 0.0f : top; }
+
+}  // namespace mpg

@@ -1,0 +1,315 @@
+// mpgemm_ops_host.cpp -- host-only part of the epilogue, grouped and linear cross entropy
+// products declared in include/mpgemm.h: argument checks, the rules that choose a kernel and the
+// workspaces' layouts.  No device call and no HIP header.
+#include "mpgemm_ops_host.hpp"
+
+#include "mpgemm_host.hpp"
+#include "mpgemm_kinds.hpp"
+
+namespace mpg_host {
+namespace {
+
+constexpr int kCus = 256;   // a whole MI355X: workspace sizes depend on the rules, not on a handle
+
+bool aligned(const void *p, unsigned to) { return ((uintptr_t)p & (to - 1)) == 0; }
+int64_t at_least1(int64_t v) { return v > 1 ? v : 1; }
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+// Largest leading dimension of elements of eb bytes (256 rows span less than 2^31 bytes).
+int64_t max_ld(int eb) { return (((int64_t)1 << 31) - 4096) / (256 * (int64_t)eb); }
+bool op_valid(mpgemm_op_t t) { return t == MPGEMM_OP_N || t == MPGEMM_OP_T; }
+bool half_type(mpgemm_dtype_t t) { return t == MPGEMM_R_16F || t == MPGEMM_R_16BF; }
+// Types of outputs and of what epilogues read: the inputs' type or FP32.
+bool out_type(int t, mpgemm_dtype_t in) { return t == in || t == MPGEMM_R_32F; }
+bool act_valid(int a) { return a >= MPGEMM_ACT_NONE && a <= MPGEMM_ACT_SILU; }
+// A stride that the kernels' addressing covers, in whole 16-byte blocks.
+bool stride_ok(int64_t ld, int eb) { return ld <= max_ld(eb) && (ld * eb) % 16 == 0; }
+
+OpPlan tiled(int64_t m, int64_t n, int edge) {
+    return OpPlan{false, 0, 0, edge, edge, ceil_div(m, edge), ceil_div(n, edge)};
+}
+OpPlan skinny(int64_t tiles_m, int64_t n, int fm, int w) {
+    return OpPlan{true, fm, w, 16 * fm, 16 * w, tiles_m, ceil_div(n, 16 * w)};
+}
+
+// Launches have a 32-bit number of lanes: at most this many workgroups of 256 or 512.
+bool launchable(const OpPlan &p, int64_t times) {
+    const int64_t most = (int64_t)UINT32_MAX / (p.skinny ? 512 : 256);
+    return p.tiles_m <= most && p.tiles_n <= most && times <= most && p.tiles_m * p.tiles_n <= most &&
+           p.tiles_m * p.tiles_n * times <= most;
+}
+
+}  // namespace
+
+OpPlan op_plan(int64_t m, int64_t n, bool tb) {
+    if (m <= 64 && n <= ((int64_t)1 << 22)) {
+        const int fm = m <= 16 ? 1 : (m <= 32 ? 2 : 4);
+        return skinny(1, n, fm, fm == 1 && tb ? 1 : 2);
+    }
+    return tiled(m, n, pick_tile(m, n, false, kCus));
+}
+
+OpPlan grouped_plan(int64_t rows, int64_t groups, int64_t n, bool tb) {
+    const int64_t mean = ceil_div(rows, groups > 0 ? groups : 1);
+    OpPlan p;
+    if (mean <= 32 && n <= ((int64_t)1 << 22)) {
+        const int fm = mean <= 8 ? 1 : (mean <= 20 ? 2 : 4);
+        p = skinny(0, n, fm, fm == 1 && tb ? 1 : 2);
+    } else {
+        p = tiled(rows, n, mean <= 64 ? 64 : (mean <= 192 ? 128 : 256));
+    }
+    p.tiles_m = rows / p.rows + (groups < rows ? groups : rows);   // an expert's last tile may be short
+    return p;
+}
+
+OpPlan wgrad_plan(int64_t groups, int64_t m, int64_t n) {
+    int edge = 64;
+    for (int e = 128; e <= 256; e *= 2)
+        if (groups * ceil_div(m, e) * ceil_div(n, e) >= kCus) edge = e;
+    return tiled(m, n, edge);
+}
+
+int64_t colsum_rows(int64_t groups, int64_t m) {
+    // two partial rows per row tile of at least 64 rows, or one per tile of at least 16
+    return m / 16 + 2 * (groups > 0 ? groups : 1);
+}
+
+bool ce_layout(int64_t m, int64_t n, int64_t k, bool train, CeLayout &L) {
+    if (m < 0 || n < 1 || k < 0 || m > kOpMaxSize || n > kOpMaxSize || k > kOpMaxSize) return false;
+    auto up = [](uint64_t v) { return (v + 255) / 256 * 256; };
+    L.logits = op_plan(m, n, true);
+    L.parts = (int)(L.logits.tiles_n * (L.logits.skinny ? 1 : 2));
+    const uint64_t stats = up((uint64_t)m * (uint64_t)L.parts * 8);
+    L.piece = n;
+    L.pieces = 1;
+    L.splits = 1;
+    L.k_split = n;
+    L.off_weight = L.off_scale = L.off_probs = L.off_dx = 0;
+    L.total = stats;
+    if (!train || m == 0) return true;
+    // Probabilities of one piece at a time, at most 128 MiB of them (or 256 columns): half of the
+    // memory-side cache, and enough columns for products of full speed.
+    int64_t most = ((int64_t)128 << 20) / (2 * m) / 256 * 256;
+    most = most < 256 ? 256 : (most > ((int64_t)1 << 20) ? (int64_t)1 << 20 : most);
+    L.pieces = ceil_div(n, most);
+    L.piece = ceil_div(ceil_div(n, L.pieces), 256) * 256;
+    L.pieces = ceil_div(n, L.piece);
+    L.logits = op_plan(m, L.piece, true);
+    L.dx = op_plan(m, k, false);
+    L.dw = op_plan(L.piece, k, false);
+    // dX sums over a whole piece: where its tiles do not fill the CUs the piece is cut into ranges
+    const int64_t tiles = at_least1(L.dx.tiles_m * L.dx.tiles_n);
+    const int64_t have = n < L.piece ? n : L.piece;
+    int64_t splits = kCus / tiles;
+    if (splits > ceil_div(have, 512)) splits = ceil_div(have, 512);
+    if (splits > 32) splits = 32;
+    if (splits < 1) splits = 1;
+    L.k_split = ceil_div(ceil_div(have, splits), 64) * 64;
+    L.splits = (int)ceil_div(have, L.k_split);
+    L.off_weight = 0;
+    L.off_scale = up((uint64_t)m * 4);
+    L.off_probs = L.off_scale + 256;
+    L.off_dx = L.off_probs + up((uint64_t)m * (uint64_t)L.piece * 2);
+    const unsigned __int128 total = (unsigned __int128)L.off_dx + (unsigned __int128)L.splits * (uint64_t)m * (uint64_t)round8(k) * 4;
+    if (total > ((unsigned __int128)1 << 62)) return false;
+    L.total = (uint64_t)total > stats ? (uint64_t)total : stats;
+    return true;
+}
+
+}  // namespace mpg_host
+
+using namespace mpg_host;
+
+namespace {
+
+// What every product checks of its operands: types, leading dimensions, and (once there is
+// something to compute) pointers, alignment and strides.
+mpgemm_status_t check_types(mpgemm_dtype_t a, mpgemm_dtype_t b, mpgemm_dtype_t d) {
+    return a == b && half_type(a) && out_type(d, a) ? MPGEMM_STATUS_SUCCESS : MPGEMM_STATUS_NOT_SUPPORTED;
+}
+
+mpgemm_status_t check_epilogue_arg(const mpgemm_epilogue_t *e, mpgemm_dtype_t in, int64_t n, bool grouped) {
+    if (!e || !act_valid(e->act)) return MPGEMM_STATUS_INVALID_VALUE;
+    if (e->bias && !out_type(e->bias_type, in)) return MPGEMM_STATUS_NOT_SUPPORTED;
+    if (e->bias && grouped && e->bias_stride < 0) return MPGEMM_STATUS_INVALID_VALUE;
+    if (e->aux && e->ld_aux < at_least1(n)) return MPGEMM_STATUS_INVALID_VALUE;
+    return MPGEMM_STATUS_SUCCESS;
+}
+
+mpgemm_status_t check_epilogue_layout(const mpgemm_epilogue_t *e) {
+    if (e->bias && !aligned(e->bias, e->bias_type == MPGEMM_R_32F ? 4 : 2)) return MPGEMM_STATUS_NOT_SUPPORTED;
+    if (e->aux && (!aligned(e->aux, 16) || !stride_ok(e->ld_aux, 2))) return MPGEMM_STATUS_NOT_SUPPORTED;
+    return MPGEMM_STATUS_SUCCESS;
+}
+
+mpgemm_status_t check_workspace(const void *ws, uint64_t bytes, uint64_t need) {
+    if (need == 0) return MPGEMM_STATUS_SUCCESS;
+    if (!ws || bytes < need) return MPGEMM_STATUS_INVALID_VALUE;
+    return aligned(ws, 256) ? MPGEMM_STATUS_SUCCESS : MPGEMM_STATUS_NOT_SUPPORTED;
+}
+
+}  // namespace
+
+#define MPGEMM_TRY(call)                                          \
+    do {                                                          \
+        const mpgemm_status_t st_ = (call);                       \
+        if (st_ != MPGEMM_STATUS_SUCCESS) return st_;             \
+    } while (0)
+
+extern "C" {
+
+mpgemm_status_t mpgemm_check_epilogue(mpgemm_op_t transa, mpgemm_op_t transb, int64_t m, int64_t n, int64_t k,
+                                      const float *alpha, const void *A, mpgemm_dtype_t a_type, int64_t lda,
+                                      const void *B, mpgemm_dtype_t b_type, int64_t ldb,
+                                      const mpgemm_epilogue_t *epilogue, const float *beta, const void *C,
+                                      mpgemm_dtype_t c_type, int64_t ldc, const void *D, mpgemm_dtype_t d_type,
+                                      int64_t ldd) {
+    if (!op_valid(transa) || !op_valid(transb) || m < 0 || n < 0 || k < 0 || !alpha || !beta) return MPGEMM_STATUS_INVALID_VALUE;
+    MPGEMM_TRY(check_types(a_type, b_type, d_type));
+    const bool read_c = !beta_is_zero(beta, MPGEMM_R_32F);
+    if (read_c && !out_type(c_type, a_type)) return MPGEMM_STATUS_NOT_SUPPORTED;
+    MPGEMM_TRY(check_epilogue_arg(epilogue, a_type, n, false));
+    const bool ta = transa == MPGEMM_OP_T, tb = transb == MPGEMM_OP_T;
+    if (lda < at_least1(ta ? m : k) || ldb < at_least1(tb ? k : n) || ldd < at_least1(n) || (read_c && ldc < at_least1(n)))
+        return MPGEMM_STATUS_INVALID_VALUE;
+    if (m == 0 || n == 0) return MPGEMM_STATUS_SUCCESS;
+    if (!D || (k > 0 && (!A || !B)) || (read_c && !C)) return MPGEMM_STATUS_INVALID_VALUE;
+    if (m > kOpMaxSize || n > kOpMaxSize || k > kOpMaxSize || !launchable(op_plan(m, n, tb), 1)) return MPGEMM_STATUS_NOT_SUPPORTED;
+    if ((k > 0 && (!aligned(A, 16) || !aligned(B, 16))) || !aligned(D, 16) || (read_c && !aligned(C, 16)))
+        return MPGEMM_STATUS_NOT_SUPPORTED;
+    if (!stride_ok(lda, 2) || !stride_ok(ldb, 2) || !stride_ok(ldd, elem_bytes(d_type)) ||
+        (read_c && !stride_ok(ldc, elem_bytes(c_type))))
+        return MPGEMM_STATUS_NOT_SUPPORTED;
+    return check_epilogue_layout(epilogue);
+}
+
+uint64_t mpgemm_epilogue_grad_workspace_size(int64_t groups, int64_t m, int64_t n) {
+    if (groups < 1 || m < 1 || n < 1 || m > kOpMaxSize || n > kOpMaxSize || groups > 65535) return 0;
+    return (uint64_t)colsum_rows(groups, m) * (uint64_t)round8(n) * 4;
+}
+
+mpgemm_status_t mpgemm_check_epilogue_grad(mpgemm_op_t transa, mpgemm_op_t transb, int64_t m, int64_t n, int64_t k,
+                                           const float *alpha, const void *A, mpgemm_dtype_t a_type, int64_t lda,
+                                           const void *B, mpgemm_dtype_t b_type, int64_t ldb, mpgemm_act_t act,
+                                           const void *Z, int64_t ldz, const void *D, mpgemm_dtype_t d_type, int64_t ldd,
+                                           const float *dbias, const void *workspace, uint64_t workspace_bytes) {
+    if (!op_valid(transa) || !op_valid(transb) || m < 0 || n < 0 || k < 0 || !alpha || !act_valid(act)) return MPGEMM_STATUS_INVALID_VALUE;
+    MPGEMM_TRY(check_types(a_type, b_type, d_type));
+    const bool ta = transa == MPGEMM_OP_T, tb = transb == MPGEMM_OP_T, read_z = act != MPGEMM_ACT_NONE;
+    if (lda < at_least1(ta ? m : k) || ldb < at_least1(tb ? k : n) || ldd < at_least1(n) || (read_z && ldz < at_least1(n)))
+        return MPGEMM_STATUS_INVALID_VALUE;
+    if (n == 0 || (m == 0 && !dbias)) return MPGEMM_STATUS_SUCCESS;
+    if (m > kOpMaxSize || n > kOpMaxSize || k > kOpMaxSize || !launchable(op_plan(m, n, tb), 1)) return MPGEMM_STATUS_NOT_SUPPORTED;
+    if (!aligned(dbias, 4)) return MPGEMM_STATUS_NOT_SUPPORTED;
+    if (m == 0) return MPGEMM_STATUS_SUCCESS;   // (the sum of no rows is written)
+    if (!D || (k > 0 && (!A || !B)) || (read_z && !Z)) return MPGEMM_STATUS_INVALID_VALUE;
+    if ((k > 0 && (!aligned(A, 16) || !aligned(B, 16))) || !aligned(D, 16) || (read_z && !aligned(Z, 16)))
+        return MPGEMM_STATUS_NOT_SUPPORTED;
+    if (!stride_ok(lda, 2) || !stride_ok(ldb, 2) || !stride_ok(ldd, elem_bytes(d_type)) || (read_z && !stride_ok(ldz, 2)))
+        return MPGEMM_STATUS_NOT_SUPPORTED;
+    return dbias ? check_workspace(workspace, workspace_bytes, mpgemm_epilogue_grad_workspace_size(1, m, n)) : MPGEMM_STATUS_SUCCESS;
+}
+
+mpgemm_status_t mpgemm_check_grouped(mpgemm_op_t transb, int64_t groups, int64_t rows, int64_t n, int64_t k, const float *alpha,
+                                     const void *A, mpgemm_dtype_t a_type, int64_t lda, const int32_t *offsets, const void *B,
+                                     mpgemm_dtype_t b_type, int64_t ldb, int64_t stride_b, const mpgemm_epilogue_t *epilogue,
+                                     const void *D, mpgemm_dtype_t d_type, int64_t ldd) {
+    if (!op_valid(transb) || groups < 0 || rows < 0 || n < 0 || k < 0 || !alpha || stride_b < 0) return MPGEMM_STATUS_INVALID_VALUE;
+    MPGEMM_TRY(check_types(a_type, b_type, d_type));
+    MPGEMM_TRY(check_epilogue_arg(epilogue, a_type, n, true));
+    const bool tb = transb == MPGEMM_OP_T;
+    if (lda < at_least1(k) || ldb < at_least1(tb ? k : n) || ldd < at_least1(n)) return MPGEMM_STATUS_INVALID_VALUE;
+    if (groups == 0 || rows == 0 || n == 0) return MPGEMM_STATUS_SUCCESS;
+    if (!D || !offsets || (k > 0 && (!A || !B))) return MPGEMM_STATUS_INVALID_VALUE;
+    if (rows > kOpMaxSize || n > kOpMaxSize || k > kOpMaxSize || groups > 65535 || !launchable(grouped_plan(rows, groups, n, tb), 1))
+        return MPGEMM_STATUS_NOT_SUPPORTED;
+    if ((k > 0 && (!aligned(A, 16) || !aligned(B, 16))) || !aligned(D, 16) || !aligned(offsets, 4)) return MPGEMM_STATUS_NOT_SUPPORTED;
+    if (!stride_ok(lda, 2) || !stride_ok(ldb, 2) || !stride_ok(ldd, elem_bytes(d_type)) || stride_b % 8 || stride_b > INT64_MAX / 131072)
+        return MPGEMM_STATUS_NOT_SUPPORTED;
+    return check_epilogue_layout(epilogue);
+}
+
+mpgemm_status_t mpgemm_check_grouped_grad(mpgemm_op_t transb, int64_t groups, int64_t rows, int64_t n, int64_t k,
+                                          const float *alpha, const void *A, mpgemm_dtype_t a_type, int64_t lda,
+                                          const int32_t *offsets, const void *B, mpgemm_dtype_t b_type, int64_t ldb,
+                                          int64_t stride_b, mpgemm_act_t act, const void *Z, int64_t ldz, const void *D,
+                                          mpgemm_dtype_t d_type, int64_t ldd, const float *dbias, const void *workspace,
+                                          uint64_t workspace_bytes) {
+    if (!act_valid(act)) return MPGEMM_STATUS_INVALID_VALUE;
+    const mpgemm_epilogue_t none = {MPGEMM_ACT_NONE, nullptr, MPGEMM_R_32F, 0, nullptr, 0};
+    MPGEMM_TRY(mpgemm_check_grouped(transb, groups, rows, n, k, alpha, A, a_type, lda, offsets, B, b_type, ldb, stride_b, &none, D,
+                                    d_type, ldd));
+    const bool read_z = act != MPGEMM_ACT_NONE;
+    if (read_z && ldz < at_least1(n)) return MPGEMM_STATUS_INVALID_VALUE;
+    if (groups == 0 || n == 0 || (rows == 0 && !dbias)) return MPGEMM_STATUS_SUCCESS;
+    if (groups > 65535 || n > kOpMaxSize || !aligned(dbias, 4)) return MPGEMM_STATUS_NOT_SUPPORTED;
+    if (rows == 0) return offsets ? MPGEMM_STATUS_SUCCESS : MPGEMM_STATUS_INVALID_VALUE;
+    if (read_z && !Z) return MPGEMM_STATUS_INVALID_VALUE;
+    if (read_z && (!aligned(Z, 16) || !stride_ok(ldz, 2))) return MPGEMM_STATUS_NOT_SUPPORTED;
+    return dbias ? check_workspace(workspace, workspace_bytes, mpgemm_epilogue_grad_workspace_size(groups, rows, n)) : MPGEMM_STATUS_SUCCESS;
+}
+
+mpgemm_status_t mpgemm_check_grouped_wgrad(int64_t groups, int64_t rows, int64_t m, int64_t n, const float *alpha, const void *A,
+                                           mpgemm_dtype_t a_type, int64_t lda, const void *X, mpgemm_dtype_t x_type, int64_t ldx,
+                                           const int32_t *offsets, const float *beta, const void *D, mpgemm_dtype_t d_type,
+                                           int64_t ldd, int64_t stride_d) {
+    if (groups < 0 || rows < 0 || m < 0 || n < 0 || !alpha || !beta) return MPGEMM_STATUS_INVALID_VALUE;
+    MPGEMM_TRY(check_types(a_type, x_type, d_type));
+    if (lda < at_least1(m) || ldx < at_least1(n) || ldd < at_least1(n)) return MPGEMM_STATUS_INVALID_VALUE;
+    if (groups == 0 || m == 0 || n == 0) return MPGEMM_STATUS_SUCCESS;
+    if (!D || !offsets || (rows > 0 && (!A || !X))) return MPGEMM_STATUS_INVALID_VALUE;
+    if (rows > kOpMaxSize || m > kOpMaxSize || n > kOpMaxSize || groups > 65535 || !launchable(wgrad_plan(groups, m, n), groups))
+        return MPGEMM_STATUS_NOT_SUPPORTED;
+    const int ed = elem_bytes(d_type);
+    if ((rows > 0 && (!aligned(A, 16) || !aligned(X, 16))) || !aligned(D, 16) || !aligned(offsets, 4)) return MPGEMM_STATUS_NOT_SUPPORTED;
+    if (!stride_ok(lda, 2) || !stride_ok(ldx, 2) || !stride_ok(ldd, ed)) return MPGEMM_STATUS_NOT_SUPPORTED;
+    // the experts' D must not overlap: they are written at the same time
+    if (groups > 1 && stride_d < (m - 1) * ldd + n) return MPGEMM_STATUS_INVALID_VALUE;
+    if (stride_d < 0 || stride_d > INT64_MAX / 131072 || (groups > 1 && (stride_d * ed) % 16)) return MPGEMM_STATUS_NOT_SUPPORTED;
+    return MPGEMM_STATUS_SUCCESS;
+}
+
+uint64_t mpgemm_linear_ce_workspace_size(int64_t m, int64_t n, int64_t k, mpgemm_dtype_t type, int train) {
+    CeLayout L;
+    if (!half_type(type) || !ce_layout(m, n, k, train != 0, L)) return 0;
+    return m == 0 ? 0 : L.total;
+}
+
+mpgemm_status_t mpgemm_check_linear_ce(int64_t m, int64_t n, int64_t k, const float *alpha, const void *X, mpgemm_dtype_t type,
+                                       int64_t ldx, const void *W, int64_t ldw, const int64_t *target, const float *loss,
+                                       const float *lse, const void *workspace, uint64_t workspace_bytes) {
+    if (m < 0 || n < 1 || k < 0 || !alpha) return MPGEMM_STATUS_INVALID_VALUE;
+    if (!half_type(type)) return MPGEMM_STATUS_NOT_SUPPORTED;
+    if (ldx < at_least1(k) || ldw < at_least1(k)) return MPGEMM_STATUS_INVALID_VALUE;
+    if (m == 0) return MPGEMM_STATUS_SUCCESS;
+    if ((k > 0 && (!X || !W)) || !target || !loss || !lse) return MPGEMM_STATUS_INVALID_VALUE;
+    CeLayout L;
+    if (!ce_layout(m, n, k, false, L) || !launchable(L.logits, 1)) return MPGEMM_STATUS_NOT_SUPPORTED;
+    if (k > 0 && (!aligned(X, 16) || !aligned(W, 16))) return MPGEMM_STATUS_NOT_SUPPORTED;
+    if (!stride_ok(ldx, 2) || !stride_ok(ldw, 2) || !aligned(target, 8) || !aligned(loss, 4) || !aligned(lse, 4))
+        return MPGEMM_STATUS_NOT_SUPPORTED;
+    return check_workspace(workspace, workspace_bytes, L.total);
+}
+
+mpgemm_status_t mpgemm_check_linear_ce_grad(int64_t m, int64_t n, int64_t k, const float *alpha, const void *X, mpgemm_dtype_t type,
+                                            int64_t ldx, const void *W, int64_t ldw, const int64_t *target, const float *lse,
+                                            const float *grad, const void *dX, int64_t lddx, const void *dW, int64_t lddw,
+                                            const void *workspace, uint64_t workspace_bytes) {
+    if (m < 0 || n < 1 || k < 0 || !alpha) return MPGEMM_STATUS_INVALID_VALUE;
+    if (!half_type(type)) return MPGEMM_STATUS_NOT_SUPPORTED;
+    if (ldx < at_least1(k) || ldw < at_least1(k) || (dX && lddx < at_least1(k)) || (dW && lddw < at_least1(k)))
+        return MPGEMM_STATUS_INVALID_VALUE;
+    if (k == 0 || (!dX && !dW) || (m == 0 && !dW)) return MPGEMM_STATUS_SUCCESS;
+    if (m > 0 && (!X || !W || !target || !lse || !grad)) return MPGEMM_STATUS_INVALID_VALUE;
+    CeLayout L;
+    if (!ce_layout(m, n, k, true, L)) return MPGEMM_STATUS_NOT_SUPPORTED;
+    if (m > 0 && (!launchable(L.logits, 1) || !launchable(L.dx, L.splits) || !launchable(L.dw, 1))) return MPGEMM_STATUS_NOT_SUPPORTED;
+    if (m == 0 && !launchable(op_plan(n, k, false), 1)) return MPGEMM_STATUS_NOT_SUPPORTED;
+    if (m > 0 && (!aligned(X, 16) || !aligned(W, 16) || !stride_ok(ldx, 2) || !stride_ok(ldw, 2) || !aligned(target, 8) ||
+                  !aligned(lse, 4) || !aligned(grad, 4)))
+        return MPGEMM_STATUS_NOT_SUPPORTED;
+    if (dX && (!aligned(dX, 16) || !stride_ok(lddx, 2))) return MPGEMM_STATUS_NOT_SUPPORTED;
+    if (dW && (!aligned(dW, 16) || !stride_ok(lddw, 2))) return MPGEMM_STATUS_NOT_SUPPORTED;
+    return m == 0 ? MPGEMM_STATUS_SUCCESS : check_workspace(workspace, workspace_bytes, L.total);
+}
+
+}  // extern "C"

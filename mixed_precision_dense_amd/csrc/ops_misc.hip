@@ -1,0 +1,183 @@
+// ops_misc.hip -- the small kernels beside the op products: sums of partial column sums, of
+// partial products and of row statistics.  All of them are bound by what they read; every sum is
+// taken in a fixed order, so that results do not change from call to call.
+#include "mpgemm_ops_epilogue.hpp"
+
+namespace mpg {
+namespace {
+
+constexpr int kSumCols = 64;   // columns per workgroup of colsum_kernel
+
+// dbias[e][c] = sum over the partial rows of expert e's row tiles: 64 columns by 4 walkers over
+// the rows, whose shares meet in the LDS.
+__global__ __launch_bounds__(256) void colsum_kernel(OpParams p, int tile_rows, int rows_per_tile, float *dbias) {
+    __shared__ float share[4][kSumCols];
+    const int lane = threadIdx.x % 64, part = threadIdx.x / 64;
+    const int col = blockIdx.x * kSumCols + lane, e = blockIdx.y;
+    int64_t first = 0;
+    int tiles = p.tiles_m;
+    if (p.groups_kind == GROUPS_ROWS) {
+        int lo, hi;
+        expert_tiles(p, tile_rows, e, lane, first, tiles, lo, hi);
+        tiles = (int)min((int64_t)tiles, max((int64_t)0, p.tiles_m - first));   // (offsets outside the contract)
+    }
+    float s = 0.0f;
+    if (col < p.n) {
+        const float *at = p.colsum + first * rows_per_tile * p.ld_colsum + col;
+        for (int r = part; r < tiles * rows_per_tile; r += 4) s += at[(int64_t)r * p.ld_colsum];
+    }
+    share[part][lane] = s;
+    __syncthreads();
+    if (part == 0 && col < p.n)
+        dbias[(int64_t)e * p.n + col] = (share[0][lane] + share[1][lane]) + (share[2][lane] + share[3][lane]);
+}
+
+// One wave per row: log-sum-exp from the parts' statistics, and the target's logit as a dot
+// product of the row of X with the target's row of W (k * 4 bytes a row, where picking the logit
+// out of the tiles would cost every tile's epilogue a comparison per element).
+template <int IN>
+__global__ __launch_bounds__(256) void ce_merge_kernel(const CeStat *stats, int parts, int m, int n, int k, float alpha,
+                                                       const uint16_t *X, int64_t ldx, const uint16_t *W, int64_t ldw,
+                                                       const int64_t *target, float *loss, float *lse) {
+    const int lane = threadIdx.x % 64;
+    const int64_t row = (int64_t)blockIdx.x * 4 + threadIdx.x / 64;
+    if (row >= m) return;
+    const int64_t t = target[row];
+    const bool counts = t >= 0 && t < n;
+    float dot = 0.0f;
+    if (counts) {
+        const uint16_t *x = X + row * ldx, *w = W + t * ldw;
+        for (int c = 8 * lane; c < k; c += 512) {
+            float a[8], b[8];
+            widen8<IN>(*(const u32x4 *)(x + c), a);
+            widen8<IN>(*(const u32x4 *)(w + c), b);
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+                if (c + q < k) dot = __builtin_fmaf(a[q], b[q], dot);
+        }
+    }
+    float top = -__builtin_inff(), sum = 0.0f;
+    const CeStat *st = stats + row * parts;
+    for (int i = lane; i < parts; i += 64) {
+        const CeStat s = st[i];
+        const float up = fmaxf(top, s.top), base = stat_base(up);
+        sum = sum * fast_exp2(top - base) + s.sum * fast_exp2(s.top - base);
+        top = up;
+    }
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+        const float o_top = __shfl_xor(top, d, 64), o_sum = __shfl_xor(sum, d, 64);
+        const float up = fmaxf(top, o_top), base = stat_base(up);
+        sum = sum * fast_exp2(top - base) + o_sum * fast_exp2(o_top - base);
+        top = up;
+        dot += __shfl_xor(dot, d, 64);
+    }
+    if (lane == 0) {
+        const float l = (top + __log2f(sum)) * 0.69314718055994531f;
+        lse[row] = l;
+        loss[row] = counts ? l - alpha * dot : 0.0f;
+    }
+}
+
+// Row weights of the gradient: grad where the target counts, else 0.  FP16 gradients of logits are
+// often below FP16's normal range (a probability times 1 / rows): the weights are brought to at
+// most 2^14 by a power of two (exact), which scale[0] takes back from the products.
+constexpr int kWeightThreads = 1024;
+__global__ __launch_bounds__(kWeightThreads) void ce_weights_kernel(int bf16, int m, int n, const int64_t *target, const float *grad,
+                                                                    float *weight, float *scale) {
+    __shared__ float most[kWeightThreads / 64];
+    float up = 1.0f;
+    if (!bf16) {
+        float a = 0.0f;
+        for (int r = threadIdx.x; r < m; r += kWeightThreads) {
+            const int64_t t = target[r];
+            if (t >= 0 && t < n) a = fmaxf(a, __builtin_fabsf(grad[r]));
+        }
+#pragma unroll
+        for (int d = 1; d < 64; d *= 2) a = fmaxf(a, __shfl_xor(a, d, 64));
+        if (threadIdx.x % 64 == 0) most[threadIdx.x / 64] = a;
+        __syncthreads();
+        for (int i = 0; i < kWeightThreads / 64; ++i) a = fmaxf(a, most[i]);
+        if (a > 0.0f && a < __builtin_inff()) {
+            // a 2^e in [2^13, 2^14), e between -100 and 100
+            const int e = 13 - ((int)(__builtin_bit_cast(uint32_t, a) >> 23) - 127);
+            up = __builtin_bit_cast(float, (uint32_t)(127 + min(max(e, -100), 100)) << 23);
+        }
+    }
+    for (int r = threadIdx.x; r < m; r += kWeightThreads) {
+        const int64_t t = target[r];
+        weight[r] = t >= 0 && t < n ? grad[r] * up : 0.0f;
+    }
+    if (threadIdx.x == 0) scale[0] = 1.0f / up;
+}
+
+template <int IN>
+__global__ __launch_bounds__(256) void sum_parts_kernel(const float *parts, int splits, int64_t stride, int64_t ld_part,
+                                                        int rows, int cols, float alpha, const float *scale, uint16_t *out,
+                                                        int64_t ld_out) {
+    const int64_t chunks = ((int64_t)cols + 7) / 8;
+    const int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int64_t row = t / chunks;
+    if (row >= rows) return;
+    const int col = (int)(t - row * chunks) * 8;
+    float v[8];
+#pragma unroll
+    for (int q = 0; q < 8; ++q) v[q] = 0.0f;
+    const float *at = parts + row * ld_part + col;   // (rows of whole 8-column blocks)
+    for (int s = 0; s < splits; ++s, at += stride) {
+        const f32x4 a = *(const f32x4 *)at, b = *(const f32x4 *)(at + 4);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            v[q] += a[q];
+            v[q + 4] += b[q];
+        }
+    }
+    const float f = alpha * scale[0];
+#pragma unroll
+    for (int q = 0; q < 8; ++q) v[q] *= f;
+    store8<IN>(out, 0, row * ld_out + col, cols - col, v);
+}
+
+int launch_1d(const void *kernel, int64_t blocks, unsigned threads, void **args, void *stream) {
+    if (blocks == 0) return (int)hipSuccess;
+    if (blocks * threads > (int64_t)UINT32_MAX) return (int)hipErrorInvalidValue;   // 32-bit dispatch size
+    return (int)hipLaunchKernel(kernel, dim3((unsigned)blocks), dim3(threads), args, 0, (hipStream_t)stream);
+}
+
+}  // namespace
+
+int launch_colsum(const OpParams &p, int tile_rows, int rows_per_tile, float *dbias, void *stream) {
+    OpParams q = p;
+    void *args[] = {&q, &tile_rows, &rows_per_tile, &dbias};
+    return (int)hipLaunchKernel(reinterpret_cast<const void *>(&colsum_kernel),
+                                dim3((unsigned)((p.n + kSumCols - 1) / kSumCols), p.groups_kind == GROUPS_ROWS ? (unsigned)p.groups : 1u),
+                                dim3(256), args, 0, (hipStream_t)stream);
+}
+
+int launch_ce_merge(bool bf16, const CeStat *stats, int parts, int m, int n, int k, float alpha, const void *X, int64_t ldx,
+                    const void *W, int64_t ldw, const int64_t *target, float *loss, float *lse, void *stream) {
+    const uint16_t *x = (const uint16_t *)X, *w = (const uint16_t *)W;
+    void *args[] = {&stats, &parts, &m, &n, &k, &alpha, &x, &ldx, &w, &ldw, &target, &loss, &lse};
+    return launch_1d(bf16 ? reinterpret_cast<const void *>(&ce_merge_kernel<IN_BF16>)
+                          : reinterpret_cast<const void *>(&ce_merge_kernel<IN_F16>),
+                     ((int64_t)m + 3) / 4, 256, args, stream);
+}
+
+int launch_ce_weights(bool bf16, int m, int n, const int64_t *target, const float *grad, float *weight, float *scale,
+                      void *stream) {
+    int b = bf16 ? 1 : 0;
+    void *args[] = {&b, &m, &n, &target, &grad, &weight, &scale};
+    return launch_1d(reinterpret_cast<const void *>(&ce_weights_kernel), 1, kWeightThreads, args, stream);
+}
+
+int launch_sum_parts(bool bf16, const float *parts, int splits, int64_t stride, int64_t ld_part, int rows, int cols, float alpha,
+                     const float *scale, void *out, int64_t ld_out, void *stream) {
+    uint16_t *o = (uint16_t *)out;
+    void *args[] = {&parts, &splits, &stride, &ld_part, &rows, &cols, &alpha, &scale, &o, &ld_out};
+    const int64_t blocks = ((int64_t)rows * (((int64_t)cols + 7) / 8) + 255) / 256;
+    return launch_1d(bf16 ? reinterpret_cast<const void *>(&sum_parts_kernel<IN_BF16>)
+                          : reinterpret_cast<const void *>(&sum_parts_kernel<IN_F16>),
+                     blocks, 256, args, stream);
+}
+
+}  // namespace mpg
