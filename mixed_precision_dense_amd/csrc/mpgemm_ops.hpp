@@ -51,6 +51,7 @@ struct OpParams {
     void *D;
     int d_f32;                   // else the inputs' type
     int64_t ldd;
+    int lines;                   // D's (and aux's) rows are whole 128-byte lines
     float *colsum;               // OP_SLOPE: two rows of partial sums per row tile, or nullptr
     int64_t ld_colsum;
     int groups_kind, groups;
@@ -69,8 +70,12 @@ struct OpParams {
 
 // ------------------------------------------------------------------------------- launchers
 // (declared with void * streams so that this header stays free of HIP)
-int launch_op_f16(bool ta, bool tb, int tile, const OpParams &p, void *stream);
-int launch_op_bf16(bool ta, bool tb, int tile, const OpParams &p, void *stream);
+// the tiled kernel for p.mode; the cross entropy's are for A stored m x k and B stored n x k
+int launch_forward_f16(bool ta, bool tb, int tile, const OpParams &p, void *stream);
+int launch_forward_bf16(bool ta, bool tb, int tile, const OpParams &p, void *stream);
+int launch_slope_f16(bool ta, bool tb, int tile, const OpParams &p, void *stream);
+int launch_slope_bf16(bool ta, bool tb, int tile, const OpParams &p, void *stream);
+int launch_ce(bool bf16, int tile, const OpParams &p, void *stream);
 int launch_skinny_f16(bool ta, bool tb, int fm, int w, const OpParams &p, void *stream);
 int launch_skinny_bf16(bool ta, bool tb, int fm, int w, const OpParams &p, void *stream);
 // dbias from the tiles' partial column sums (rows_per_tile partial rows a tile)

@@ -15,6 +15,10 @@ using namespace mpg_host;
 
 namespace {
 
+// Rows of `ld` elements that start and end on 128-byte lines: whole tiles of them are stored past
+// the caches, which are left to the operands.
+bool lines(const void *base, int64_t ld, int bytes) { return ((uintptr_t)base & 127) == 0 && (ld * bytes) % 128 == 0; }
+
 mpg::OpParams product(const OpPlan &plan, int64_t m, int64_t n, int64_t k, float alpha, const void *A, int64_t lda,
                       const void *B, int64_t ldb, void *D, bool d_f32, int64_t ldd) {
     mpg::OpParams p = {};
@@ -34,6 +38,7 @@ mpg::OpParams product(const OpPlan &plan, int64_t m, int64_t n, int64_t k, float
     p.ldd = ldd;
     p.splits = 1;
     p.k_split = (int)k;
+    p.lines = lines(D, ldd, d_f32 ? 4 : 2);
     return p;
 }
 
@@ -44,6 +49,7 @@ void set_epilogue(mpg::OpParams &p, const mpgemm_epilogue_t *e) {
     p.bias_stride = e->bias_stride;
     p.aux = e->aux;
     p.ld_aux = e->ld_aux;
+    if (e->aux && !lines(e->aux, e->ld_aux, 2)) p.lines = 0;
 }
 
 void set_slope(mpg::OpParams &p, mpgemm_act_t act, const void *Z, int64_t ldz, float *dbias, void *workspace) {
@@ -55,12 +61,15 @@ void set_slope(mpg::OpParams &p, mpgemm_act_t act, const void *Z, int64_t ldz, f
     p.ld_colsum = round8(p.n);
 }
 
-mpgemm_status_t launch(const OpPlan &plan, bool bf16, bool ta, bool tb, const mpg::OpParams &p, void *stream) {
-    const int e = plan.skinny ? (bf16 ? mpg::launch_skinny_bf16 : mpg::launch_skinny_f16)(ta, tb, plan.fm, plan.w, p, stream)
-                              : (bf16 ? mpg::launch_op_bf16 : mpg::launch_op_f16)(ta, tb, plan.rows, p, stream);
-    return e == 0 ? MPGEMM_STATUS_SUCCESS : MPGEMM_STATUS_LAUNCH_FAILED;
-}
 mpgemm_status_t queued(int e) { return e == 0 ? MPGEMM_STATUS_SUCCESS : MPGEMM_STATUS_LAUNCH_FAILED; }
+
+mpgemm_status_t launch(const OpPlan &plan, bool bf16, bool ta, bool tb, const mpg::OpParams &p, void *stream) {
+    if (plan.skinny) return queued((bf16 ? mpg::launch_skinny_bf16 : mpg::launch_skinny_f16)(ta, tb, plan.fm, plan.w, p, stream));
+    if (p.mode == mpg::OP_CE_STATS || p.mode == mpg::OP_CE_PROBS) return queued(mpg::launch_ce(bf16, plan.rows, p, stream));
+    const auto f = p.mode == mpg::OP_SLOPE ? (bf16 ? mpg::launch_slope_bf16 : mpg::launch_slope_f16)
+                                           : (bf16 ? mpg::launch_forward_bf16 : mpg::launch_forward_f16);
+    return queued(f(ta, tb, plan.rows, p, stream));
+}
 
 mpgemm_status_t launch_dbias(const OpPlan &plan, const mpg::OpParams &p, float *dbias, void *stream) {
     return queued(mpg::launch_colsum(p, plan.rows, plan.skinny ? 1 : 2, dbias, stream));

@@ -18,77 +18,97 @@ __device__ __forceinline__ float fast_rcp(float x) { return __builtin_amdgcn_rcp
 // infinity for very negative x, whose reciprocal is the 0 that the sigmoid rounds to.
 __device__ __forceinline__ float sigmoid(float x) { return fast_rcp(1.0f + fast_exp2(-kLog2e * x)); }
 
-// Slopes are those of a point within +-30, where every activation's slope has reached 0 or 1 in
-// FP32: an infinite (or huge) value kept from the forward pass gives that limit, and no 0 * inf.
-// NaN stays NaN.
-__device__ __forceinline__ float near_zero(float z) { return z > 30.0f ? 30.0f : (z < -30.0f ? -30.0f : z); }
+// Where a slope multiplies by z the factor beside it has reached 0 beyond +-30 in FP32: z is cut
+// there, so that an infinite (or huge) value kept from the forward pass gives the slope's limit and
+// no 0 * inf.  (NaN comes through the other factor.)
+__device__ __forceinline__ float cut(float z) { return __builtin_amdgcn_fmed3f(z, -30.0f, 30.0f); }
 
-// The normal distribution's Phi(z) and exp(-z^2 / 2).  With x = |z| / sqrt(2) and
-// t = 1 / (1 + 0.43 x), erfc(x) = exp(-x^2) t q(t), q a polynomial of degree 7 fitted to erfcx(x)
-// in relative minimax over x in [0, 12] (2e-7, 5e-7 as evaluated in FP32): the lower tail keeps its
-// relative accuracy, as 1 + erf would not.
-__device__ __forceinline__ float normal_cdf(float z, float &bell) {
-    const float a = __builtin_fabsf(z);
-    const float t = fast_rcp(__builtin_fmaf(a, 0.43f * 0.70710678118654752f, 1.0f));
-    bell = fast_exp2(z * z * (-0.5f * kLog2e));
-    float q = 0.07090955117377087f;
-    q = __builtin_fmaf(q, t, -0.2990298556651683f);
-    q = __builtin_fmaf(q, t, 0.36473237500049616f);
-    q = __builtin_fmaf(q, t, -0.06881683436104556f);
-    q = __builtin_fmaf(q, t, 0.2382076128012132f);
-    q = __builtin_fmaf(q, t, 0.20746980043114047f);
-    q = __builtin_fmaf(q, t, 0.24398845434153432f);
-    q = __builtin_fmaf(q, t, 0.2425387182165695f);
-    const float tail = 0.5f * bell * (q * t);   // Phi(-|z|)
-    return z > 0.0f ? 1.0f - tail : tail;
+// Phi(-|z|) of the normal distribution, and bell = exp(-z^2 / 2).  With x = |z| / sqrt(2) and
+// t = 1 / (1 + p x), erfc(x) = exp(-x^2) t q(t), q a polynomial fitted to erfcx(x) in relative
+// minimax over x in [0, 12]; its coefficients are halved here.  The lower tail keeps its relative
+// accuracy, as 1 + erf would not.  Of degree 7 (p = 0.43): 2e-7, and 5e-7 as evaluated in FP32.  Of
+// degree 5 (p = 0.44): 5e-6, an eightieth of half a step of FP16's; what is stored in 16 bits is
+// taken from that one (two of 23 instruction slots less).
+template <bool SHORT>
+__device__ __forceinline__ float normal_tail(float z, float &bell) {
+    const float t = fast_rcp(__builtin_fmaf(__builtin_fabsf(z), (SHORT ? 0.44f : 0.43f) * 0.70710678118654752f, 1.0f));
+    bell = fast_exp2(z * (-0.5f * kLog2e) * z);
+    float q;
+    if constexpr (SHORT) {
+        q = -0.5f * 0.14610657632724167f;
+        q = __builtin_fmaf(q, t, 0.5f * 0.350655200165003f);
+        q = __builtin_fmaf(q, t, 0.5f * 0.04072797427306728f);
+        q = __builtin_fmaf(q, t, 0.5f * 0.26358810029300594f);
+        q = __builtin_fmaf(q, t, 0.5f * 0.24256906750537888f);
+        q = __builtin_fmaf(q, t, 0.5f * 0.24856106715653906f);
+    } else {
+        q = 0.5f * 0.07090955117377087f;
+        q = __builtin_fmaf(q, t, -0.5f * 0.2990298556651683f);
+        q = __builtin_fmaf(q, t, 0.5f * 0.36473237500049616f);
+        q = __builtin_fmaf(q, t, -0.5f * 0.06881683436104556f);
+        q = __builtin_fmaf(q, t, 0.5f * 0.2382076128012132f);
+        q = __builtin_fmaf(q, t, 0.5f * 0.20746980043114047f);
+        q = __builtin_fmaf(q, t, 0.5f * 0.24398845434153432f);
+        q = __builtin_fmaf(q, t, 0.5f * 0.2425387182165695f);
+    }
+    return bell * (q * t);
 }
 
 constexpr float kGeluC = 0.79788456080286536f;   // sqrt(2 / pi)
 constexpr float kGeluA = 0.044715f;
 
-template <int ACT>
+// SHORT: the value is stored in 16 bits (see normal_tail).
+template <int ACT, bool SHORT>
 __device__ __forceinline__ float act_value(float z) {
     if constexpr (ACT == ACT_RELU) return z <= 0.0f ? 0.0f : z;   // NaN stays NaN
+    // z Phi(z) = max(z, 0) - |z| Phi(-|z|); |z| is cut where the tail is 0, for infinite z
     if constexpr (ACT == ACT_GELU) {
         float bell;
-        return z * normal_cdf(z, bell);
+        const float tail = normal_tail<SHORT>(z, bell);
+        return __builtin_fmaf(-__builtin_fminf(__builtin_fabsf(z), 30.0f), tail, __builtin_fmaxf(z, 0.0f));
     }
     // 0.5 z (1 + tanh u) = z / (1 + exp(-2u))
     if constexpr (ACT == ACT_GELU_TANH)
-        return z * sigmoid(2.0f * kGeluC * z * __builtin_fmaf(kGeluA * z, z, 1.0f));
+        return z * sigmoid(z * __builtin_fmaf(2.0f * kGeluC * kGeluA * z, z, 2.0f * kGeluC));
     if constexpr (ACT == ACT_SILU) return z * sigmoid(z);
     return z;
 }
 
-template <int ACT>
+template <int ACT, bool SHORT>
 __device__ __forceinline__ float act_slope(float z) {
     if constexpr (ACT == ACT_RELU) return z > 0.0f ? 1.0f : 0.0f;
     if constexpr (ACT == ACT_NONE) return 1.0f;
-    z = near_zero(z);
     if constexpr (ACT == ACT_GELU) {
         float bell;
-        const float phi = normal_cdf(z, bell);
-        return __builtin_fmaf(z * 0.39894228040143268f, bell, phi);
+        const float tail = normal_tail<SHORT>(z, bell);
+        return __builtin_fmaf(cut(z) * 0.39894228040143268f, bell, z > 0.0f ? 1.0f - tail : tail);
     }
     if constexpr (ACT == ACT_GELU_TANH) {
-        const float z2 = z * z;
-        const float g = sigmoid(2.0f * kGeluC * z * __builtin_fmaf(kGeluA, z2, 1.0f));
+        const float g = sigmoid(z * __builtin_fmaf(2.0f * kGeluC * kGeluA * z, z, 2.0f * kGeluC));
         // d(2u)/dz = 2 c (1 + 3 a z^2)
-        return __builtin_fmaf(z * g * (1.0f - g), 2.0f * kGeluC * __builtin_fmaf(3.0f * kGeluA, z2, 1.0f), g);
+        const float c = cut(z);
+        return __builtin_fmaf(__builtin_fmaf(-g, g, g) * c, __builtin_fmaf(6.0f * kGeluC * kGeluA * c, c, 2.0f * kGeluC), g);
     }
-    const float g = sigmoid(z);   // ACT_SILU
-    return g * __builtin_fmaf(z, 1.0f - g, 1.0f);
+    const float g = sigmoid(z);   // ACT_SILU: g + z g (1 - g)
+    return __builtin_fmaf(__builtin_fmaf(-g, g, g), cut(z), g);
 }
 
-// Calls f(std::integral_constant<int, ACT>) for the activation named at run time (uniform).
+// Calls f(std::integral_constant<int, ACT>, std::bool_constant<SHORT>) for the activation named at
+// run time (uniform) and the output's type.
 template <typename F>
-__device__ __forceinline__ void with_act(int act, F &&f) {
+__device__ __forceinline__ void with_act(int act, bool f32, F &&f) {
+    using Long = std::false_type;
     switch (act) {
-    case ACT_RELU: f(std::integral_constant<int, ACT_RELU>{}); break;
-    case ACT_GELU: f(std::integral_constant<int, ACT_GELU>{}); break;
-    case ACT_GELU_TANH: f(std::integral_constant<int, ACT_GELU_TANH>{}); break;
-    case ACT_SILU: f(std::integral_constant<int, ACT_SILU>{}); break;
-    default: f(std::integral_constant<int, ACT_NONE>{}); break;
+    case ACT_RELU: f(std::integral_constant<int, ACT_RELU>{}, Long{}); break;
+    case ACT_GELU:
+        if (f32)
+            f(std::integral_constant<int, ACT_GELU>{}, Long{});
+        else
+            f(std::integral_constant<int, ACT_GELU>{}, std::true_type{});
+        break;
+    case ACT_GELU_TANH: f(std::integral_constant<int, ACT_GELU_TANH>{}, Long{}); break;
+    case ACT_SILU: f(std::integral_constant<int, ACT_SILU>{}, Long{}); break;
+    default: f(std::integral_constant<int, ACT_NONE>{}, Long{}); break;
     }
 }
 
@@ -136,35 +156,44 @@ struct OpTile {
     int64_t d_off;       // element offset of its D
 };
 
-// What an epilogue reads besides the product: eight columns of C and aux, as stored.
+// What an epilogue reads besides the product: eight columns of C or of the kept Z, as stored (hi: the
+// last four of FP32 values).
 struct ChunkIn {
-    u32x4 c0, c1, z;
+    u32x4 lo, hi;
 };
 
 // The eight columns col .. col + 7 of row `row` of D (ncol >= 1 of them exist).  C and aux are read
 // in whole 16-byte blocks that hold a column that exists.
+template <int MODE>
 __device__ __forceinline__ void chunk_load(const OpParams &p, const OpTile &w, int64_t row, int col, int ncol,
                                            ChunkIn &in) {
-    if (p.C != nullptr) {
+    if (MODE == OP_FORWARD && p.C != nullptr) {
         const int64_t at = w.d_off + row * p.ldc + col;
         if (p.c_f32) {
             const float *c = (const float *)p.C + at;
-            in.c0 = *(const u32x4 *)c;
-            if (ncol > 4) in.c1 = *(const u32x4 *)(c + 4);
+            in.lo = *(const u32x4 *)c;
+            if (ncol > 4) in.hi = *(const u32x4 *)(c + 4);
         } else {
-            in.c0 = *(const u32x4 *)((const uint16_t *)p.C + at);
+            in.lo = *(const u32x4 *)((const uint16_t *)p.C + at);
         }
     }
-    if (p.mode == OP_SLOPE && p.aux != nullptr) in.z = *(const u32x4 *)((const uint16_t *)p.aux + row * p.ld_aux + col);
+    if (MODE == OP_SLOPE && p.aux != nullptr) in.lo = *(const u32x4 *)((const uint16_t *)p.aux + row * p.ld_aux + col);
 }
 
+// Stores eight columns, ncol of which exist.  nt: past the caches (for whole 128-byte lines).
 template <int IN>
-__device__ __forceinline__ void store8(void *base, int f32, int64_t at, int ncol, const float (&v)[8]) {
+__device__ __forceinline__ void store8(void *base, int f32, int64_t at, int ncol, const float (&v)[8], bool nt = false) {
     if (f32) {
         float *d = (float *)base + at;
         if (ncol >= 8) {
-            *(f32x4 *)d = f32x4{v[0], v[1], v[2], v[3]};
-            *(f32x4 *)(d + 4) = f32x4{v[4], v[5], v[6], v[7]};
+            const f32x4 lo = {v[0], v[1], v[2], v[3]}, hi = {v[4], v[5], v[6], v[7]};
+            if (nt) {
+                __builtin_nontemporal_store(lo, (f32x4 *)d);
+                __builtin_nontemporal_store(hi, (f32x4 *)(d + 4));
+            } else {
+                *(f32x4 *)d = lo;
+                *(f32x4 *)(d + 4) = hi;
+            }
         } else {
 #pragma unroll
             for (int q = 0; q < 8; ++q)
@@ -174,7 +203,10 @@ __device__ __forceinline__ void store8(void *base, int f32, int64_t at, int ncol
         uint16_t *d = (uint16_t *)base + at;
         const u32x4 x = narrow8<IN>(v);
         if (ncol >= 8) {
-            *(u32x4 *)d = x;
+            if (nt)
+                __builtin_nontemporal_store(x, (u32x4 *)d);
+            else
+                *(u32x4 *)d = x;
         } else {
 #pragma unroll
             for (int q = 0; q < 8; ++q)
@@ -184,11 +216,11 @@ __device__ __forceinline__ void store8(void *base, int f32, int64_t at, int ncol
 }
 
 // The bias of columns col .. col + 7 (zeros where there is none).
-template <int IN>
+template <int IN, int MODE>
 __device__ __forceinline__ void bias_load(const OpParams &p, int expert, int col, float (&b)[8]) {
 #pragma unroll
     for (int q = 0; q < 8; ++q) b[q] = 0.0f;
-    if (p.bias == nullptr || p.mode != OP_FORWARD) return;
+    if (MODE != OP_FORWARD || p.bias == nullptr) return;
     const int64_t at = (int64_t)expert * p.bias_stride + col;
 #pragma unroll
     for (int q = 0; q < 8; ++q)
@@ -201,56 +233,107 @@ __device__ __forceinline__ float op_alpha(const OpParams &p) {
     return p.scale != nullptr ? p.alpha * p.scale[0] : p.alpha;
 }
 
-// Turns the products v of eight columns into what is stored, and stores it; sums adds up what
-// OP_SLOPE stores (before its rounding).  `drow` is the row of D, C and aux.
-template <int IN>
-__device__ __forceinline__ void chunk_finish(const OpParams &p, float alpha, const OpTile &w, int64_t drow, int col,
-                                             int ncol, const ChunkIn &in, const float (&bias)[8], float (&v)[8],
-                                             float (&sums)[8]) {
-    const int64_t at = w.d_off + drow * p.ldd + col;
-    if (p.mode == OP_SLOPE) {
-        float z[8];
-        widen8<IN>(in.z, z);
-        with_act(p.act, [&](auto a) {
+// Turns the products v of eight columns col .. in each of G rows into what is stored, and stores it;
+// sums adds up what OP_SLOPE stores (before its rounding).  drow(i) is row i of D, C and aux,
+// and ncol(i) how many of the columns exist there (at most 0: the row does not; whole: all do).  Branches that a
+// lane may take alone stand only around loads and stores: the arithmetic of two rows runs together,
+// so that one element's latencies are covered by the others' (all rows at once would need more
+// registers than a wave has).
+template <int IN, int MODE, int G, typename Row, typename Cols>
+__device__ __forceinline__ void rows_finish(const OpParams &p, float alpha, const OpTile &w, int col, bool whole, bool nt,
+                                            Row &&drow, Cols &&ncol, const ChunkIn (&in)[G], const float (&bias)[8], float (&v)[G][8],
+                                            float (&sums)[8]) {
+    if constexpr (MODE == OP_SLOPE) {
+        float z[G][8];
 #pragma unroll
-            for (int q = 0; q < 8; ++q) v[q] = alpha * v[q] * act_slope<decltype(a)::value>(z[q]);
+        for (int i = 0; i < G; ++i) widen8<IN>(in[i].lo, z[i]);
+        // (FP32 sums are taken of what is stored in 16 bits: those have the longer form, too)
+        with_act(p.act, p.d_f32 || p.colsum != nullptr, [&](auto a, auto s) {
+#pragma unroll
+            for (int i = 0; i < G; ++i) {
+#pragma unroll
+                for (int q = 0; q < 8; ++q)
+                    v[i][q] = alpha * v[i][q] * act_slope<decltype(a)::value, decltype(s)::value>(z[i][q]);
+                if (i % 2 == 1) __builtin_amdgcn_sched_barrier(0);
+            }
         });
+        if (p.colsum != nullptr) {
+            if (whole) {
 #pragma unroll
-        for (int q = 0; q < 8; ++q) sums[q] += v[q];
-    } else if (p.mode == OP_CE_PROBS) {
-        // A row that does not count has weight 0: nothing of its product may reach D.
-        const float wt = p.weight[drow], lse = p.lse[drow];
-        const int64_t t = p.target[drow] - p.col0 - col;
+                for (int i = 0; i < G; ++i)
 #pragma unroll
-        for (int q = 0; q < 8; ++q) {
-            const float e = fast_exp2(kLog2e * __builtin_fmaf(alpha, v[q], -lse));
-            v[q] = wt == 0.0f ? 0.0f : (e - (t == q ? 1.0f : 0.0f)) * wt;
+                    for (int q = 0; q < 8; ++q) sums[q] += v[i][q];
+            } else {
+#pragma unroll
+                for (int i = 0; i < G; ++i)
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) sums[q] += ncol(i) > 0 ? v[i][q] : 0.0f;
+            }
         }
+    } else if constexpr (MODE == OP_CE_PROBS) {
+        float wt[G], lse[G];
+        int64_t t[G];
+#pragma unroll
+        for (int i = 0; i < G; ++i) {
+            wt[i] = lse[i] = 0.0f;
+            t[i] = -1;
+            if (ncol(i) > 0) {
+                wt[i] = p.weight[drow(i)];
+                lse[i] = p.lse[drow(i)];
+                t[i] = p.target[drow(i)] - p.col0 - col;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < G; ++i)
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+                const float e = fast_exp2(kLog2e * __builtin_fmaf(alpha, v[i][q], -lse[i]));
+                // a row that does not count has weight 0: nothing of its product may reach D
+                v[i][q] = wt[i] == 0.0f ? 0.0f : (e - (t[i] == q ? 1.0f : 0.0f)) * wt[i];
+            }
     } else {
 #pragma unroll
-        for (int q = 0; q < 8; ++q) v[q] = __builtin_fmaf(alpha, v[q], bias[q]);
-        if (p.aux != nullptr) store8<IN>(p.aux, 0, drow * p.ld_aux + col, ncol, v);
-        with_act(p.act, [&](auto a) {
+        for (int i = 0; i < G; ++i)
 #pragma unroll
-            for (int q = 0; q < 8; ++q) v[q] = act_value<decltype(a)::value>(v[q]);
+            for (int q = 0; q < 8; ++q) v[i][q] = __builtin_fmaf(alpha, v[i][q], bias[q]);
+        if (p.aux != nullptr) {
+#pragma unroll
+            for (int i = 0; i < G; ++i)
+                if (ncol(i) > 0) store8<IN>(p.aux, 0, drow(i) * p.ld_aux + col, ncol(i), v[i], nt);
+        }
+        with_act(p.act, p.d_f32, [&](auto a, auto s) {
+#pragma unroll
+            for (int i = 0; i < G; ++i) {
+#pragma unroll
+                for (int q = 0; q < 8; ++q) v[i][q] = act_value<decltype(a)::value, decltype(s)::value>(v[i][q]);
+                if (i % 2 == 1) __builtin_amdgcn_sched_barrier(0);
+            }
         });
         if (p.C != nullptr) {
-            float c[8];
             if (p.c_f32) {
-                const f32x4 lo = __builtin_bit_cast(f32x4, in.c0), hi = __builtin_bit_cast(f32x4, in.c1);
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    c[q] = lo[q];
-                    c[q + 4] = hi[q];
+                for (int i = 0; i < G; ++i) {
+                    const f32x4 lo = __builtin_bit_cast(f32x4, in[i].lo), hi = __builtin_bit_cast(f32x4, in[i].hi);
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        v[i][q] = __builtin_fmaf(p.beta, lo[q], v[i][q]);
+                        v[i][q + 4] = __builtin_fmaf(p.beta, hi[q], v[i][q + 4]);
+                    }
                 }
             } else {
-                widen8<IN>(in.c0, c);
-            }
 #pragma unroll
-            for (int q = 0; q < 8; ++q) v[q] = __builtin_fmaf(p.beta, c[q], v[q]);
+                for (int i = 0; i < G; ++i) {
+                    float c[8];
+                    widen8<IN>(in[i].lo, c);
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) v[i][q] = __builtin_fmaf(p.beta, c[q], v[i][q]);
+                }
+            }
         }
     }
-    store8<IN>(p.D, p.d_f32, at, ncol, v);
+#pragma unroll
+    for (int i = 0; i < G; ++i)
+        if (ncol(i) > 0) store8<IN>(p.D, p.d_f32, w.d_off + drow(i) * p.ldd + col, ncol(i), v[i], nt);
 }
 
 // ------------------------------------------------------------------------------- experts' rows

@@ -160,17 +160,17 @@ void skinny_kernel(OpParams p) {
     const bool mine = row < BM;                    // (512 threads cover at most 64 rows x 8 chunks)
     static_assert(BM * CH <= 64 * kSkinnyWaves, "one chunk per thread");
     const int col = w.tn * BN + 8 * c, ncol = p.n - col;
-    float v[8];
+    float v[1][8];
 #pragma unroll
-    for (int q = 0; q < 8; ++q) v[q] = 0.0f;
+    for (int q = 0; q < 8; ++q) v[0][q] = 0.0f;
     if (mine) {
 #pragma unroll
         for (int x = 0; x < kSkinnyWaves; ++x) {
             const f32x4 lo = *(const f32x4 *)&part[x][row][8 * c], hi = *(const f32x4 *)&part[x][row][8 * c + 4];
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-                v[q] += lo[q];
-                v[q + 4] += hi[q];
+                v[0][q] += lo[q];
+                v[0][q + 4] += hi[q];
             }
         }
     }
@@ -179,13 +179,13 @@ void skinny_kernel(OpParams p) {
         float top = -__builtin_inff(), sum = 0.0f;
 #pragma unroll
         for (int q = 0; q < 8; ++q) {
-            v[q] = q < ncol ? v[q] * (alpha * kLog2e) : -__builtin_inff();
-            top = fmaxf(top, v[q]);
+            v[0][q] = q < ncol ? v[0][q] * (alpha * kLog2e) : -__builtin_inff();
+            top = fmaxf(top, v[0][q]);
         }
 #pragma unroll
         for (int d = 1; d < CH; d *= 2) top = fmaxf(top, __shfl_xor(top, d, 64));
 #pragma unroll
-        for (int q = 0; q < 8; ++q) sum += fast_exp2(v[q] - stat_base(top));
+        for (int q = 0; q < 8; ++q) sum += fast_exp2(v[0][q] - stat_base(top));
 #pragma unroll
         for (int d = 1; d < CH; d *= 2) sum += __shfl_xor(sum, d, 64);
         if (c == 0 && mine && row < m_left) p.stats[(int64_t)(w.tm * BM + row) * p.parts + w.tn] = CeStat{top, sum};
@@ -196,10 +196,20 @@ void skinny_kernel(OpParams p) {
     for (int q = 0; q < 8; ++q) sums[q] = 0.0f;
     const int64_t drow = (int64_t)w.row0 + w.tm * BM + row;
     if (live) {
-        ChunkIn in;
-        chunk_load(p, w, drow, col, ncol, in);
-        bias_load<IN>(p, w.expert, col, bias);
-        chunk_finish<IN>(p, alpha, w, drow, col, ncol, in, bias, v, sums);
+        auto finish = [&](auto mode) {
+            constexpr int MODE = decltype(mode)::value;
+            ChunkIn in[1];
+            chunk_load<MODE>(p, w, drow, col, ncol, in[0]);
+            bias_load<IN, MODE>(p, w.expert, col, bias);
+            rows_finish<IN, MODE, 1>(p, alpha, w, col, false, false, [&](int) { return drow; }, [&](int) { return ncol; }, in,
+                                     bias, v, sums);
+        };
+        if (p.mode == OP_SLOPE)
+            finish(std::integral_constant<int, OP_SLOPE>{});
+        else if (!TA && TB && p.mode == OP_CE_PROBS)
+            finish(std::integral_constant<int, OP_CE_PROBS>{});
+        else
+            finish(std::integral_constant<int, OP_FORWARD>{});
     }
     if (p.colsum != nullptr) {
         // the rows' shares in the LDS (the partial sums have been read), then one thread a column
