@@ -399,8 +399,9 @@ mpgemm_status_t mpgemm_run_linear_ce(mpgemm_handle_t handle, int64_t m, int64_t 
  * rows whose target does not count,
  *   dX = alpha * P W,   dW = alpha * P^T X      (type's; either may be NULL and is then skipped).
  *   lse: as mpgemm_run_linear_ce wrote it.  grad: m FP32 values, the gradient of each row's loss.
- *   P is computed in pieces of the vocabulary and rounded to the inputs' type for the products
- *   (FP16: scaled by a power of two first, so that small probabilities stay normal).
+ *   P is computed in pieces of the vocabulary and rounded to the inputs' type for the products,
+ *   after division by the largest |grad(i)| (FP16: and scaling by 2^13, so that small
+ *   probabilities stay normal).
  *   workspace: mpgemm_linear_ce_workspace_size(m, n, k, type, 1) bytes, which is also enough for
  *   mpgemm_run_linear_ce. */
 mpgemm_status_t mpgemm_run_linear_ce_grad(mpgemm_handle_t handle, int64_t m, int64_t n, int64_t k,

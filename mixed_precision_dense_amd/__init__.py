@@ -141,8 +141,15 @@ def _scalar(v, compute_type: int):
     return ctypes.c_float(float(v))
 
 
+# torch's current stream as an address, without the stream object that torch.cuda.current_stream()
+# makes on every call (2.8 us against 0.3, in calls of about 8 us).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream) -> Optional[int]:
     if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(torch.cuda.current_device())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
@@ -295,7 +302,12 @@ def _act(act: Union[str, int]) -> int:
 
 
 def _f32(v):
-    return ctypes.byref(ctypes.c_float(v))
+    """A scalar argument: the library reads it before the call returns and never writes it."""
+    known = _F32.get(v)
+    return ctypes.byref(ctypes.c_float(v)) if known is None else known
+
+
+_F32 = {v: ctypes.byref(ctypes.c_float(v)) for v in (1.0, 0.0)}   # (equal keys: 0.0 stands for -0.0 too)
 
 
 def _epi(e: Optional[Epilogue]):

@@ -76,15 +76,15 @@ int launch_forward_bf16(bool ta, bool tb, int tile, const OpParams &p, void *str
 int launch_slope_f16(bool ta, bool tb, int tile, const OpParams &p, void *stream);
 int launch_slope_bf16(bool ta, bool tb, int tile, const OpParams &p, void *stream);
 int launch_ce(bool bf16, int tile, const OpParams &p, void *stream);
-int launch_skinny_f16(bool ta, bool tb, int fm, int w, const OpParams &p, void *stream);
-int launch_skinny_bf16(bool ta, bool tb, int fm, int w, const OpParams &p, void *stream);
+int launch_skinny_f16(bool ta, bool tb, int fm, int w, int waves, const OpParams &p, void *stream);
+int launch_skinny_bf16(bool ta, bool tb, int fm, int w, int waves, const OpParams &p, void *stream);
 // dbias from the tiles' partial column sums (rows_per_tile partial rows a tile)
 int launch_colsum(const OpParams &p, int tile_rows, int rows_per_tile, float *dbias, void *stream);
 // loss and log-sum-exp from the row statistics; X and W give the target's logit
 int launch_ce_merge(bool bf16, const CeStat *stats, int parts, int m, int n, int k, float alpha,
                     const void *X, int64_t ldx, const void *W, int64_t ldw, const int64_t *target,
                     float *loss, float *lse, void *stream);
-// per-row weights (0 where the target does not count) scaled by a power of two; scale[0] = its inverse
+// per-row weights (0 where the target does not count) over a common factor, which goes to scale[0]
 int launch_ce_weights(bool bf16, int m, int n, const int64_t *target, const float *grad, float *weight,
                       float *scale, void *stream);
 // out (rows x cols, 16 bit) = alpha * scale[0] * sum of `splits` FP32 parts

@@ -64,7 +64,8 @@ void set_slope(mpg::OpParams &p, mpgemm_act_t act, const void *Z, int64_t ldz, f
 mpgemm_status_t queued(int e) { return e == 0 ? MPGEMM_STATUS_SUCCESS : MPGEMM_STATUS_LAUNCH_FAILED; }
 
 mpgemm_status_t launch(const OpPlan &plan, bool bf16, bool ta, bool tb, const mpg::OpParams &p, void *stream) {
-    if (plan.skinny) return queued((bf16 ? mpg::launch_skinny_bf16 : mpg::launch_skinny_f16)(ta, tb, plan.fm, plan.w, p, stream));
+    if (plan.skinny)
+        return queued((bf16 ? mpg::launch_skinny_bf16 : mpg::launch_skinny_f16)(ta, tb, plan.fm, plan.w, plan.waves, p, stream));
     if (p.mode == mpg::OP_CE_STATS || p.mode == mpg::OP_CE_PROBS) return queued(mpg::launch_ce(bf16, plan.rows, p, stream));
     const auto f = p.mode == mpg::OP_SLOPE ? (bf16 ? mpg::launch_slope_bf16 : mpg::launch_slope_f16)
                                            : (bf16 ? mpg::launch_forward_bf16 : mpg::launch_forward_f16);

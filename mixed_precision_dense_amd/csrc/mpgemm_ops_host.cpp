@@ -25,10 +25,38 @@ bool act_valid(int a) { return a >= MPGEMM_ACT_NONE && a <= MPGEMM_ACT_SILU; }
 bool stride_ok(int64_t ld, int eb) { return ld <= max_ld(eb) && (ld * eb) % 16 == 0; }
 
 OpPlan tiled(int64_t m, int64_t n, int edge) {
-    return OpPlan{false, 0, 0, edge, edge, ceil_div(m, edge), ceil_div(n, edge)};
+    return OpPlan{false, 0, 0, 0, edge, edge, ceil_div(m, edge), ceil_div(n, edge)};
 }
-OpPlan skinny(int64_t tiles_m, int64_t n, int fm, int w) {
-    return OpPlan{true, fm, w, 16 * fm, 16 * w, tiles_m, ceil_div(n, 16 * w)};
+
+// The kernel for few rows, tiles_m row tiles of 16 fm rows.  Columns per workgroup: with up to 16
+// rows, 64 where that still gives most CUs two workgroups (each row of A is read once for four
+// columns' blocks instead of one: 8 x 32000 x 4096, 63 -> 59 us), else as few as the storage of B
+// allows in loads of some width (16 where it is n x k, 32 where it is k x n), so that more CUs
+// read (1 x 4096 x 4096, B n x k: 9.4 us with 16 columns, 13.9 with 32).  Waves: eight, sharing k, where
+// there are at most two workgroups per CU (the same case: 9.4 us against 11.3 with four), else four,
+// whose shorter ends overlap with other workgroups' loads (64 rows of 32 experts, 1408 x 2048: 38 us
+// against 48 with eight).
+OpPlan skinny(int64_t tiles_m, int64_t n, int fm, bool tb) {
+    int w = 2;
+    if (fm == 1) w = tiles_m * ceil_div(n, 64) >= 3 * kCus / 2 ? 4 : (tb ? 1 : 2);
+    const int64_t tiles_n = ceil_div(n, 16 * w);
+    const int waves = fm == 4 || tiles_m * tiles_n <= 2 * kCus ? 8 : 4;
+    return OpPlan{true, fm, w, waves, 16 * fm, 16 * w, tiles_m, tiles_n};
+}
+// Tile edge with the least estimated time for a number of tiles of each size.  A 256-wide tile has a
+// CU to itself; two workgroups of 128-wide ones share a CU, which hides their epilogues but reads
+// the LDS twice as often per product: a round of 512 of them takes 0.55 to 0.6 of a round of 256
+// large ones (8192 x 8192 x 2048: 243 us against 215; 16384 rows over 64 experts, 2816 x 2048:
+// 294 against 298; 1999 rows over 7 experts, 1490 x 1003: 18 against 35).  64-wide ones are for
+// problems that would leave CUs without work.
+int best_edge(int64_t tiles256, int64_t tiles128, int64_t tiles64) {
+    const auto cost = [](int64_t tiles, int64_t slots, double alone, double shared) {
+        return tiles <= kCus ? alone : (double)ceil_div(tiles, slots) * shared;
+    };
+    const double c256 = cost(tiles256, kCus, 1.0, 1.0), c128 = cost(tiles128, 2 * kCus, 0.45, 0.6),
+                 c64 = cost(tiles64, 3 * kCus, 0.3, 0.5);
+    if (c256 <= c128 && c256 <= c64) return 256;
+    return c128 <= c64 ? 128 : 64;
 }
 
 // Launches have a 32-bit number of lanes: at most this many workgroups of 256 or 512.
@@ -43,29 +71,29 @@ bool launchable(const OpPlan &p, int64_t times) {
 OpPlan op_plan(int64_t m, int64_t n, bool tb) {
     if (m <= 64 && n <= ((int64_t)1 << 22)) {
         const int fm = m <= 16 ? 1 : (m <= 32 ? 2 : 4);
-        return skinny(1, n, fm, fm == 1 && tb ? 1 : 2);
+        return skinny(1, n, fm, tb);
     }
-    return tiled(m, n, pick_tile(m, n, false, kCus));
+    const auto tiles = [&](int64_t e) { return ceil_div(m, e) * ceil_div(n, e); };
+    return tiled(m, n, best_edge(tiles(256), tiles(128), tiles(64)));
 }
 
 OpPlan grouped_plan(int64_t rows, int64_t groups, int64_t n, bool tb) {
     const int64_t mean = ceil_div(rows, groups > 0 ? groups : 1);
-    OpPlan p;
+    const int64_t owners = groups < rows ? groups : rows;   // an expert's last tile may be short
     if (mean <= 32 && n <= ((int64_t)1 << 22)) {
         const int fm = mean <= 8 ? 1 : (mean <= 20 ? 2 : 4);
-        p = skinny(0, n, fm, fm == 1 && tb ? 1 : 2);
-    } else {
-        p = tiled(rows, n, mean <= 64 ? 64 : (mean <= 192 ? 128 : 256));
+        return skinny(rows / (16 * fm) + owners, n, fm, tb);
     }
-    p.tiles_m = rows / p.rows + (groups < rows ? groups : rows);   // an expert's last tile may be short
+    // half a tile per expert is lost on average
+    const auto tiles = [&](int64_t e) { return (rows / e + owners / 2) * ceil_div(n, e); };
+    OpPlan p = tiled(rows, n, best_edge(tiles(256), tiles(128), tiles(64)));
+    p.tiles_m = rows / p.rows + owners;
     return p;
 }
 
 OpPlan wgrad_plan(int64_t groups, int64_t m, int64_t n) {
-    int edge = 64;
-    for (int e = 128; e <= 256; e *= 2)
-        if (groups * ceil_div(m, e) * ceil_div(n, e) >= kCus) edge = e;
-    return tiled(m, n, edge);
+    const auto tiles = [&](int64_t e) { return groups * ceil_div(m, e) * ceil_div(n, e); };
+    return tiled(m, n, best_edge(tiles(256), tiles(128), tiles(64)));
 }
 
 int64_t colsum_rows(int64_t groups, int64_t m) {

@@ -10,10 +10,10 @@ namespace mpg_host {
 
 constexpr int64_t kOpMaxSize = (int64_t)INT32_MAX - 255;   // sizes, rounded up to a tile, stay 32-bit
 
-// The kernel of one product: the kernel for few rows (fm x w blocks of 16) or a tile edge.
+// The kernel of one product: the kernel for few rows (fm x w blocks of 16, four or eight waves) or a tile edge.
 struct OpPlan {
     bool skinny;
-    int fm, w;
+    int fm, w, waves;
     int rows, cols;   // of D per workgroup
     int64_t tiles_m, tiles_n;
 };

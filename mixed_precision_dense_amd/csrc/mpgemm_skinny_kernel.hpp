@@ -2,11 +2,11 @@
 // workgroup, with the same epilogues as the tiled kernel.
 //
 // With few rows a product is bound by reading B once, and a tile of 64 or more columns per
-// workgroup leaves most CUs without work.  Here a workgroup of eight waves takes 16 or 32 columns
-// and its waves share k: each reads blocks of B (and the rows of A, which the L2 holds) straight
-// into MFMA fragments, a block ahead of the one it multiplies, and the eight partial sums meet in
-// the LDS at the end, in a fixed order.  No barrier stands inside the loop, so the loads of eight
-// waves keep flowing.
+// workgroup leaves most CUs without work.  Here a workgroup of four or eight waves takes 16, 32 or
+// 64 columns and its waves share k: each reads blocks of B (and the rows of A, which the L2 holds) straight
+// into MFMA fragments, a block ahead of the one it multiplies, and the partial sums meet in the LDS
+// at the end, in a fixed order.  No barrier stands inside the loop, so the loads of all waves keep
+// flowing.
 //
 // Fragments of a K-contiguous operand are its 16-byte chunks.  An operand that is contiguous the
 // other way is read W (or FM) neighbouring elements of a row per lane, for the lane's eight k, and
@@ -17,8 +17,6 @@
 #include "mpgemm_ops_epilogue.hpp"
 
 namespace mpg {
-
-constexpr int kSkinnyWaves = 8;
 
 template <int IN>
 __device__ __forceinline__ f32x4 mfma32(u32x4 a, u32x4 b, f32x4 c) {
@@ -83,13 +81,13 @@ struct Strip {
     static __device__ __forceinline__ int place(int j, int u) { return KC ? 16 * j + u : NB * u + j; }
 };
 
-template <int IN, bool TA, bool TB, int FM, int W>
-__global__ __launch_bounds__(64 * kSkinnyWaves)
+template <int IN, bool TA, bool TB, int FM, int W, int NWV>
+__global__ __launch_bounds__(64 * NWV)
 void skinny_kernel(OpParams p) {
     constexpr int BM = 16 * FM, BN = 16 * W;
     constexpr int RS = BN + 4;                     // floats of a staged row
     constexpr int UN = FM * W >= 8 ? 2 : 4;        // MFMA steps per block
-    __shared__ __attribute__((aligned(16))) float part[kSkinnyWaves][BM][RS];
+    __shared__ __attribute__((aligned(16))) float part[NWV][BM][RS];
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), lane = threadIdx.x % 64;
     OpTile w;
     if (!locate<BM>(p, blockIdx.x, blockIdx.y, lane, w)) return;
@@ -133,15 +131,15 @@ void skinny_kernel(OpParams p) {
                 for (int j = 0; j < W; ++j) acc[i][j] = mfma32<IN>(fa[i], fb[j], acc[i][j]);
         }
     };
-    // blocks wave, wave + 8, ...: one is multiplied while the next is on its way
+    // blocks wave, wave + NWV, ...: one is multiplied while the next is on its way
     const int nb = (w.k + 32 * UN - 1) / (32 * UN);
     int b = wave;
     if (b < nb) load(blk[0], b);
-    for (; b < nb; b += 2 * kSkinnyWaves) {
-        if (b + kSkinnyWaves < nb) load(blk[1], b + kSkinnyWaves);
+    for (; b < nb; b += 2 * NWV) {
+        if (b + NWV < nb) load(blk[1], b + NWV);
         multiply(blk[0], b);
-        if (b + 2 * kSkinnyWaves < nb) load(blk[0], b + 2 * kSkinnyWaves);
-        if (b + kSkinnyWaves < nb) multiply(blk[1], b + kSkinnyWaves);
+        if (b + 2 * NWV < nb) load(blk[0], b + 2 * NWV);
+        if (b + NWV < nb) multiply(blk[1], b + NWV);
     }
 
     const int g = lane / 16, u = lane % 16;
@@ -157,15 +155,15 @@ void skinny_kernel(OpParams p) {
     constexpr int CH = BN / 8;
     const float alpha = op_alpha(p);
     const int c = threadIdx.x % CH, row = threadIdx.x / CH;
-    const bool mine = row < BM;                    // (512 threads cover at most 64 rows x 8 chunks)
-    static_assert(BM * CH <= 64 * kSkinnyWaves, "one chunk per thread");
+    const bool mine = row < BM;
+    static_assert(BM * CH <= 64 * NWV, "one chunk per thread");
     const int col = w.tn * BN + 8 * c, ncol = p.n - col;
     float v[1][8];
 #pragma unroll
     for (int q = 0; q < 8; ++q) v[0][q] = 0.0f;
     if (mine) {
 #pragma unroll
-        for (int x = 0; x < kSkinnyWaves; ++x) {
+        for (int x = 0; x < NWV; ++x) {
             const f32x4 lo = *(const f32x4 *)&part[x][row][8 * c], hi = *(const f32x4 *)&part[x][row][8 * c + 4];
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
@@ -228,12 +226,17 @@ void skinny_kernel(OpParams p) {
     }
 }
 
-template <int IN, bool TA, bool TB, int FM, int W>
-int launch_skinny(const OpParams &p, hipStream_t stream) {
+template <int IN, bool TA, bool TB, int FM, int W, int NWV>
+int launch_skinny_shape(const OpParams &p, hipStream_t stream) {
     const unsigned tiles = (unsigned)p.tiles_m * (unsigned)p.tiles_n;
     void *args[] = {const_cast<OpParams *>(&p)};
-    return (int)hipLaunchKernel(reinterpret_cast<const void *>(&skinny_kernel<IN, TA, TB, FM, W>),
-                                dim3(tiles, (unsigned)p.splits), dim3(64 * kSkinnyWaves), args, 0, stream);
+    return (int)hipLaunchKernel(reinterpret_cast<const void *>(&skinny_kernel<IN, TA, TB, FM, W, NWV>),
+                                dim3(tiles, (unsigned)p.splits), dim3(64 * NWV), args, 0, stream);
+}
+
+template <int IN, bool TA, bool TB, int FM, int W>
+int launch_skinny(int waves, const OpParams &p, hipStream_t s) {
+    return waves == 8 ? launch_skinny_shape<IN, TA, TB, FM, W, 8>(p, s) : launch_skinny_shape<IN, TA, TB, FM, W, 4>(p, s);
 }
 
 }  // namespace mpg

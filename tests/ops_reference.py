@@ -144,8 +144,8 @@ def cross_entropy_grad64(x, w, target, grad, alpha, k, t):
     p[rows, tt[counts]] -= 1
     weight = torch.where(counts, grad.double().cpu(), torch.zeros(m, dtype=torch.float64))
     p, p_err = p * weight[:, None], p_err * weight.abs()[:, None]
-    # the rounding; FP16's weights are brought to 2^13 and more first, so that its smallest step
-    # (2^-24, half of it off) stands for at most max |weight| 2^-37
+    # the rounding; FP16's weights are brought to 2^13 first, so that its smallest step (2^-24, half
+    # of it off) stands for max |weight| 2^-37
     step = 2.0 ** -38 * float(weight.abs().max()) if t == "f16" and m else 0.0
     p_err = p_err + torch.finfo(TYPES[t]).eps / 2 * (p.abs() + p_err) + step + 2.0 ** -23 * p.abs()
     xd, wd = x.double().cpu(), w.double().cpu()
