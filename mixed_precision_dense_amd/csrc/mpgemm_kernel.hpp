@@ -251,8 +251,12 @@ struct Operand {
     // one; at least 1.
     // lds_base: byte offset of this operand's stages in LDS, folded into the read offsets.
     // wave: the quarter v this wave loads (wave index mod 4); hi: the wave index / 4.
+    // first_blk: the wave's first fragment block.  Where a wave has fewer blocks than a column group,
+    // its read offsets start at that block's place in the group, so that block j of the wave always
+    // uses offset j mod kGroupBlocks: a place known only at run time would turn the offsets into
+    // an array in memory (64 x 64 tiles, MN-contiguous operand: 840 x 728 x 168 in 15 us, not 5).
     __device__ __forceinline__ void init(int wave, int hi, int lane, int64_t ld, int mn_left,
-                                         uint32_t lds_base) {
+                                         uint32_t lds_base, int first_blk = 0) {
         const uint32_t row_bytes = (uint32_t)(ld * EB);
         const int g = lane / 16, u = lane % 16;
         if constexpr (KC) {
@@ -268,6 +272,7 @@ struct Operand {
         } else {
             const int kr = wave * 8 + lane / 8;                     // k-row within a 32-row slot
             const int c = (lane % 8) ^ mn_swz(kr);                  // logical chunk in the group
+            const int b0 = first_blk % kGroupBlocks;
             // chunks past the operand's row end (edge tiles) are clamped to its last 16-byte
             // block, so no load runs into later rows
             const int col_max = ((mn_left * EB + 15) & ~15) - 16;
@@ -283,14 +288,14 @@ struct Operand {
                 const int s = u >> 2, q = u & 3, k = 8 * g + s;
 #pragma unroll
                 for (int pb = 0; pb < kGroupBlocks; ++pb)
-                    r_off[pb] = lds_base + (uint32_t)(k * 128 + 16 * ((2 * pb + (q >> 1)) ^ mn_swz(k)) + 8 * (q & 1));
+                    r_off[pb] = lds_base + (uint32_t)(k * 128 + 16 * ((2 * (b0 + pb) + (q >> 1)) ^ mn_swz(k)) + 8 * (q & 1));
             } else {
                 // tr8: lane 2 s + q of group g reads k-row 16 g + s (+8 for the high half),
                 // 8 bytes at column 8 q of its 16-column block
                 const int s = u >> 1, q = u & 1, k = 16 * g + s;
 #pragma unroll
                 for (int pb = 0; pb < kGroupBlocks; ++pb)
-                    r_off[pb] = lds_base + (uint32_t)(k * 128 + 16 * (pb ^ mn_swz(k)) + 8 * q);
+                    r_off[pb] = lds_base + (uint32_t)(k * 128 + 16 * ((b0 + pb) ^ mn_swz(k)) + 8 * q);
             }
         }
     }
@@ -359,21 +364,22 @@ struct Operand {
         }
     }
 
-    // 16-byte MFMA operand of 16-wide block `blk` at k step `ks` (0 or 1) of a stage; `stage`
-    // is the LDS start plus the stage's offset from this operand's first stage.
-    __device__ __forceinline__ u32x4 frag(const lds_char *stage, int blk, int ks) const {
+    // 16-byte MFMA operand of the 16-wide block j of the wave whose first block is first_blk (as in
+    // init) at k step `ks` (0 or 1) of a stage; `stage` is the LDS start plus the stage's offset
+    // from this operand's first stage.
+    __device__ __forceinline__ u32x4 frag(const lds_char *stage, int first_blk, int j, int ks) const {
         if constexpr (KC) {
-            return *(const __attribute__((address_space(3))) u32x4 *)(stage + blk * 2048 + r_off[ks]);
+            return *(const __attribute__((address_space(3))) u32x4 *)(stage + (first_blk + j) * 2048 + r_off[ks]);
         } else if constexpr (EB == 2) {
             typedef __attribute__((address_space(3))) i16x4 lds_i16x4;
-            const lds_char *p = stage + (blk / kGroupBlocks) * kGroupBytes + r_off[blk % kGroupBlocks] + ks * kStepK * 128;
+            const lds_char *p = stage + (first_blk / kGroupBlocks + j / kGroupBlocks) * kGroupBytes + r_off[j % kGroupBlocks] + ks * kStepK * 128;
             const i16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4 *)(p));
             const i16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4 *)(p + 4 * 128));
             // register concatenation only: no arithmetic waits on the reads here
             return __builtin_bit_cast(u32x4, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
         } else {
             typedef __attribute__((address_space(3))) i32x2 lds_i32x2;
-            const lds_char *p = stage + (blk / kGroupBlocks) * kGroupBytes + r_off[blk % kGroupBlocks] + ks * kStepK * 128;
+            const lds_char *p = stage + (first_blk / kGroupBlocks + j / kGroupBlocks) * kGroupBytes + r_off[j % kGroupBlocks] + ks * kStepK * 128;
             const i32x2 lo = __builtin_amdgcn_ds_read_tr8_b64_v2i32((lds_i32x2 *)(p));
             const i32x2 hi = __builtin_amdgcn_ds_read_tr8_b64_v2i32((lds_i32x2 *)(p + 8 * 128));
             return __builtin_bit_cast(u32x4, __builtin_shufflevector(lo, hi, 0, 1, 2, 3));
@@ -918,8 +924,8 @@ __device__ __forceinline__ void tile_product(const Params &p, int m0, int n0, ld
 
     OpA opa;
     OpB opb;
-    opa.init(vq, hi, lane, p.lda, m_left, 0u);
-    opb.init(vq, hi, lane, p.ldb, n_left, (uint32_t)(kBuffers * A_BYTES));
+    opa.init(vq, hi, lane, p.lda, m_left, 0u, wm * FM);
+    opb.init(vq, hi, lane, p.ldb, n_left, (uint32_t)(kBuffers * A_BYTES), wn * FN);
 
     const int nk = (p.k + kStageK - 1) / kStageK;
     const int k_tail = p.k % kStageK;
@@ -984,13 +990,13 @@ __device__ __forceinline__ void tile_product(const Params &p, int m0, int n0, ld
         // u - FM of B from the B buffer at b_off (whose bases are bb[bpar])
         auto read_unit = [&](int set, int pa, uint32_t b_off, int bpar, int ks, int u) {
             if (u < FM) {
-                fa[set][u] = opa.frag(smem + pa * A_BYTES, wm * FM + u, ks);
+                fa[set][u] = opa.frag(smem + pa * A_BYTES, wm * FM, u, ks);
             } else {
                 const int j = u - FM;
                 if constexpr (kPinB)
                     fb[set][j] = opb.frag_at(bb[bpar][TB ? ks : j % OpB::kGroupBlocks], j, ks);
                 else
-                    fb[set][j] = opb.frag(smem + b_off, wn * FN + j, ks);
+                    fb[set][j] = opb.frag(smem + b_off, wn * FN, j, ks);
             }
         };
         // Load slot l of a stage's A (into A buffer pa) or B (into the B buffer whose LDS
@@ -1177,11 +1183,11 @@ __device__ __forceinline__ void tile_product(const Params &p, int m0, int n0, ld
         static_assert(FM % 2 == 0 && FN >= 2, "FP8 tiles");
         u32x8 fa8[FM], fb8[FN];
         auto read_a = [&](int parity, int blk, int ks) {
-            set_half(fa8[blk], ks, opa.frag(smem + parity * A_BYTES, wm * FM + blk, ks));
+            set_half(fa8[blk], ks, opa.frag(smem + parity * A_BYTES, wm * FM, blk, ks));
         };
         // B from the B buffer at b_off (three buffers, rotating as in the 2-byte path)
         auto read_b = [&](uint32_t b_off, int blk, int ks) {
-            set_half(fb8[blk], ks, opb.frag(smem + b_off, wn * FN + blk, ks));
+            set_half(fb8[blk], ks, opb.frag(smem + b_off, wn * FN, blk, ks));
         };
         i32x4 rs_a, rs_b;
         auto load_a = [&](int pa, int l) { opa.load(rs_a, lds_w + (uint32_t)(pa * A_BYTES), l); };

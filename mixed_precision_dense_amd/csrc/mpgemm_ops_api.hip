@@ -97,7 +97,7 @@ mpgemm_status_t mpgemm_run_epilogue(mpgemm_handle_t handle, mpgemm_op_t transa, 
     if (m == 0 || n == 0) return MPGEMM_STATUS_SUCCESS;
     MPGEMM_TRY(handle_on_device(handle));
     const bool ta = transa == MPGEMM_OP_T, tb = transb == MPGEMM_OP_T;
-    const OpPlan plan = op_plan(m, n, tb);
+    const OpPlan plan = op_plan(m, n, k, tb);
     mpg::OpParams p = product(plan, m, n, k, *alpha, A, lda, B, ldb, D, d_type == MPGEMM_R_32F, ldd);
     set_epilogue(p, epilogue);
     if (!beta_is_zero(beta, MPGEMM_R_32F)) {
@@ -120,7 +120,7 @@ mpgemm_status_t mpgemm_run_epilogue_grad(mpgemm_handle_t handle, mpgemm_op_t tra
     if (n == 0 || (m == 0 && !dbias)) return MPGEMM_STATUS_SUCCESS;
     MPGEMM_TRY(handle_on_device(handle));
     const bool ta = transa == MPGEMM_OP_T, tb = transb == MPGEMM_OP_T;
-    const OpPlan plan = op_plan(m, n, tb);
+    const OpPlan plan = op_plan(m, n, k, tb);
     mpg::OpParams p = product(plan, m, n, k, *alpha, A, lda, B, ldb, D, d_type == MPGEMM_R_32F, ldd);
     set_slope(p, act, Z, ldz, dbias, workspace);
     if (m == 0) p.tiles_m = 0;   // no rows: only their sum is written
@@ -138,7 +138,7 @@ mpgemm_status_t mpgemm_run_grouped(mpgemm_handle_t handle, mpgemm_op_t transb, i
     if (groups == 0 || rows == 0 || n == 0) return MPGEMM_STATUS_SUCCESS;
     MPGEMM_TRY(handle_on_device(handle));
     const bool tb = transb == MPGEMM_OP_T;
-    const OpPlan plan = grouped_plan(rows, groups, n, tb);
+    const OpPlan plan = grouped_plan(rows, groups, n, k, tb);
     mpg::OpParams p = product(plan, rows, n, k, *alpha, A, lda, B, ldb, D, d_type == MPGEMM_R_32F, ldd);
     set_epilogue(p, epilogue);
     p.groups_kind = mpg::GROUPS_ROWS;
@@ -159,7 +159,7 @@ mpgemm_status_t mpgemm_run_grouped_grad(mpgemm_handle_t handle, mpgemm_op_t tran
     if (groups == 0 || n == 0 || (rows == 0 && !dbias)) return MPGEMM_STATUS_SUCCESS;
     MPGEMM_TRY(handle_on_device(handle));
     const bool tb = transb == MPGEMM_OP_T;
-    const OpPlan plan = grouped_plan(rows, groups, n, tb);
+    const OpPlan plan = grouped_plan(rows, groups, n, k, tb);
     mpg::OpParams p = product(plan, rows, n, k, *alpha, A, lda, B, ldb, D, d_type == MPGEMM_R_32F, ldd);
     set_slope(p, act, Z, ldz, dbias, workspace);
     p.groups_kind = mpg::GROUPS_ROWS;
@@ -179,7 +179,7 @@ mpgemm_status_t mpgemm_run_grouped_wgrad(mpgemm_handle_t handle, int64_t groups,
                                           stride_d));
     if (groups == 0 || m == 0 || n == 0) return MPGEMM_STATUS_SUCCESS;
     MPGEMM_TRY(handle_on_device(handle));
-    const OpPlan plan = wgrad_plan(groups, m, n);
+    const OpPlan plan = wgrad_plan(groups, rows, m, n);
     mpg::OpParams p = product(plan, m, n, rows, *alpha, A, lda, X, ldx, D, d_type == MPGEMM_R_32F, ldd);
     p.groups_kind = mpg::GROUPS_K;
     p.groups = (int)groups;
@@ -224,7 +224,7 @@ mpgemm_status_t mpgemm_run_linear_ce_grad(mpgemm_handle_t handle, int64_t m, int
     MPGEMM_TRY(handle_on_device(handle));
     const bool bf16 = type == MPGEMM_R_16BF;
     if (m == 0) {   // a sum over no rows
-        const OpPlan plan = op_plan(n, k, false);
+        const OpPlan plan = op_plan(n, k, 0, false);
         return launch(plan, bf16, true, false, product(plan, n, k, 0, 0.0f, nullptr, 8, nullptr, 8, dW, false, lddw), stream);
     }
     CeLayout L;
@@ -237,7 +237,7 @@ mpgemm_status_t mpgemm_run_linear_ce_grad(mpgemm_handle_t handle, int64_t m, int
     for (int64_t c = 0; c < L.pieces; ++c) {
         const int64_t first = c * L.piece, have = n - first < L.piece ? n - first : L.piece;
         const char *w = (const char *)W + first * ldw * 2;
-        const OpPlan lp = op_plan(m, have, true);
+        const OpPlan lp = op_plan(m, have, k, true);
         mpg::OpParams p = product(lp, m, have, k, *alpha, X, ldx, w, ldw, probs, false, L.piece);
         p.mode = mpg::OP_CE_PROBS;
         p.target = target;
@@ -246,7 +246,7 @@ mpgemm_status_t mpgemm_run_linear_ce_grad(mpgemm_handle_t handle, int64_t m, int
         p.col0 = (int)first;
         MPGEMM_TRY(launch(lp, bf16, false, true, p, stream));
         if (dW) {
-            const OpPlan plan = op_plan(have, k, false);
+            const OpPlan plan = op_plan(have, k, m, false);
             mpg::OpParams q = product(plan, have, k, m, *alpha, probs, L.piece, X, ldx, (char *)dW + first * lddw * 2, false, lddw);
             q.scale = scale;
             MPGEMM_TRY(launch(plan, bf16, true, false, q, stream));

@@ -43,20 +43,31 @@ OpPlan skinny(int64_t tiles_m, int64_t n, int fm, bool tb) {
     const int waves = fm == 4 || tiles_m * tiles_n <= 2 * kCus ? 8 : 4;
     return OpPlan{true, fm, w, waves, 16 * fm, 16 * w, tiles_m, tiles_n};
 }
-// Tile edge with the least estimated time for a number of tiles of each size.  A 256-wide tile has a
-// CU to itself; two workgroups of 128-wide ones share a CU, which hides their epilogues but reads
-// the LDS twice as often per product: a round of 512 of them takes 0.55 to 0.6 of a round of 256
-// large ones (8192 x 8192 x 2048: 243 us against 215; 16384 rows over 64 experts, 2816 x 2048:
-// 294 against 298; 1999 rows over 7 experts, 1490 x 1003: 18 against 35).  64-wide ones are for
-// problems that would leave CUs without work.
-int best_edge(int64_t tiles256, int64_t tiles128, int64_t tiles64) {
-    const auto cost = [](int64_t tiles, int64_t slots, double alone, double shared) {
-        return tiles <= kCus ? alone : (double)ceil_div(tiles, slots) * shared;
-    };
-    const double c256 = cost(tiles256, kCus, 1.0, 1.0), c128 = cost(tiles128, 2 * kCus, 0.45, 0.6),
-                 c64 = cost(tiles64, 3 * kCus, 0.3, 0.5);
-    if (c256 <= c128 && c256 <= c64) return 256;
-    return c128 <= c64 ? 128 : 64;
+// Estimated time (us) of tiles of an edge with a summed length k.  A 256-wide tile has a CU to itself;
+// two workgroups of 128-wide ones or four of 64-wide ones share a CU, which hides their epilogues
+// but reads the LDS more often per product.  Fitted to BF16 products of 512^2 to 4096^2 with k of 256,
+// 1024 and 3000: a round of a tile per CU, and one that fills the CUs, take (us)
+//   256: 18 - 22, 28 - 36, 57 - 78        128: 9, 14, 36 and 10, 21, 52
+//    64: 5, 7, 22 and 8, 17, 46
+// and in between a round grows with every 256 tiles.
+double tiles_time(int edge, int64_t tiles, int64_t k) {
+    struct Fit { int per_cu; double alone, alone_k, full, full_k; };
+    const Fit f = edge == 256 ? Fit{1, 14.5, 0.018, 14.5, 0.018}
+                  : edge == 128 ? Fit{2, 6.0, 0.0098, 6.0, 0.0155} : Fit{4, 3.2, 0.006, 4.0, 0.014};
+    const double alone = f.alone + f.alone_k * (double)k, full = f.full + f.full_k * (double)k;
+    const int64_t slots = f.per_cu * kCus, left = tiles % slots;
+    double last = 0.0;
+    if (left > 0) last = f.per_cu == 1 ? alone : alone + (full - alone) * (double)(ceil_div(left, kCus) - 1) / (double)(f.per_cu - 1);
+    return (double)(tiles / slots) * full + last;
+}
+
+// The edge with the least estimated time; tiles(edge) counts the tiles.
+template <typename Tiles>
+int best_edge(int64_t k, Tiles &&tiles) {
+    int best = 256;
+    for (int e = 128; e >= 64; e /= 2)
+        if (tiles_time(e, tiles(e), k) < tiles_time(best, tiles(best), k)) best = e;
+    return best;
 }
 
 // Launches have a 32-bit number of lanes: at most this many workgroups of 256 or 512.
@@ -68,16 +79,15 @@ bool launchable(const OpPlan &p, int64_t times) {
 
 }  // namespace
 
-OpPlan op_plan(int64_t m, int64_t n, bool tb) {
+OpPlan op_plan(int64_t m, int64_t n, int64_t k, bool tb) {
     if (m <= 64 && n <= ((int64_t)1 << 22)) {
         const int fm = m <= 16 ? 1 : (m <= 32 ? 2 : 4);
         return skinny(1, n, fm, tb);
     }
-    const auto tiles = [&](int64_t e) { return ceil_div(m, e) * ceil_div(n, e); };
-    return tiled(m, n, best_edge(tiles(256), tiles(128), tiles(64)));
+    return tiled(m, n, best_edge(k, [&](int64_t e) { return ceil_div(m, e) * ceil_div(n, e); }));
 }
 
-OpPlan grouped_plan(int64_t rows, int64_t groups, int64_t n, bool tb) {
+OpPlan grouped_plan(int64_t rows, int64_t groups, int64_t n, int64_t k, bool tb) {
     const int64_t mean = ceil_div(rows, groups > 0 ? groups : 1);
     const int64_t owners = groups < rows ? groups : rows;   // an expert's last tile may be short
     if (mean <= 32 && n <= ((int64_t)1 << 22)) {
@@ -85,15 +95,13 @@ OpPlan grouped_plan(int64_t rows, int64_t groups, int64_t n, bool tb) {
         return skinny(rows / (16 * fm) + owners, n, fm, tb);
     }
     // half a tile per expert is lost on average
-    const auto tiles = [&](int64_t e) { return (rows / e + owners / 2) * ceil_div(n, e); };
-    OpPlan p = tiled(rows, n, best_edge(tiles(256), tiles(128), tiles(64)));
+    OpPlan p = tiled(rows, n, best_edge(k, [&](int64_t e) { return (rows / e + owners / 2) * ceil_div(n, e); }));
     p.tiles_m = rows / p.rows + owners;
     return p;
 }
 
-OpPlan wgrad_plan(int64_t groups, int64_t m, int64_t n) {
-    const auto tiles = [&](int64_t e) { return groups * ceil_div(m, e) * ceil_div(n, e); };
-    return tiled(m, n, best_edge(tiles(256), tiles(128), tiles(64)));
+OpPlan wgrad_plan(int64_t groups, int64_t rows, int64_t m, int64_t n) {
+    return tiled(m, n, best_edge(rows / (groups > 0 ? groups : 1), [&](int64_t e) { return groups * ceil_div(m, e) * ceil_div(n, e); }));
 }
 
 int64_t colsum_rows(int64_t groups, int64_t m) {
@@ -104,7 +112,7 @@ int64_t colsum_rows(int64_t groups, int64_t m) {
 bool ce_layout(int64_t m, int64_t n, int64_t k, bool train, CeLayout &L) {
     if (m < 0 || n < 1 || k < 0 || m > kOpMaxSize || n > kOpMaxSize || k > kOpMaxSize) return false;
     auto up = [](uint64_t v) { return (v + 255) / 256 * 256; };
-    L.logits = op_plan(m, n, true);
+    L.logits = op_plan(m, n, k, true);
     L.parts = (int)(L.logits.tiles_n * (L.logits.skinny ? 1 : 2));
     const uint64_t stats = up((uint64_t)m * (uint64_t)L.parts * 8);
     L.piece = n;
@@ -121,17 +129,30 @@ bool ce_layout(int64_t m, int64_t n, int64_t k, bool train, CeLayout &L) {
     L.pieces = ceil_div(n, most);
     L.piece = ceil_div(ceil_div(n, L.pieces), 256) * 256;
     L.pieces = ceil_div(n, L.piece);
-    L.logits = op_plan(m, L.piece, true);
-    L.dx = op_plan(m, k, false);
-    L.dw = op_plan(L.piece, k, false);
-    // dX sums over a whole piece: where its tiles do not fill the CUs the piece is cut into ranges
-    const int64_t tiles = at_least1(L.dx.tiles_m * L.dx.tiles_n);
+    L.logits = op_plan(m, L.piece, k, true);
+    L.dw = op_plan(L.piece, k, m, false);
+    // dX sums over a whole piece, which is cut into ranges where its tiles do not fill the CUs; their
+    // FP32 parts are written and read once more, at 4 TB/s.
     const int64_t have = n < L.piece ? n : L.piece;
-    int64_t splits = kCus / tiles;
-    if (splits > ceil_div(have, 512)) splits = ceil_div(have, 512);
-    if (splits > 32) splits = 32;
-    if (splits < 1) splits = 1;
-    L.k_split = ceil_div(ceil_div(have, splits), 64) * 64;
+    const int64_t most_splits = ceil_div(have, 512) < 32 ? ceil_div(have, 512) : 32;
+    L.dx = op_plan(m, k, have, false);
+    if (L.dx.skinny) {
+        const int64_t fill = 3 * kCus / at_least1(L.dx.tiles_m * L.dx.tiles_n);
+        L.splits = (int)(fill < 1 ? 1 : (fill > most_splits ? most_splits : fill));
+    } else {
+        double least = 0.0;
+        for (int e = 256; e >= 64; e /= 2)
+            for (int64_t s = 1; s <= most_splits; ++s) {
+                const double t = tiles_time(e, ceil_div(m, e) * ceil_div(k, e) * s, ceil_div(have, s)) +
+                                 (double)s * (double)m * (double)k * 8.0 / 4.0e6;
+                if (least == 0.0 || t < least) {
+                    least = t;
+                    L.dx = tiled(m, k, e);
+                    L.splits = (int)s;
+                }
+            }
+    }
+    L.k_split = ceil_div(ceil_div(have, L.splits), 64) * 64;
     L.splits = (int)ceil_div(have, L.k_split);
     L.off_weight = 0;
     L.off_scale = up((uint64_t)m * 4);
@@ -201,7 +222,7 @@ mpgemm_status_t mpgemm_check_epilogue(mpgemm_op_t transa, mpgemm_op_t transb, in
         return MPGEMM_STATUS_INVALID_VALUE;
     if (m == 0 || n == 0) return MPGEMM_STATUS_SUCCESS;
     if (!D || (k > 0 && (!A || !B)) || (read_c && !C)) return MPGEMM_STATUS_INVALID_VALUE;
-    if (m > kOpMaxSize || n > kOpMaxSize || k > kOpMaxSize || !launchable(op_plan(m, n, tb), 1)) return MPGEMM_STATUS_NOT_SUPPORTED;
+    if (m > kOpMaxSize || n > kOpMaxSize || k > kOpMaxSize || !launchable(op_plan(m, n, k, tb), 1)) return MPGEMM_STATUS_NOT_SUPPORTED;
     if ((k > 0 && (!aligned(A, 16) || !aligned(B, 16))) || !aligned(D, 16) || (read_c && !aligned(C, 16)))
         return MPGEMM_STATUS_NOT_SUPPORTED;
     if (!stride_ok(lda, 2) || !stride_ok(ldb, 2) || !stride_ok(ldd, elem_bytes(d_type)) ||
@@ -226,7 +247,7 @@ mpgemm_status_t mpgemm_check_epilogue_grad(mpgemm_op_t transa, mpgemm_op_t trans
     if (lda < at_least1(ta ? m : k) || ldb < at_least1(tb ? k : n) || ldd < at_least1(n) || (read_z && ldz < at_least1(n)))
         return MPGEMM_STATUS_INVALID_VALUE;
     if (n == 0 || (m == 0 && !dbias)) return MPGEMM_STATUS_SUCCESS;
-    if (m > kOpMaxSize || n > kOpMaxSize || k > kOpMaxSize || !launchable(op_plan(m, n, tb), 1)) return MPGEMM_STATUS_NOT_SUPPORTED;
+    if (m > kOpMaxSize || n > kOpMaxSize || k > kOpMaxSize || !launchable(op_plan(m, n, k, tb), 1)) return MPGEMM_STATUS_NOT_SUPPORTED;
     if (!aligned(dbias, 4)) return MPGEMM_STATUS_NOT_SUPPORTED;
     if (m == 0) return MPGEMM_STATUS_SUCCESS;   // (the sum of no rows is written)
     if (!D || (k > 0 && (!A || !B)) || (read_z && !Z)) return MPGEMM_STATUS_INVALID_VALUE;
@@ -248,7 +269,7 @@ mpgemm_status_t mpgemm_check_grouped(mpgemm_op_t transb, int64_t groups, int64_t
     if (lda < at_least1(k) || ldb < at_least1(tb ? k : n) || ldd < at_least1(n)) return MPGEMM_STATUS_INVALID_VALUE;
     if (groups == 0 || rows == 0 || n == 0) return MPGEMM_STATUS_SUCCESS;
     if (!D || !offsets || (k > 0 && (!A || !B))) return MPGEMM_STATUS_INVALID_VALUE;
-    if (rows > kOpMaxSize || n > kOpMaxSize || k > kOpMaxSize || groups > 65535 || !launchable(grouped_plan(rows, groups, n, tb), 1))
+    if (rows > kOpMaxSize || n > kOpMaxSize || k > kOpMaxSize || groups > 65535 || !launchable(grouped_plan(rows, groups, n, k, tb), 1))
         return MPGEMM_STATUS_NOT_SUPPORTED;
     if ((k > 0 && (!aligned(A, 16) || !aligned(B, 16))) || !aligned(D, 16) || !aligned(offsets, 4)) return MPGEMM_STATUS_NOT_SUPPORTED;
     if (!stride_ok(lda, 2) || !stride_ok(ldb, 2) || !stride_ok(ldd, elem_bytes(d_type)) || stride_b % 8 || stride_b > INT64_MAX / 131072)
@@ -285,7 +306,7 @@ mpgemm_status_t mpgemm_check_grouped_wgrad(int64_t groups, int64_t rows, int64_t
     if (lda < at_least1(m) || ldx < at_least1(n) || ldd < at_least1(n)) return MPGEMM_STATUS_INVALID_VALUE;
     if (groups == 0 || m == 0 || n == 0) return MPGEMM_STATUS_SUCCESS;
     if (!D || !offsets || (rows > 0 && (!A || !X))) return MPGEMM_STATUS_INVALID_VALUE;
-    if (rows > kOpMaxSize || m > kOpMaxSize || n > kOpMaxSize || groups > 65535 || !launchable(wgrad_plan(groups, m, n), groups))
+    if (rows > kOpMaxSize || m > kOpMaxSize || n > kOpMaxSize || groups > 65535 || !launchable(wgrad_plan(groups, rows, m, n), groups))
         return MPGEMM_STATUS_NOT_SUPPORTED;
     const int ed = elem_bytes(d_type);
     if ((rows > 0 && (!aligned(A, 16) || !aligned(X, 16))) || !aligned(D, 16) || !aligned(offsets, 4)) return MPGEMM_STATUS_NOT_SUPPORTED;
@@ -331,7 +352,7 @@ mpgemm_status_t mpgemm_check_linear_ce_grad(int64_t m, int64_t n, int64_t k, con
     CeLayout L;
     if (!ce_layout(m, n, k, true, L)) return MPGEMM_STATUS_NOT_SUPPORTED;
     if (m > 0 && (!launchable(L.logits, 1) || !launchable(L.dx, L.splits) || !launchable(L.dw, 1))) return MPGEMM_STATUS_NOT_SUPPORTED;
-    if (m == 0 && !launchable(op_plan(n, k, false), 1)) return MPGEMM_STATUS_NOT_SUPPORTED;
+    if (m == 0 && !launchable(op_plan(n, k, 0, false), 1)) return MPGEMM_STATUS_NOT_SUPPORTED;
     if (m > 0 && (!aligned(X, 16) || !aligned(W, 16) || !stride_ok(ldx, 2) || !stride_ok(ldw, 2) || !aligned(target, 8) ||
                   !aligned(lse, 4) || !aligned(grad, 4)))
         return MPGEMM_STATUS_NOT_SUPPORTED;

@@ -17,13 +17,13 @@ struct OpPlan {
     int rows, cols;   // of D per workgroup
     int64_t tiles_m, tiles_n;
 };
-// A product of m rows and n columns (splits: it may also be cut along the summed index).
-OpPlan op_plan(int64_t m, int64_t n, bool tb);
+// A product of m rows and n columns with a summed length k.
+OpPlan op_plan(int64_t m, int64_t n, int64_t k, bool tb);
 // A product of `rows` rows divided among `groups` experts; tiles_m is the most row tiles that
 // any division can take.
-OpPlan grouped_plan(int64_t rows, int64_t groups, int64_t n, bool tb);
+OpPlan grouped_plan(int64_t rows, int64_t groups, int64_t n, int64_t k, bool tb);
 // The products of each expert's rows summed: D is m x n for each.
-OpPlan wgrad_plan(int64_t groups, int64_t m, int64_t n);
+OpPlan wgrad_plan(int64_t groups, int64_t rows, int64_t m, int64_t n);
 
 // Rows of partial column sums, and their row length.
 int64_t colsum_rows(int64_t groups, int64_t m);
