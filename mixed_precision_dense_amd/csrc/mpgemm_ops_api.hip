@@ -97,10 +97,11 @@ mpgemm_status_t mpgemm_run_epilogue(mpgemm_handle_t handle, mpgemm_op_t transa, 
     if (m == 0 || n == 0) return MPGEMM_STATUS_SUCCESS;
     MPGEMM_TRY(handle_on_device(handle));
     const bool ta = transa == MPGEMM_OP_T, tb = transb == MPGEMM_OP_T;
-    const OpPlan plan = op_plan(m, n, k, tb);
+    const bool read_c = !beta_is_zero(beta, MPGEMM_R_32F);
+    const OpPlan plan = op_plan(m, n, k, tb, forward_weight(epilogue->act, epilogue->aux != nullptr, read_c));
     mpg::OpParams p = product(plan, m, n, k, *alpha, A, lda, B, ldb, D, d_type == MPGEMM_R_32F, ldd);
     set_epilogue(p, epilogue);
-    if (!beta_is_zero(beta, MPGEMM_R_32F)) {
+    if (read_c) {
         p.beta = *beta;
         p.C = C;
         p.c_f32 = c_type == MPGEMM_R_32F;
@@ -120,11 +121,21 @@ mpgemm_status_t mpgemm_run_epilogue_grad(mpgemm_handle_t handle, mpgemm_op_t tra
     if (n == 0 || (m == 0 && !dbias)) return MPGEMM_STATUS_SUCCESS;
     MPGEMM_TRY(handle_on_device(handle));
     const bool ta = transa == MPGEMM_OP_T, tb = transb == MPGEMM_OP_T;
-    const OpPlan plan = op_plan(m, n, k, tb);
+    const OpPlan plan = op_plan(m, n, k, tb, slope_weight(act));
     mpg::OpParams p = product(plan, m, n, k, *alpha, A, lda, B, ldb, D, d_type == MPGEMM_R_32F, ldd);
     set_slope(p, act, Z, ldz, dbias, workspace);
-    if (m == 0) p.tiles_m = 0;   // no rows: only their sum is written
-    else MPGEMM_TRY(launch(plan, a_type == MPGEMM_R_16BF, ta, tb, p, stream));
+    if (m == 0) {
+        p.tiles_m = 0;   // no rows: only their sum is written
+    } else {
+        // one row tile of the few rows' kernel: its partial sums are the sums
+        const bool direct = dbias && plan.skinny && plan.tiles_m == 1;
+        if (direct) {
+            p.colsum = dbias;
+            p.ld_colsum = 0;
+        }
+        MPGEMM_TRY(launch(plan, a_type == MPGEMM_R_16BF, ta, tb, p, stream));
+        if (direct) return MPGEMM_STATUS_SUCCESS;
+    }
     return dbias ? launch_dbias(plan, p, dbias, stream) : MPGEMM_STATUS_SUCCESS;
 }
 
@@ -138,7 +149,7 @@ mpgemm_status_t mpgemm_run_grouped(mpgemm_handle_t handle, mpgemm_op_t transb, i
     if (groups == 0 || rows == 0 || n == 0) return MPGEMM_STATUS_SUCCESS;
     MPGEMM_TRY(handle_on_device(handle));
     const bool tb = transb == MPGEMM_OP_T;
-    const OpPlan plan = grouped_plan(rows, groups, n, k, tb);
+    const OpPlan plan = grouped_plan(rows, groups, n, k, tb, forward_weight(epilogue->act, epilogue->aux != nullptr, false));
     mpg::OpParams p = product(plan, rows, n, k, *alpha, A, lda, B, ldb, D, d_type == MPGEMM_R_32F, ldd);
     set_epilogue(p, epilogue);
     p.groups_kind = mpg::GROUPS_ROWS;
@@ -159,7 +170,7 @@ mpgemm_status_t mpgemm_run_grouped_grad(mpgemm_handle_t handle, mpgemm_op_t tran
     if (groups == 0 || n == 0 || (rows == 0 && !dbias)) return MPGEMM_STATUS_SUCCESS;
     MPGEMM_TRY(handle_on_device(handle));
     const bool tb = transb == MPGEMM_OP_T;
-    const OpPlan plan = grouped_plan(rows, groups, n, k, tb);
+    const OpPlan plan = grouped_plan(rows, groups, n, k, tb, slope_weight(act));
     mpg::OpParams p = product(plan, rows, n, k, *alpha, A, lda, B, ldb, D, d_type == MPGEMM_R_32F, ldd);
     set_slope(p, act, Z, ldz, dbias, workspace);
     p.groups_kind = mpg::GROUPS_ROWS;
@@ -224,7 +235,7 @@ mpgemm_status_t mpgemm_run_linear_ce_grad(mpgemm_handle_t handle, int64_t m, int
     MPGEMM_TRY(handle_on_device(handle));
     const bool bf16 = type == MPGEMM_R_16BF;
     if (m == 0) {   // a sum over no rows
-        const OpPlan plan = op_plan(n, k, 0, false);
+        const OpPlan plan = op_plan(n, k, 0, false, 0.0);
         return launch(plan, bf16, true, false, product(plan, n, k, 0, 0.0f, nullptr, 8, nullptr, 8, dW, false, lddw), stream);
     }
     CeLayout L;
@@ -237,7 +248,7 @@ mpgemm_status_t mpgemm_run_linear_ce_grad(mpgemm_handle_t handle, int64_t m, int
     for (int64_t c = 0; c < L.pieces; ++c) {
         const int64_t first = c * L.piece, have = n - first < L.piece ? n - first : L.piece;
         const char *w = (const char *)W + first * ldw * 2;
-        const OpPlan lp = op_plan(m, have, k, true);
+        const OpPlan lp = op_plan(m, have, k, true, kProbsWeight);
         mpg::OpParams p = product(lp, m, have, k, *alpha, X, ldx, w, ldw, probs, false, L.piece);
         p.mode = mpg::OP_CE_PROBS;
         p.target = target;
@@ -246,7 +257,7 @@ mpgemm_status_t mpgemm_run_linear_ce_grad(mpgemm_handle_t handle, int64_t m, int
         p.col0 = (int)first;
         MPGEMM_TRY(launch(lp, bf16, false, true, p, stream));
         if (dW) {
-            const OpPlan plan = op_plan(have, k, m, false);
+            const OpPlan plan = op_plan(have, k, m, false, 0.0);
             mpg::OpParams q = product(plan, have, k, m, *alpha, probs, L.piece, X, ldx, (char *)dW + first * lddw * 2, false, lddw);
             q.scale = scale;
             MPGEMM_TRY(launch(plan, bf16, true, false, q, stream));

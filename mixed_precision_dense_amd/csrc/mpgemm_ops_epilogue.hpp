@@ -180,6 +180,13 @@ __device__ __forceinline__ void chunk_load(const OpParams &p, const OpTile &w, i
     if (MODE == OP_SLOPE && p.aux != nullptr) in.lo = *(const u32x4 *)((const uint16_t *)p.aux + row * p.ld_aux + col);
 }
 
+// What OP_CE_PROBS takes from a row: its weight, its log-sum-exp in units of log 2 and where its target
+// lies from the first of the eight columns (any other number: not among them).
+struct RowScale {
+    float weight, lse2;
+    int target;
+};
+
 // Stores eight columns, ncol of which exist.  nt: past the caches (for whole 128-byte lines).
 template <int IN>
 __device__ __forceinline__ void store8(void *base, int f32, int64_t at, int ncol, const float (&v)[8], bool nt = false) {
@@ -241,8 +248,8 @@ __device__ __forceinline__ float op_alpha(const OpParams &p) {
 // registers than a wave has).
 template <int IN, int MODE, int G, typename Row, typename Cols>
 __device__ __forceinline__ void rows_finish(const OpParams &p, float alpha, const OpTile &w, int col, bool whole, bool nt,
-                                            Row &&drow, Cols &&ncol, const ChunkIn (&in)[G], const float (&bias)[8], float (&v)[G][8],
-                                            float (&sums)[8]) {
+                                            Row &&drow, Cols &&ncol, const ChunkIn (&in)[G], const RowScale (&scale)[G],
+                                            const float (&bias)[8], float (&v)[G][8], float (&sums)[8]) {
     if constexpr (MODE == OP_SLOPE) {
         float z[G][8];
 #pragma unroll
@@ -271,25 +278,13 @@ __device__ __forceinline__ void rows_finish(const OpParams &p, float alpha, cons
             }
         }
     } else if constexpr (MODE == OP_CE_PROBS) {
-        float wt[G], lse[G];
-        int64_t t[G];
-#pragma unroll
-        for (int i = 0; i < G; ++i) {
-            wt[i] = lse[i] = 0.0f;
-            t[i] = -1;
-            if (ncol(i) > 0) {
-                wt[i] = p.weight[drow(i)];
-                lse[i] = p.lse[drow(i)];
-                t[i] = p.target[drow(i)] - p.col0 - col;
-            }
-        }
 #pragma unroll
         for (int i = 0; i < G; ++i)
 #pragma unroll
             for (int q = 0; q < 8; ++q) {
-                const float e = fast_exp2(kLog2e * __builtin_fmaf(alpha, v[i][q], -lse[i]));
+                const float e = fast_exp2(__builtin_fmaf(alpha * kLog2e, v[i][q], -scale[i].lse2));
                 // a row that does not count has weight 0: nothing of its product may reach D
-                v[i][q] = wt[i] == 0.0f ? 0.0f : (e - (t[i] == q ? 1.0f : 0.0f)) * wt[i];
+                v[i][q] = scale[i].weight == 0.0f ? 0.0f : (e - (scale[i].target == q ? 1.0f : 0.0f)) * scale[i].weight;
             }
     } else {
 #pragma unroll

@@ -28,33 +28,30 @@ OpPlan tiled(int64_t m, int64_t n, int edge) {
     return OpPlan{false, 0, 0, 0, edge, edge, ceil_div(m, edge), ceil_div(n, edge)};
 }
 
-// The kernel for few rows, tiles_m row tiles of 16 fm rows.  Columns per workgroup: with up to 16
-// rows, 64 where that still gives most CUs two workgroups (each row of A is read once for four
-// columns' blocks instead of one: 8 x 32000 x 4096, 63 -> 59 us), else as few as the storage of B
-// allows in loads of some width (16 where it is n x k, 32 where it is k x n), so that more CUs
-// read (1 x 4096 x 4096, B n x k: 9.4 us with 16 columns, 13.9 with 32).  Waves: eight, sharing k, where
-// there are at most two workgroups per CU (the same case: 9.4 us against 11.3 with four), else four,
-// whose shorter ends overlap with other workgroups' loads (64 rows of 32 experts, 1408 x 2048: 38 us
-// against 48 with eight).
-OpPlan skinny(int64_t tiles_m, int64_t n, int fm, bool tb) {
-    int w = 2;
-    if (fm == 1) w = tiles_m * ceil_div(n, 64) >= 3 * kCus / 2 ? 4 : (tb ? 1 : 2);
+// The kernel for few rows: tiles_m row tiles of 16 fm rows, columns in blocks of 16 w.  Eight waves share
+// k where there are at most two workgroups per CU (1 x 4096 x 4096: 9.4 us, 11.3 with four), else
+// four, whose shorter ends overlap with other workgroups' loads (64 rows over 32 experts, 1408 x
+// 2048: 32 us, 40 with eight).
+OpPlan skinny(int64_t tiles_m, int64_t n, int fm, int w) {
     const int64_t tiles_n = ceil_div(n, 16 * w);
-    const int waves = fm == 4 || tiles_m * tiles_n <= 2 * kCus ? 8 : 4;
+    const int waves = fm == 4 || (w < 4 && tiles_m * tiles_n <= 2 * kCus) ? 8 : 4;
     return OpPlan{true, fm, w, waves, 16 * fm, 16 * w, tiles_m, tiles_n};
 }
-// Estimated time (us) of tiles of an edge with a summed length k.  A 256-wide tile has a CU to itself;
-// two workgroups of 128-wide ones or four of 64-wide ones share a CU, which hides their epilogues
-// but reads the LDS more often per product.  Fitted to BF16 products of 512^2 to 4096^2 with k of 256,
-// 1024 and 3000: a round of a tile per CU, and one that fills the CUs, take (us)
+
+// Estimated time (us) of tiles of an edge with a summed length k and an epilogue of a weight.  A
+// 256-wide tile has a CU to itself; two workgroups of 128-wide ones or four of 64-wide ones share
+// a CU, which hides their epilogues but reads the LDS more often per product.  Fitted to BF16 products
+// of 512^2 to 4096^2 with k of 256, 1024 and 3000 (stages come in pairs of 128 k): a round of a tile per CU,
+// and one that fills the CUs, take (us)
 //   256: 18 - 22, 28 - 36, 57 - 78        128: 9, 14, 36 and 10, 21, 52
 //    64: 5, 7, 22 and 8, 17, 46
 // and in between a round grows with every 256 tiles.
-double tiles_time(int edge, int64_t tiles, int64_t k) {
-    struct Fit { int per_cu; double alone, alone_k, full, full_k; };
-    const Fit f = edge == 256 ? Fit{1, 14.5, 0.018, 14.5, 0.018}
-                  : edge == 128 ? Fit{2, 6.0, 0.0098, 6.0, 0.0155} : Fit{4, 3.2, 0.006, 4.0, 0.014};
-    const double alone = f.alone + f.alone_k * (double)k, full = f.full + f.full_k * (double)k;
+double tiles_time(int edge, int64_t tiles, int64_t k, double weight) {
+    struct Fit { int per_cu; double alone, alone_k, full, full_k, per_weight; };
+    const Fit f = edge == 256 ? Fit{1, 15.5, 0.0195, 15.5, 0.0195, 5.0}
+                  : edge == 128 ? Fit{2, 6.0, 0.0098, 6.0, 0.0155, 1.7} : Fit{4, 3.2, 0.006, 4.0, 0.014, 1.0};
+    const double kk = (double)ceil_div(k, 128) * 128.0, epilogue = f.per_weight * weight;
+    const double alone = f.alone + f.alone_k * kk + epilogue, full = f.full + f.full_k * kk + epilogue;
     const int64_t slots = f.per_cu * kCus, left = tiles % slots;
     double last = 0.0;
     if (left > 0) last = f.per_cu == 1 ? alone : alone + (full - alone) * (double)(ceil_div(left, kCus) - 1) / (double)(f.per_cu - 1);
@@ -63,10 +60,10 @@ double tiles_time(int edge, int64_t tiles, int64_t k) {
 
 // The edge with the least estimated time; tiles(edge) counts the tiles.
 template <typename Tiles>
-int best_edge(int64_t k, Tiles &&tiles) {
+int best_edge(int64_t k, double weight, Tiles &&tiles) {
     int best = 256;
     for (int e = 128; e >= 64; e /= 2)
-        if (tiles_time(e, tiles(e), k) < tiles_time(best, tiles(best), k)) best = e;
+        if (tiles_time(e, tiles(e), k, weight) < tiles_time(best, tiles(best), k, weight)) best = e;
     return best;
 }
 
@@ -79,29 +76,52 @@ bool launchable(const OpPlan &p, int64_t times) {
 
 }  // namespace
 
-OpPlan op_plan(int64_t m, int64_t n, int64_t k, bool tb) {
-    if (m <= 64 && n <= ((int64_t)1 << 22)) {
-        const int fm = m <= 16 ? 1 : (m <= 32 ? 2 : 4);
-        return skinny(1, n, fm, tb);
-    }
-    return tiled(m, n, best_edge(k, [&](int64_t e) { return ceil_div(m, e) * ceil_div(n, e); }));
+// Weights measured per 256-wide tile, in units of 5 us.
+double forward_weight(int act, bool aux, bool c) {
+    const double acts[] = {0.0, 0.0, 1.5, 0.7, 0.5};
+    return acts[act] + (aux ? 0.7 : 0.0) + (c ? 1.4 : 0.0);
+}
+double slope_weight(int act) {
+    const double acts[] = {0.0, 0.5, 2.2, 1.7, 1.2};
+    return acts[act];
 }
 
-OpPlan grouped_plan(int64_t rows, int64_t groups, int64_t n, int64_t k, bool tb) {
+// Few rows go to their own kernel as long as its workgroups are few: beyond that the tiled kernel's
+// stages stream B faster.  Measured (us, few rows' kernel / 64-wide tiles):
+//   up to 16 rows:  1 x 4096 x 4096 9.4 with 16 columns a workgroup (13.9 with 32);
+//                   8 x 32000 x 4096 57 / 61 where B is n x k and a workgroup takes 64 columns (63 with
+//                   16), 50 / 45 where B is k x n
+//   up to 32 rows:  32 x 8192 x 4096 23 / 29; 16 x 32000 x 4096 70 / 61
+//   more rows:      64 x 4096 x 4096 27 / 28; 96 x 3784 x 3320 20 / 23; 64 x 8192 x 4096 30 / 30;
+//                   64 x 117760 x 1725 185 / 96
+OpPlan op_plan(int64_t m, int64_t n, int64_t k, bool tb, double weight) {
+    const int64_t cols64 = ceil_div(n, 64);
+    if (m <= 16 && n <= ((int64_t)1 << 22) && (tb || cols64 < 384)) return skinny(1, n, 1, cols64 >= 384 ? 4 : (tb ? 1 : 2));
+    if (m <= 32 && cols64 < 384) return skinny(1, n, 2, 2);
+    if (ceil_div(m, 64) * ceil_div(n, 32) <= kCus && k >= 512) return skinny(ceil_div(m, 64), n, 4, 2);
+    return tiled(m, n, best_edge(k, weight, [&](int64_t e) { return ceil_div(m, e) * ceil_div(n, e); }));
+}
+
+// The same for experts' rows (us, few rows' kernel / best tiled one):
+//   64 rows of 32 experts, 1408 x 2048: 32 with 16 columns (41 with 64) / 46 where B is n x k,
+//   33 with 64 columns (36 with 32) / 37 where it is k x n; 256 rows: 45 / 49 and 37 / 41;
+//   512 rows: 54 / 49 and 48 / 42; 215 rows of 4 experts, 504 x 1832: 10.6 with 32 rows / 13.2
+OpPlan grouped_plan(int64_t rows, int64_t groups, int64_t n, int64_t k, bool tb, double weight) {
     const int64_t mean = ceil_div(rows, groups > 0 ? groups : 1);
     const int64_t owners = groups < rows ? groups : rows;   // an expert's last tile may be short
-    if (mean <= 32 && n <= ((int64_t)1 << 22)) {
-        const int fm = mean <= 8 ? 1 : (mean <= 20 ? 2 : 4);
-        return skinny(rows / (16 * fm) + owners, n, fm, tb);
-    }
+    const bool many = owners * ceil_div(n, 64) >= 384;
+    if (mean <= 10 && n <= ((int64_t)1 << 22))
+        return skinny(rows / 16 + owners, n, 1, many && (!tb || mean > 5) ? 4 : (tb ? 1 : 2));
+    if (mean <= 64 && (rows / 32 + owners) * ceil_div(n, 32) <= kCus) return skinny(rows / 32 + owners, n, 2, 2);
     // half a tile per expert is lost on average
-    OpPlan p = tiled(rows, n, best_edge(k, [&](int64_t e) { return (rows / e + owners / 2) * ceil_div(n, e); }));
+    OpPlan p = tiled(rows, n, best_edge(k, weight, [&](int64_t e) { return (rows / e + owners / 2) * ceil_div(n, e); }));
     p.tiles_m = rows / p.rows + owners;
     return p;
 }
 
 OpPlan wgrad_plan(int64_t groups, int64_t rows, int64_t m, int64_t n) {
-    return tiled(m, n, best_edge(rows / (groups > 0 ? groups : 1), [&](int64_t e) { return groups * ceil_div(m, e) * ceil_div(n, e); }));
+    return tiled(m, n, best_edge(rows / (groups > 0 ? groups : 1), 0.0,
+                                 [&](int64_t e) { return groups * ceil_div(m, e) * ceil_div(n, e); }));
 }
 
 int64_t colsum_rows(int64_t groups, int64_t m) {
@@ -112,7 +132,7 @@ int64_t colsum_rows(int64_t groups, int64_t m) {
 bool ce_layout(int64_t m, int64_t n, int64_t k, bool train, CeLayout &L) {
     if (m < 0 || n < 1 || k < 0 || m > kOpMaxSize || n > kOpMaxSize || k > kOpMaxSize) return false;
     auto up = [](uint64_t v) { return (v + 255) / 256 * 256; };
-    L.logits = op_plan(m, n, k, true);
+    L.logits = op_plan(m, n, k, true, kStatsWeight);
     L.parts = (int)(L.logits.tiles_n * (L.logits.skinny ? 1 : 2));
     const uint64_t stats = up((uint64_t)m * (uint64_t)L.parts * 8);
     L.piece = n;
@@ -129,13 +149,13 @@ bool ce_layout(int64_t m, int64_t n, int64_t k, bool train, CeLayout &L) {
     L.pieces = ceil_div(n, most);
     L.piece = ceil_div(ceil_div(n, L.pieces), 256) * 256;
     L.pieces = ceil_div(n, L.piece);
-    L.logits = op_plan(m, L.piece, k, true);
-    L.dw = op_plan(L.piece, k, m, false);
+    L.logits = op_plan(m, L.piece, k, true, kProbsWeight);
+    L.dw = op_plan(L.piece, k, m, false, 0.0);
     // dX sums over a whole piece, which is cut into ranges where its tiles do not fill the CUs; their
     // FP32 parts are written and read once more, at 4 TB/s.
     const int64_t have = n < L.piece ? n : L.piece;
     const int64_t most_splits = ceil_div(have, 512) < 32 ? ceil_div(have, 512) : 32;
-    L.dx = op_plan(m, k, have, false);
+    L.dx = op_plan(m, k, have, false, 1.4);
     if (L.dx.skinny) {
         const int64_t fill = 3 * kCus / at_least1(L.dx.tiles_m * L.dx.tiles_n);
         L.splits = (int)(fill < 1 ? 1 : (fill > most_splits ? most_splits : fill));
@@ -143,7 +163,7 @@ bool ce_layout(int64_t m, int64_t n, int64_t k, bool train, CeLayout &L) {
         double least = 0.0;
         for (int e = 256; e >= 64; e /= 2)
             for (int64_t s = 1; s <= most_splits; ++s) {
-                const double t = tiles_time(e, ceil_div(m, e) * ceil_div(k, e) * s, ceil_div(have, s)) +
+                const double t = tiles_time(e, ceil_div(m, e) * ceil_div(k, e) * s, ceil_div(have, s), 1.4) +
                                  (double)s * (double)m * (double)k * 8.0 / 4.0e6;
                 if (least == 0.0 || t < least) {
                     least = t;
@@ -222,7 +242,8 @@ mpgemm_status_t mpgemm_check_epilogue(mpgemm_op_t transa, mpgemm_op_t transb, in
         return MPGEMM_STATUS_INVALID_VALUE;
     if (m == 0 || n == 0) return MPGEMM_STATUS_SUCCESS;
     if (!D || (k > 0 && (!A || !B)) || (read_c && !C)) return MPGEMM_STATUS_INVALID_VALUE;
-    if (m > kOpMaxSize || n > kOpMaxSize || k > kOpMaxSize || !launchable(op_plan(m, n, k, tb), 1)) return MPGEMM_STATUS_NOT_SUPPORTED;
+    if (m > kOpMaxSize || n > kOpMaxSize || k > kOpMaxSize || !launchable(op_plan(m, n, k, tb, forward_weight(epilogue->act, epilogue->aux != nullptr, read_c)), 1))
+        return MPGEMM_STATUS_NOT_SUPPORTED;
     if ((k > 0 && (!aligned(A, 16) || !aligned(B, 16))) || !aligned(D, 16) || (read_c && !aligned(C, 16)))
         return MPGEMM_STATUS_NOT_SUPPORTED;
     if (!stride_ok(lda, 2) || !stride_ok(ldb, 2) || !stride_ok(ldd, elem_bytes(d_type)) ||
@@ -247,7 +268,8 @@ mpgemm_status_t mpgemm_check_epilogue_grad(mpgemm_op_t transa, mpgemm_op_t trans
     if (lda < at_least1(ta ? m : k) || ldb < at_least1(tb ? k : n) || ldd < at_least1(n) || (read_z && ldz < at_least1(n)))
         return MPGEMM_STATUS_INVALID_VALUE;
     if (n == 0 || (m == 0 && !dbias)) return MPGEMM_STATUS_SUCCESS;
-    if (m > kOpMaxSize || n > kOpMaxSize || k > kOpMaxSize || !launchable(op_plan(m, n, k, tb), 1)) return MPGEMM_STATUS_NOT_SUPPORTED;
+    if (m > kOpMaxSize || n > kOpMaxSize || k > kOpMaxSize || !launchable(op_plan(m, n, k, tb, slope_weight(act)), 1))
+        return MPGEMM_STATUS_NOT_SUPPORTED;
     if (!aligned(dbias, 4)) return MPGEMM_STATUS_NOT_SUPPORTED;
     if (m == 0) return MPGEMM_STATUS_SUCCESS;   // (the sum of no rows is written)
     if (!D || (k > 0 && (!A || !B)) || (read_z && !Z)) return MPGEMM_STATUS_INVALID_VALUE;
@@ -269,7 +291,8 @@ mpgemm_status_t mpgemm_check_grouped(mpgemm_op_t transb, int64_t groups, int64_t
     if (lda < at_least1(k) || ldb < at_least1(tb ? k : n) || ldd < at_least1(n)) return MPGEMM_STATUS_INVALID_VALUE;
     if (groups == 0 || rows == 0 || n == 0) return MPGEMM_STATUS_SUCCESS;
     if (!D || !offsets || (k > 0 && (!A || !B))) return MPGEMM_STATUS_INVALID_VALUE;
-    if (rows > kOpMaxSize || n > kOpMaxSize || k > kOpMaxSize || groups > 65535 || !launchable(grouped_plan(rows, groups, n, k, tb), 1))
+    if (rows > kOpMaxSize || n > kOpMaxSize || k > kOpMaxSize || groups > 65535 || 
+        !launchable(grouped_plan(rows, groups, n, k, tb, forward_weight(epilogue->act, epilogue->aux != nullptr, false)), 1))
         return MPGEMM_STATUS_NOT_SUPPORTED;
     if ((k > 0 && (!aligned(A, 16) || !aligned(B, 16))) || !aligned(D, 16) || !aligned(offsets, 4)) return MPGEMM_STATUS_NOT_SUPPORTED;
     if (!stride_ok(lda, 2) || !stride_ok(ldb, 2) || !stride_ok(ldd, elem_bytes(d_type)) || stride_b % 8 || stride_b > INT64_MAX / 131072)
@@ -294,6 +317,7 @@ mpgemm_status_t mpgemm_check_grouped_grad(mpgemm_op_t transb, int64_t groups, in
     if (rows == 0) return offsets ? MPGEMM_STATUS_SUCCESS : MPGEMM_STATUS_INVALID_VALUE;
     if (read_z && !Z) return MPGEMM_STATUS_INVALID_VALUE;
     if (read_z && (!aligned(Z, 16) || !stride_ok(ldz, 2))) return MPGEMM_STATUS_NOT_SUPPORTED;
+    if (!launchable(grouped_plan(rows, groups, n, k, transb == MPGEMM_OP_T, slope_weight(act)), 1)) return MPGEMM_STATUS_NOT_SUPPORTED;
     return dbias ? check_workspace(workspace, workspace_bytes, mpgemm_epilogue_grad_workspace_size(groups, rows, n)) : MPGEMM_STATUS_SUCCESS;
 }
 
@@ -352,7 +376,7 @@ mpgemm_status_t mpgemm_check_linear_ce_grad(int64_t m, int64_t n, int64_t k, con
     CeLayout L;
     if (!ce_layout(m, n, k, true, L)) return MPGEMM_STATUS_NOT_SUPPORTED;
     if (m > 0 && (!launchable(L.logits, 1) || !launchable(L.dx, L.splits) || !launchable(L.dw, 1))) return MPGEMM_STATUS_NOT_SUPPORTED;
-    if (m == 0 && !launchable(op_plan(n, k, 0, false), 1)) return MPGEMM_STATUS_NOT_SUPPORTED;
+    if (m == 0 && !launchable(op_plan(n, k, 0, false, 0.0), 1)) return MPGEMM_STATUS_NOT_SUPPORTED;
     if (m > 0 && (!aligned(X, 16) || !aligned(W, 16) || !stride_ok(ldx, 2) || !stride_ok(ldw, 2) || !aligned(target, 8) ||
                   !aligned(lse, 4) || !aligned(grad, 4)))
         return MPGEMM_STATUS_NOT_SUPPORTED;

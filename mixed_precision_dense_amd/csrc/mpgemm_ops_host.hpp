@@ -17,11 +17,15 @@ struct OpPlan {
     int rows, cols;   // of D per workgroup
     int64_t tiles_m, tiles_n;
 };
+// How much an epilogue adds to a tile's time, for the rules below.
+double forward_weight(int act, bool aux, bool c);
+double slope_weight(int act);
+constexpr double kStatsWeight = 0.7, kProbsWeight = 1.0;
 // A product of m rows and n columns with a summed length k.
-OpPlan op_plan(int64_t m, int64_t n, int64_t k, bool tb);
+OpPlan op_plan(int64_t m, int64_t n, int64_t k, bool tb, double weight);
 // A product of `rows` rows divided among `groups` experts; tiles_m is the most row tiles that
 // any division can take.
-OpPlan grouped_plan(int64_t rows, int64_t groups, int64_t n, int64_t k, bool tb);
+OpPlan grouped_plan(int64_t rows, int64_t groups, int64_t n, int64_t k, bool tb, double weight);
 // The products of each expert's rows summed: D is m x n for each.
 OpPlan wgrad_plan(int64_t groups, int64_t rows, int64_t m, int64_t n);
 

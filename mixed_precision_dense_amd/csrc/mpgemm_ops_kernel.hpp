@@ -98,6 +98,29 @@ __device__ __forceinline__ void op_store_tile(const OpParams &p, const OpTile &w
         wait_vmem<0>();
         for (int i = 0; i < depth; ++i) fetch(i);
     }
+    // Row factors of the cross entropy's probabilities, read once per tile into the ring's place: weight,
+    // log-sum-exp (in units of log 2) and the target's column.
+    struct RowFactor {
+        float weight, lse;
+        int target, pad;
+    };
+    typedef __attribute__((address_space(3))) RowFactor lds_factor;
+    static_assert(WR * (int)sizeof(RowFactor) <= kRing, "row factors fit the ring");
+    if constexpr (MODE == OP_CE_PROBS) {
+        for (int r = lane; r < WR; r += 64) {
+            RowFactor f = {0.0f, 0.0f, -1, 0};
+            if (row_t + r < w.m) {
+                f.weight = p.weight[row_t + r];
+                f.lse = p.lse[row_t + r] * kLog2e;
+                const int64_t t = p.target[row_t + r] - p.col0;
+                f.target = t >= 0 && t < p.n ? (int)t : -1;
+            }
+            lds_factor *to = (lds_factor *)(ring + r * (int)sizeof(RowFactor));
+            to->weight = f.weight;
+            to->lse = f.lse;
+            to->target = f.target;
+        }
+    }
     // Operations that may be in flight when a group's loads have landed: the loads of the groups
     // after it and, in a whole tile (where none is masked off), the stores since.
     const int stores = full && loads > 0 ? G * ((p.d_f32 ? 2 : 1) + (MODE == OP_FORWARD && p.aux != nullptr ? 1 : 0)) : 0;
@@ -147,10 +170,19 @@ __device__ __forceinline__ void op_store_tile(const OpParams &p, const OpTile &w
                     if (wide) in[q].hi = *(const lds_u32x4 *)(at + (q * loads + 1) * 1024);
                 }
             }
+            RowScale scale[G];
+            if constexpr (MODE == OP_CE_PROBS) {
+#pragma unroll
+                for (int q = 0; q < G; ++q) {
+                    const lds_factor *f =
+                        (const lds_factor *)(ring + ((pass * kSteps + s + q) * RI + rr) * (int)sizeof(RowFactor));
+                    scale[q] = RowScale{f->weight, f->lse, f->target - col};
+                }
+            }
             const int row_s = row_t + (pass * kSteps + s) * RI + rr;
             rows_finish<IN, MODE, G>(
                 p, alpha, w, col, full, nt, [&](int q) { return (int64_t)w.row0 + row_s + q * RI; },
-                [&](int q) { return cols_of(row_s + q * RI); }, in, bias, v, sums);
+                [&](int q) { return cols_of(row_s + q * RI); }, in, scale, bias, v, sums);
             if (loads > 0 && group + depth < kGroups) {
                 wait_lds<0>();                     // the group's place has been read
                 fetch(group + depth);

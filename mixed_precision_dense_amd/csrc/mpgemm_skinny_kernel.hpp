@@ -131,15 +131,20 @@ void skinny_kernel(OpParams p) {
                 for (int j = 0; j < W; ++j) acc[i][j] = mfma32<IN>(fa[i], fb[j], acc[i][j]);
         }
     };
-    // blocks wave, wave + NWV, ...: one is multiplied while the next is on its way
+    // Blocks wave, wave + NWV, ... of an order that starts at another block in every column tile: one
+    // is multiplied while the next is on its way.  (Where the columns' rows lie a power of two apart,
+    // workgroups that all read the same k at a time would crowd the same memory channels: 8 x 32000 x
+    // 4096 in 60 us from block 0, 57 so.)
     const int nb = (w.k + 32 * UN - 1) / (32 * UN);
+    const int first = TB && nb > 0 ? (int)((unsigned)w.tn * 37u % (unsigned)nb) : 0;
+    auto block = [&](int b) { return b + first < nb ? b + first : b + first - nb; };
     int b = wave;
-    if (b < nb) load(blk[0], b);
+    if (b < nb) load(blk[0], block(b));
     for (; b < nb; b += 2 * NWV) {
-        if (b + NWV < nb) load(blk[1], b + NWV);
-        multiply(blk[0], b);
-        if (b + 2 * NWV < nb) load(blk[0], b + 2 * NWV);
-        if (b + NWV < nb) multiply(blk[1], b + NWV);
+        if (b + NWV < nb) load(blk[1], block(b + NWV));
+        multiply(blk[0], block(b));
+        if (b + 2 * NWV < nb) load(blk[0], block(b + 2 * NWV));
+        if (b + NWV < nb) multiply(blk[1], block(b + NWV));
     }
 
     const int g = lane / 16, u = lane % 16;
@@ -199,8 +204,13 @@ void skinny_kernel(OpParams p) {
             ChunkIn in[1];
             chunk_load<MODE>(p, w, drow, col, ncol, in[0]);
             bias_load<IN, MODE>(p, w.expert, col, bias);
+            RowScale scale[1];
+            if constexpr (MODE == OP_CE_PROBS) {
+                const int64_t t = p.target[drow] - p.col0 - col;
+                scale[0] = RowScale{p.weight[drow], p.lse[drow] * kLog2e, t >= 0 && t < 8 ? (int)t : -1};
+            }
             rows_finish<IN, MODE, 1>(p, alpha, w, col, false, false, [&](int) { return drow; }, [&](int) { return ncol; }, in,
-                                     bias, v, sums);
+                                     scale, bias, v, sums);
         };
         if (p.mode == OP_SLOPE)
             finish(std::integral_constant<int, OP_SLOPE>{});
@@ -210,17 +220,23 @@ void skinny_kernel(OpParams p) {
             finish(std::integral_constant<int, OP_FORWARD>{});
     }
     if (p.colsum != nullptr) {
-        // the rows' shares in the LDS (the partial sums have been read), then one thread a column
-        __syncthreads();
-        float *stage = &part[0][0][0];
-        if (mine)
+        // the rows of a wave by lane exchanges, the waves through the LDS (its partial sums have been read)
 #pragma unroll
-            for (int q = 0; q < 8; ++q) stage[row * BN + 8 * c + q] = sums[q];
+        for (int d = CH; d < 64; d *= 2)
+#pragma unroll
+            for (int q = 0; q < 8; ++q) sums[q] += __shfl_xor(sums[q], d, 64);
+        constexpr int kRowWaves = (BM * CH + 63) / 64;
+        float *stage = &part[0][0][0];
+        __syncthreads();
+        if (wave < kRowWaves && lane < CH)
+#pragma unroll
+            for (int q = 0; q < 8; ++q) stage[wave * BN + 8 * c + q] = sums[q];
         __syncthreads();
         const int at = w.tn * BN + (int)threadIdx.x;
         if (threadIdx.x < BN && at < p.n && w.tile < p.tiles_m) {
             float s = 0.0f;
-            for (int r = 0; r < BM; ++r) s += stage[r * BN + threadIdx.x];
+#pragma unroll
+            for (int r = 0; r < kRowWaves; ++r) s += stage[r * BN + threadIdx.x];
             p.colsum[(int64_t)w.tile * p.ld_colsum + at] = s;
         }
     }
