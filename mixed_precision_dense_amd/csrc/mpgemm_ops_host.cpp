@@ -92,13 +92,14 @@ double slope_weight(int act) {
 //                   8 x 32000 x 4096 57 / 61 where B is n x k and a workgroup takes 64 columns (63 with
 //                   16), 50 / 45 where B is k x n
 //   up to 32 rows:  32 x 8192 x 4096 23 / 29; 16 x 32000 x 4096 70 / 61
-//   more rows:      64 x 4096 x 4096 27 / 28; 96 x 3784 x 3320 20 / 23; 64 x 8192 x 4096 30 / 30;
+//   up to 64 rows:  37 x 5000 x 1001 7.4 / 8.4; 64 x 4096 x 4096 27 / 28; 64 x 8192 x 4096 30 / 30;
 //                   64 x 117760 x 1725 185 / 96
+//   more rows:      108 x 751 x 1408 10 / 6
 OpPlan op_plan(int64_t m, int64_t n, int64_t k, bool tb, double weight) {
     const int64_t cols64 = ceil_div(n, 64);
     if (m <= 16 && n <= ((int64_t)1 << 22) && (tb || cols64 < 384)) return skinny(1, n, 1, cols64 >= 384 ? 4 : (tb ? 1 : 2));
     if (m <= 32 && cols64 < 384) return skinny(1, n, 2, 2);
-    if (ceil_div(m, 64) * ceil_div(n, 32) <= kCus && k >= 512) return skinny(ceil_div(m, 64), n, 4, 2);
+    if (m <= 64 && ceil_div(n, 32) <= kCus) return skinny(1, n, 4, 2);
     return tiled(m, n, best_edge(k, weight, [&](int64_t e) { return ceil_div(m, e) * ceil_div(n, e); }));
 }
 
