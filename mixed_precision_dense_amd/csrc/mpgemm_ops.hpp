@@ -60,6 +60,8 @@ struct OpParams {
     int splits, k_split;         // the summed index in `splits` ranges of k_split, each with its D
     int64_t stride_split;        // elements between two ranges' D
     const float *scale;          // device factor of alpha, or nullptr
+    const int *count;            // device count of the rows (count_k: of the summed index) that take
+    int count_k;                 // part, at most m (k); nullptr: all of them
     // cross entropy
     const int64_t *target;
     const float *lse, *weight;
@@ -84,11 +86,23 @@ int launch_colsum(const OpParams &p, int tile_rows, int rows_per_tile, float *db
 int launch_ce_merge(bool bf16, const CeStat *stats, int parts, int m, int n, int k, float alpha,
                     const void *X, int64_t ldx, const void *W, int64_t ldw, const int64_t *target,
                     float *loss, float *lse, void *stream);
-// per-row weights (0 where the target does not count) over a common factor, which goes to scale[0]
-int launch_ce_weights(bool bf16, int m, int n, const int64_t *target, const float *grad, float *weight,
-                      float *scale, void *stream);
-// out (rows x cols, 16 bit) = alpha * scale[0] * sum of `splits` FP32 parts
-int launch_sum_parts(bool bf16, const float *parts, int splits, int64_t stride, int64_t ld_part, int rows,
+// What the cross entropy's gradient takes from its rows, m entries each.
+struct CeRows {
+    float *weight, *lse;   // of a row; weight 0: its target does not count
+    int64_t *target;
+    int *source, *place;   // nullptr: rows stay where they are.  Else only those that count are listed:
+                           // entry j is row source[j], row r is entry place[r] (-1: none)
+    float *scale;          // one factor common to the weights
+    int *count;            // number of entries
+};
+int launch_ce_rows(bool bf16, int m, int n, const int64_t *target, const float *lse, const float *grad, const CeRows &rows,
+                   void *stream);
+// out row j (16-byte blocks, ld_out) = in row source[j], for count[0] rows of at most m
+int launch_gather_rows(const void *in, int64_t ld_in, const int *source, const int *count, int m, int k, void *out, int64_t ld_out,
+                       void *stream);
+// out (rows x cols, 16 bit) = alpha * scale[0] * sum of `splits` FP32 parts; with place, row r's are in
+// row place[r], and a row without one is 0
+int launch_sum_parts(bool bf16, const float *parts, int splits, int64_t stride, int64_t ld_part, const int *place, int rows,
                      int cols, float alpha, const float *scale, void *out, int64_t ld_out, void *stream);
 
 }  // namespace mpg

@@ -241,25 +241,40 @@ mpgemm_status_t mpgemm_run_linear_ce_grad(mpgemm_handle_t handle, int64_t m, int
     CeLayout L;
     if (!ce_layout(m, n, k, true, L)) return MPGEMM_STATUS_INTERNAL_ERROR;   // checked above
     char *ws = (char *)workspace;
-    float *weight = (float *)(ws + L.off_weight), *scale = (float *)(ws + L.off_scale), *part = (float *)(ws + L.off_dx);
+    mpg::CeRows rows = {(float *)ws, (float *)(ws + L.off_lse), (int64_t *)(ws + L.off_target), nullptr, nullptr,
+                        (float *)(ws + L.off_scale), (int *)(ws + L.off_scale) + 1};
+    if (L.listed) {
+        rows.source = (int *)(ws + L.off_source);
+        rows.place = (int *)(ws + L.off_place);
+    }
+    float *part = (float *)(ws + L.off_dx);
     void *probs = ws + L.off_probs;
     const int64_t ld_part = round8(k);
-    MPGEMM_TRY(queued(mpg::launch_ce_weights(bf16, (int)m, (int)n, target, grad, weight, scale, stream)));
+    MPGEMM_TRY(queued(mpg::launch_ce_rows(bf16, (int)m, (int)n, target, lse, grad, rows, stream)));
+    const int *count = L.listed ? rows.count : nullptr;
+    if (L.listed) {   // from here on X is its rows that count
+        MPGEMM_TRY(queued(mpg::launch_gather_rows(X, ldx, rows.source, rows.count, (int)m, (int)k, ws + L.off_x, round8(k), stream)));
+        X = ws + L.off_x;
+        ldx = round8(k);
+    }
     for (int64_t c = 0; c < L.pieces; ++c) {
         const int64_t first = c * L.piece, have = n - first < L.piece ? n - first : L.piece;
         const char *w = (const char *)W + first * ldw * 2;
         const OpPlan lp = op_plan(m, have, k, true, kProbsWeight);
         mpg::OpParams p = product(lp, m, have, k, *alpha, X, ldx, w, ldw, probs, false, L.piece);
         p.mode = mpg::OP_CE_PROBS;
-        p.target = target;
-        p.lse = lse;
-        p.weight = weight;
+        p.target = rows.target;
+        p.lse = rows.lse;
+        p.weight = rows.weight;
+        p.count = count;
         p.col0 = (int)first;
         MPGEMM_TRY(launch(lp, bf16, false, true, p, stream));
         if (dW) {
             const OpPlan plan = op_plan(have, k, m, false, 0.0);
             mpg::OpParams q = product(plan, have, k, m, *alpha, probs, L.piece, X, ldx, (char *)dW + first * lddw * 2, false, lddw);
-            q.scale = scale;
+            q.scale = rows.scale;
+            q.count = count;
+            q.count_k = 1;
             MPGEMM_TRY(launch(plan, bf16, true, false, q, stream));
         }
         if (dX) {
@@ -267,6 +282,7 @@ mpgemm_status_t mpgemm_run_linear_ce_grad(mpgemm_handle_t handle, int64_t m, int
             q.splits = (int)((have + L.k_split - 1) / L.k_split);
             q.k_split = (int)L.k_split;
             q.stride_split = m * ld_part;
+            q.count = count;
             if (c > 0) {   // added to what the pieces before have summed
                 q.beta = 1.0f;
                 q.C = part;
@@ -277,7 +293,8 @@ mpgemm_status_t mpgemm_run_linear_ce_grad(mpgemm_handle_t handle, int64_t m, int
         }
     }
     if (!dX) return MPGEMM_STATUS_SUCCESS;
-    return queued(mpg::launch_sum_parts(bf16, part, L.splits, m * ld_part, ld_part, (int)m, (int)k, *alpha, scale, dX, lddx, stream));
+    return queued(mpg::launch_sum_parts(bf16, part, L.splits, m * ld_part, ld_part, rows.place, (int)m, (int)k, *alpha, rows.scale, dX,
+                                        lddx, stream));
 }
 
 }  // extern "C"

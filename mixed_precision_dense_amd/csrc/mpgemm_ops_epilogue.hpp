@@ -441,6 +441,15 @@ __device__ __forceinline__ bool locate(const OpParams &p, int wg, int split, int
     }
     tile_coords(wg, p.tiles_m, p.tiles_n, w.tm, w.tn);
     w.tile = w.tm;
+    if (p.count != nullptr) {
+        const int count = max(uniform(p.count[0]), 0);
+        if (p.count_k) {
+            w.k = min(p.k, count);
+        } else {
+            w.m = min(p.m, count);
+            if (w.tm * BM >= w.m) return false;
+        }
+    }
     if (p.splits > 1) {
         w.k = min(p.k_split, p.k - split * p.k_split);
         w.d_off = (int64_t)split * p.stride_split;

@@ -140,7 +140,8 @@ bool ce_layout(int64_t m, int64_t n, int64_t k, bool train, CeLayout &L) {
     L.pieces = 1;
     L.splits = 1;
     L.k_split = n;
-    L.off_weight = L.off_scale = L.off_probs = L.off_dx = 0;
+    L.listed = false;
+    L.off_lse = L.off_target = L.off_source = L.off_place = L.off_scale = L.off_x = L.off_probs = L.off_dx = 0;
     L.total = stats;
     if (!train || m == 0) return true;
     // Probabilities of one piece at a time, at most 128 MiB of them (or 256 columns): half of the
@@ -175,10 +176,17 @@ bool ce_layout(int64_t m, int64_t n, int64_t k, bool train, CeLayout &L) {
     }
     L.k_split = ceil_div(ceil_div(have, L.splits), 64) * 64;
     L.splits = (int)ceil_div(have, L.k_split);
-    L.off_weight = 0;
-    L.off_scale = up((uint64_t)m * 4);
-    L.off_probs = L.off_scale + 256;
-    L.off_dx = L.off_probs + up((uint64_t)m * (uint64_t)L.piece * 2);
+    // (fewer rows than two tiles: nothing to win)
+    L.listed = m >= 512;
+    const uint64_t rows = (uint64_t)m, row_x = L.listed ? (uint64_t)round8(k) * 2 : 0;
+    L.off_lse = up(rows * 4);
+    L.off_target = L.off_lse + up(rows * 4);
+    L.off_source = L.off_target + up(rows * 8);
+    L.off_place = L.off_source + (L.listed ? up(rows * 4) : 0);
+    L.off_scale = L.off_place + (L.listed ? up(rows * 4) : 0);
+    L.off_x = L.off_scale + 256;
+    L.off_probs = L.off_x + up(rows * row_x);
+    L.off_dx = L.off_probs + up(rows * (uint64_t)L.piece * 2);
     const unsigned __int128 total = (unsigned __int128)L.off_dx + (unsigned __int128)L.splits * (uint64_t)m * (uint64_t)round8(k) * 4;
     if (total > ((unsigned __int128)1 << 62)) return false;
     L.total = (uint64_t)total > stats ? (uint64_t)total : stats;

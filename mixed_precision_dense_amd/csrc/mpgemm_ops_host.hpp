@@ -40,7 +40,11 @@ struct CeLayout {
     OpPlan dx, dw;
     int splits;               // of the piece, in dX's product
     int64_t k_split;
-    uint64_t off_weight, off_scale, off_probs, off_dx, total;   // bytes; statistics and probabilities share offset 0 onwards
+    // Gradients of many rows first list those whose target counts and gather their X, so that rows
+    // that do not (padding, a prompt) cost nothing in the products.
+    bool listed;
+    uint64_t off_lse, off_target, off_source, off_place, off_scale, off_x, off_probs, off_dx;   // bytes; weights at 0
+    uint64_t total;           // also covers the row statistics of the forward pass, which start at 0
 };
 bool ce_layout(int64_t m, int64_t n, int64_t k, bool train, CeLayout &L);
 

@@ -104,33 +104,73 @@ __global__ __launch_bounds__(kMergeThreads) void ce_merge_kernel(const CeStat *s
 // weights, a mean's, the largest entries of P, a target's p - 1, then start from a power of two:
 // times 1 / rows they would all be rounded the same way, an error of up to half a step that no
 // summation averages out (relative error of dX and dW in BF16 0.0034 where it is now 0.0017).
-constexpr int kWeightThreads = 1024;
-__global__ __launch_bounds__(kWeightThreads) void ce_weights_kernel(int bf16, int m, int n, const int64_t *target, const float *grad,
-                                                                    float *weight, float *scale) {
-    __shared__ float most[kWeightThreads / 64];
+//
+// With lists (rows.source), the rows that count are also numbered in their order, so that the products
+// after this one take only them; their number stays on the device.
+constexpr int kRowThreads = 1024;
+__global__ __launch_bounds__(kRowThreads) void ce_rows_kernel(int bf16, int m, int n, const int64_t *target, const float *lse,
+                                                              const float *grad, CeRows rows) {
+    __shared__ float most[kRowThreads / 64];
+    __shared__ int found[kRowThreads / 64];
+    const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
     float a = 0.0f;
-    for (int r = threadIdx.x; r < m; r += kWeightThreads) {
+    for (int r = threadIdx.x; r < m; r += kRowThreads) {
         const int64_t t = target[r];
         if (t >= 0 && t < n) a = fmaxf(a, __builtin_fabsf(grad[r]));
     }
 #pragma unroll
     for (int d = 1; d < 64; d *= 2) a = fmaxf(a, __shfl_xor(a, d, 64));
-    if (threadIdx.x % 64 == 0) most[threadIdx.x / 64] = a;
+    if (lane == 0) most[wave] = a;
     __syncthreads();
-    for (int i = 0; i < kWeightThreads / 64; ++i) a = fmaxf(a, most[i]);
+    for (int i = 0; i < kRowThreads / 64; ++i) a = fmaxf(a, most[i]);
     const bool usable = a > 0.0f && a < __builtin_inff();   // (else the weights stay as they are)
     const float top = usable && !bf16 ? 8192.0f : 1.0f;
-    for (int r = threadIdx.x; r < m; r += kWeightThreads) {
-        const int64_t t = target[r];
-        const float g = t >= 0 && t < n ? grad[r] : 0.0f;
-        weight[r] = usable ? g / a * top : g;
+    if (threadIdx.x == 0) rows.scale[0] = usable ? a / top : 1.0f;
+    int before = 0;                                         // entries of the rows before this turn's
+    for (int base = 0; base < m; base += kRowThreads) {     // (the same number of turns for every wave)
+        const int r = base + (int)threadIdx.x;
+        const int64_t t = r < m ? target[r] : -1;
+        const bool counts = t >= 0 && t < n;
+        const float g = counts ? grad[r] : 0.0f;
+        const float weight = usable ? g / a * top : g;
+        int at = r;
+        if (rows.source != nullptr) {
+            const uint64_t mask = __ballot(counts);
+            if (lane == 0) found[wave] = __popcll(mask);
+            __syncthreads();
+            int sum = 0, own = 0;
+            for (int i = 0; i < kRowThreads / 64; ++i) {
+                if (i == wave) own = sum;
+                sum += found[i];
+            }
+            at = before + own + __popcll(mask & (((uint64_t)1 << lane) - 1));
+            before += sum;
+            __syncthreads();                                // found is written again in the next turn
+            if (r < m) rows.place[r] = counts ? at : -1;
+            if (counts) rows.source[at] = r;
+        }
+        if (r < m && (counts || rows.source == nullptr)) {
+            rows.weight[at] = weight;
+            rows.lse[at] = lse[r];
+            rows.target[at] = t;
+        }
     }
-    if (threadIdx.x == 0) scale[0] = usable ? a / top : 1.0f;
+    if (threadIdx.x == 0) rows.count[0] = rows.source != nullptr ? before : m;
+}
+
+// One thread per 16-byte block of a listed row.
+__global__ __launch_bounds__(256) void gather_rows_kernel(const uint16_t *in, int64_t ld_in, const int *source, const int *count,
+                                                          int m, int blocks, uint16_t *out, int64_t ld_out) {
+    const int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int64_t j = t / blocks;
+    if (j >= min(count[0], m)) return;
+    const int64_t at = (t - j * blocks) * 8;
+    *(u32x4 *)(out + j * ld_out + at) = *(const u32x4 *)(in + source[j] * ld_in + at);
 }
 
 template <int IN>
 __global__ __launch_bounds__(256) void sum_parts_kernel(const float *parts, int splits, int64_t stride, int64_t ld_part,
-                                                        int rows, int cols, float alpha, const float *scale, uint16_t *out,
+                                                        const int *place, int rows, int cols, float alpha, const float *scale, uint16_t *out,
                                                         int64_t ld_out) {
     const int64_t chunks = ((int64_t)cols + 7) / 8;
     const int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x;
@@ -140,7 +180,9 @@ __global__ __launch_bounds__(256) void sum_parts_kernel(const float *parts, int 
     float v[8];
 #pragma unroll
     for (int q = 0; q < 8; ++q) v[q] = 0.0f;
-    const float *at = parts + row * ld_part + col;   // (rows of whole 8-column blocks)
+    const int64_t from = place != nullptr ? place[row] : row;
+    if (from < 0) splits = 0;
+    const float *at = parts + from * ld_part + col;   // (rows of whole 8-column blocks)
     for (int s = 0; s < splits; ++s, at += stride) {
         const f32x4 a = *(const f32x4 *)at, b = *(const f32x4 *)(at + 4);
 #pragma unroll
@@ -180,17 +222,27 @@ int launch_ce_merge(bool bf16, const CeStat *stats, int parts, int m, int n, int
                      m, kMergeThreads, args, stream);
 }
 
-int launch_ce_weights(bool bf16, int m, int n, const int64_t *target, const float *grad, float *weight, float *scale,
-                      void *stream) {
+int launch_ce_rows(bool bf16, int m, int n, const int64_t *target, const float *lse, const float *grad, const CeRows &rows,
+                   void *stream) {
     int b = bf16 ? 1 : 0;
-    void *args[] = {&b, &m, &n, &target, &grad, &weight, &scale};
-    return launch_1d(reinterpret_cast<const void *>(&ce_weights_kernel), 1, kWeightThreads, args, stream);
+    CeRows r = rows;
+    void *args[] = {&b, &m, &n, &target, &lse, &grad, &r};
+    return launch_1d(reinterpret_cast<const void *>(&ce_rows_kernel), 1, kRowThreads, args, stream);
 }
 
-int launch_sum_parts(bool bf16, const float *parts, int splits, int64_t stride, int64_t ld_part, int rows, int cols, float alpha,
-                     const float *scale, void *out, int64_t ld_out, void *stream) {
+int launch_gather_rows(const void *in, int64_t ld_in, const int *source, const int *count, int m, int k, void *out, int64_t ld_out,
+                       void *stream) {
+    const uint16_t *from = (const uint16_t *)in;
+    uint16_t *to = (uint16_t *)out;
+    int blocks = (k + 7) / 8;
+    void *args[] = {&from, &ld_in, &source, &count, &m, &blocks, &to, &ld_out};
+    return launch_1d(reinterpret_cast<const void *>(&gather_rows_kernel), ((int64_t)m * blocks + 255) / 256, 256, args, stream);
+}
+
+int launch_sum_parts(bool bf16, const float *parts, int splits, int64_t stride, int64_t ld_part, const int *place, int rows, int cols,
+                     float alpha, const float *scale, void *out, int64_t ld_out, void *stream) {
     uint16_t *o = (uint16_t *)out;
-    void *args[] = {&parts, &splits, &stride, &ld_part, &rows, &cols, &alpha, &scale, &o, &ld_out};
+    void *args[] = {&parts, &splits, &stride, &ld_part, &place, &rows, &cols, &alpha, &scale, &o, &ld_out};
     const int64_t blocks = ((int64_t)rows * (((int64_t)cols + 7) / 8) + 255) / 256;
     return launch_1d(bf16 ? reinterpret_cast<const void *>(&sum_parts_kernel<IN_BF16>)
                           : reinterpret_cast<const void *>(&sum_parts_kernel<IN_F16>),

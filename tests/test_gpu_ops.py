@@ -362,6 +362,13 @@ def test_linear_ce_counting_rows(m, ignored):
     run_ce(m, 90, 48, "f16", alpha=0.5, ignored=ignored, seed=m)
 
 
+@pytest.mark.parametrize("ignored", ["none", "some", "all"])
+@pytest.mark.parametrize("t,m", [("bf16", 511), ("bf16", 512), ("f16", 1100)])
+def test_linear_ce_listed_rows(t, m, ignored):
+    """From 512 rows on the gradient lists the rows that count."""
+    run_ce(m, 300, 75, t, ignored=ignored, seed=m)
+
+
 def test_linear_ce_small_weights_and_large_logits():
     run_ce(100, 2000, 64, "f16", weight=1e-4, seed=1)     # gradients far below FP16's normal range
     run_ce(100, 2000, 64, "f16", weight=6e4, seed=2)
