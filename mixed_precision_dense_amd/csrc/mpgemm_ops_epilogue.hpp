@@ -120,13 +120,18 @@ __device__ __forceinline__ float widen(uint32_t bits16) {
     else
         return __builtin_bit_cast(float, bits16 << 16);
 }
+// Two values as 16-bit ones, a in the low half: one conversion instruction for BF16 (converted one by
+// one and joined they take four), two and a pack for FP16.
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 template <int IN>
-__device__ __forceinline__ unsigned short narrow(float v) {
+__device__ __forceinline__ uint32_t narrow2(float a, float b) {
     if constexpr (IN == IN_F16) {
-        asm("" : "+v"(v));   // the FP32 value first, then one rounding (no fused fma and conversion)
-        return __builtin_bit_cast(unsigned short, (_Float16)v);
+        asm("" : "+v"(a), "+v"(b));   // the FP32 values first, then one rounding (no fused fma and conversion)
+        return __builtin_bit_cast(uint32_t, f16x2{(_Float16)a, (_Float16)b});
     } else {
-        return __builtin_bit_cast(unsigned short, (__bf16)v);
+        return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{a, b}, bf16x2));
     }
 }
 template <int IN>
@@ -142,7 +147,7 @@ __device__ __forceinline__ u32x4 narrow8(const float (&v)[8]) {
     u32x4 x;
 #pragma unroll
     for (int q = 0; q < 4; ++q)
-        x[q] = (uint32_t)narrow<IN>(v[2 * q]) | ((uint32_t)narrow<IN>(v[2 * q + 1]) << 16);
+        x[q] = narrow2<IN>(v[2 * q], v[2 * q + 1]);
     return x;
 }
 
@@ -187,37 +192,50 @@ struct RowScale {
     int target;
 };
 
-// Stores eight columns, ncol of which exist.  nt: past the caches (for whole 128-byte lines).
+// A tile of D or aux: its first element and the bytes from one row to the next.
+struct OpOut {
+    __amdgpu_buffer_rsrc_t to;
+    uint32_t ld;
+};
+__device__ __forceinline__ OpOut op_out(void *base, int64_t element, int64_t ld, int bytes) {
+    return OpOut{make_rsrc((const char *)base + element * bytes), (uint32_t)(ld * bytes)};
+}
+
+// Stores eight values from column c of row `row` of a tile, ncol of which exist (whole: all).  What does
+// not exist goes to an offset that the buffer drops, so that only a row's last, part-filled block
+// takes a branch.  nt: past the caches (for whole 128-byte lines).
+template <int POLICY>
+__device__ __forceinline__ void store16(const OpOut &o, uint32_t off, u32x4 x) {
+    __builtin_amdgcn_raw_buffer_store_b128(x, o.to, (int)off, 0, POLICY);
+}
 template <int IN>
-__device__ __forceinline__ void store8(void *base, int f32, int64_t at, int ncol, const float (&v)[8], bool nt = false) {
+__device__ __forceinline__ void store8(const OpOut &o, int f32, int row, int c, int ncol, bool whole, bool nt, const float (&v)[8]) {
+    uint32_t off = (uint32_t)row * o.ld + (uint32_t)(f32 ? 4 * c : 2 * c);
+    if (!whole && ncol <= 0) off = kOobOffset;
     if (f32) {
-        float *d = (float *)base + at;
-        if (ncol >= 8) {
-            const f32x4 lo = {v[0], v[1], v[2], v[3]}, hi = {v[4], v[5], v[6], v[7]};
-            if (nt) {
-                __builtin_nontemporal_store(lo, (f32x4 *)d);
-                __builtin_nontemporal_store(hi, (f32x4 *)(d + 4));
-            } else {
-                *(f32x4 *)d = lo;
-                *(f32x4 *)(d + 4) = hi;
-            }
-        } else {
+        const u32x4 lo = __builtin_bit_cast(u32x4, f32x4{v[0], v[1], v[2], v[3]});
+        const u32x4 hi = __builtin_bit_cast(u32x4, f32x4{v[4], v[5], v[6], v[7]});
+        if (!whole && ncol > 0 && ncol < 8) {
 #pragma unroll
             for (int q = 0; q < 8; ++q)
-                if (q < ncol) d[q] = v[q];
+                Out<OUT_F32>::store(o.to, q < ncol ? off + 4 * q : kOobOffset, v[q]);
+        } else {
+            // (two stores share each line: not past the caches, which would cost 273 us instead of 221 at
+            // 8192 x 8192 x 2048)
+            store16<0>(o, off, lo);
+            store16<0>(o, off == kOobOffset ? off : off + 16, hi);
         }
     } else {
-        uint16_t *d = (uint16_t *)base + at;
         const u32x4 x = narrow8<IN>(v);
-        if (ncol >= 8) {
-            if (nt)
-                __builtin_nontemporal_store(x, (u32x4 *)d);
-            else
-                *(u32x4 *)d = x;
-        } else {
+        if (!whole && ncol > 0 && ncol < 8) {
 #pragma unroll
             for (int q = 0; q < 8; ++q)
-                if (q < ncol) d[q] = (uint16_t)(q & 1 ? x[q / 2] >> 16 : x[q / 2]);
+                __builtin_amdgcn_raw_buffer_store_b16((unsigned short)(q & 1 ? x[q / 2] >> 16 : x[q / 2]), o.to,
+                                                      (int)(q < ncol ? off + 2 * q : kOobOffset), 0, 0);
+        } else if (nt) {
+            store16<kStreamPolicy>(o, off, x);
+        } else {
+            store16<0>(o, off, x);
         }
     }
 }
@@ -240,15 +258,14 @@ __device__ __forceinline__ float op_alpha(const OpParams &p) {
     return p.scale != nullptr ? p.alpha * p.scale[0] : p.alpha;
 }
 
-// Turns the products v of eight columns col .. in each of G rows into what is stored, and stores it;
-// sums adds up what OP_SLOPE stores (before its rounding).  drow(i) is row i of D, C and aux,
-// and ncol(i) how many of the columns exist there (at most 0: the row does not; whole: all do).  Branches that a
-// lane may take alone stand only around loads and stores: the arithmetic of two rows runs together,
-// so that one element's latencies are covered by the others' (all rows at once would need more
-// registers than a wave has).
+// Turns the products v of eight columns from column c of the tile in each of G rows into what is stored,
+// and stores it to D's tile d (and Z's, aux); sums adds up what OP_SLOPE stores (before its rounding).
+// row(i) is row i's place in the tile, ncol(i) how many of the columns exist there (at most 0: the row
+// does not; whole: all do).  The arithmetic of two rows runs together, so that one element's
+// latencies are covered by the others' (all rows at once would need more registers than a wave has).
 template <int IN, int MODE, int G, typename Row, typename Cols>
-__device__ __forceinline__ void rows_finish(const OpParams &p, float alpha, const OpTile &w, int col, bool whole, bool nt,
-                                            Row &&drow, Cols &&ncol, const ChunkIn (&in)[G], const RowScale (&scale)[G],
+__device__ __forceinline__ void rows_finish(const OpParams &p, float alpha, const OpOut &d, const OpOut &aux, int c, bool whole,
+                                            bool nt, Row &&row, Cols &&ncol, const ChunkIn (&in)[G], const RowScale (&scale)[G],
                                             const float (&bias)[8], float (&v)[G][8], float (&sums)[8]) {
     if constexpr (MODE == OP_SLOPE) {
         float z[G][8];
@@ -293,8 +310,7 @@ __device__ __forceinline__ void rows_finish(const OpParams &p, float alpha, cons
             for (int q = 0; q < 8; ++q) v[i][q] = __builtin_fmaf(alpha, v[i][q], bias[q]);
         if (p.aux != nullptr) {
 #pragma unroll
-            for (int i = 0; i < G; ++i)
-                if (ncol(i) > 0) store8<IN>(p.aux, 0, drow(i) * p.ld_aux + col, ncol(i), v[i], nt);
+            for (int i = 0; i < G; ++i) store8<IN>(aux, 0, row(i), c, ncol(i), whole, nt, v[i]);
         }
         with_act(p.act, p.d_f32, [&](auto a, auto s) {
 #pragma unroll
@@ -318,17 +334,16 @@ __device__ __forceinline__ void rows_finish(const OpParams &p, float alpha, cons
             } else {
 #pragma unroll
                 for (int i = 0; i < G; ++i) {
-                    float c[8];
-                    widen8<IN>(in[i].lo, c);
+                    float old[8];
+                    widen8<IN>(in[i].lo, old);
 #pragma unroll
-                    for (int q = 0; q < 8; ++q) v[i][q] = __builtin_fmaf(p.beta, c[q], v[i][q]);
+                    for (int q = 0; q < 8; ++q) v[i][q] = __builtin_fmaf(p.beta, old[q], v[i][q]);
                 }
             }
         }
     }
 #pragma unroll
-    for (int i = 0; i < G; ++i)
-        if (ncol(i) > 0) store8<IN>(p.D, p.d_f32, w.d_off + drow(i) * p.ldd + col, ncol(i), v[i], nt);
+    for (int i = 0; i < G; ++i) store8<IN>(d, p.d_f32, row(i), c, ncol(i), whole, nt, v[i]);
 }
 
 // ------------------------------------------------------------------------------- experts' rows

@@ -88,6 +88,11 @@ __device__ __forceinline__ void op_store_tile(const OpParams &p, const OpTile &w
             if (wide) dma16(rs, nc > 4 ? off + 16u : kOobOffset, 0u, at + (uint32_t)(q * loads + 1) * 1024u);
         }
     };
+    // the wave's sub-tile of D and of the Z that is kept
+    const int64_t row_d = (int64_t)w.row0 + row_t;
+    const int col_d = w.tn * BN + wn * WC;
+    const OpOut out_d = op_out(p.D, w.d_off + row_d * p.ldd + col_d, p.ldd, p.d_f32 ? 4 : 2);
+    const OpOut out_z = op_out(p.aux, row_d * p.ld_aux + col_d, p.ld_aux, 2);
     const float alpha = op_alpha(p);
     float bias[8], sums[8];
     bias_load<IN, MODE>(p, w.expert, col, bias);
@@ -179,10 +184,10 @@ __device__ __forceinline__ void op_store_tile(const OpParams &p, const OpTile &w
                     scale[q] = RowScale{f->weight, f->lse, f->target - col};
                 }
             }
-            const int row_s = row_t + (pass * kSteps + s) * RI + rr;
+            const int row_s = (pass * kSteps + s) * RI + rr;
             rows_finish<IN, MODE, G>(
-                p, alpha, w, col, full, nt, [&](int q) { return (int64_t)w.row0 + row_s + q * RI; },
-                [&](int q) { return cols_of(row_s + q * RI); }, in, scale, bias, v, sums);
+                p, alpha, out_d, out_z, 8 * c, full, nt, [&](int q) { return row_s + q * RI; },
+                [&](int q) { return cols_of(row_t + row_s + q * RI); }, in, scale, bias, v, sums);
             if (loads > 0 && group + depth < kGroups) {
                 wait_lds<0>();                     // the group's place has been read
                 fetch(group + depth);

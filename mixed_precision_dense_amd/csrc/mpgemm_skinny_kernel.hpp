@@ -197,7 +197,9 @@ void skinny_kernel(OpParams p) {
     float sums[8], bias[8];
 #pragma unroll
     for (int q = 0; q < 8; ++q) sums[q] = 0.0f;
-    const int64_t drow = (int64_t)w.row0 + w.tm * BM + row;
+    const int64_t tile_row = (int64_t)w.row0 + w.tm * BM, drow = tile_row + row;
+    const OpOut out_d = op_out(p.D, w.d_off + tile_row * p.ldd + w.tn * BN, p.ldd, p.d_f32 ? 4 : 2);
+    const OpOut out_z = op_out(p.aux, tile_row * p.ld_aux + w.tn * BN, p.ld_aux, 2);
     if (live) {
         auto finish = [&](auto mode) {
             constexpr int MODE = decltype(mode)::value;
@@ -209,8 +211,8 @@ void skinny_kernel(OpParams p) {
                 const int64_t t = p.target[drow] - p.col0 - col;
                 scale[0] = RowScale{p.weight[drow], p.lse[drow] * kLog2e, t >= 0 && t < 8 ? (int)t : -1};
             }
-            rows_finish<IN, MODE, 1>(p, alpha, w, col, false, false, [&](int) { return drow; }, [&](int) { return ncol; }, in,
-                                     scale, bias, v, sums);
+            rows_finish<IN, MODE, 1>(p, alpha, out_d, out_z, 8 * c, false, false, [&](int) { return row; },
+                                     [&](int) { return ncol; }, in, scale, bias, v, sums);
         };
         if (p.mode == OP_SLOPE)
             finish(std::integral_constant<int, OP_SLOPE>{});

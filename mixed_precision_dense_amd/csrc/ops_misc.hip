@@ -194,7 +194,15 @@ __global__ __launch_bounds__(256) void sum_parts_kernel(const float *parts, int 
     const float f = alpha * scale[0];
 #pragma unroll
     for (int q = 0; q < 8; ++q) v[q] *= f;
-    store8<IN>(out, 0, row * ld_out + col, cols - col, v);
+    uint16_t *to = out + row * ld_out + col;
+    const u32x4 x = narrow8<IN>(v);
+    if (col + 8 <= cols) {
+        *(u32x4 *)to = x;
+    } else {
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+            if (col + q < cols) to[q] = (uint16_t)(q & 1 ? x[q / 2] >> 16 : x[q / 2]);
+    }
 }
 
 int launch_1d(const void *kernel, int64_t blocks, unsigned threads, void **args, void *stream) {
