@@ -210,34 +210,44 @@ __device__ __forceinline__ void op_store_tile(const OpParams &p, const OpTile &w
 
 // Maximum and sum of exponentials of each row over the wave's columns, straight from the
 // accumulators: a row's columns lie in the 16 lanes of a DPP row and FN registers, so both
-// reductions need no LDS.  Values are in units of log 2.
-template <int FM, int FN, int BM, int BN>
-__device__ __forceinline__ void op_row_stats(const OpParams &p, const OpTile &w, f32x4 (&acc)[FM][FN], int wave, int lane) {
+// reductions need no LDS.  Values are in units of log 2.  kPlain: a whole tile and scale > 0, where
+// the maximum is taken of the products as they are and the scaling is part of the exponent's
+// subtraction (3 instead of 6 operations around each exponential).
+template <bool kPlain, int FM, int FN, int BM, int BN>
+__device__ __forceinline__ void op_row_stats(const OpParams &p, const OpTile &w, f32x4 (&acc)[FM][FN], float scale, int wave, int lane) {
     const int wm = wave / 2, wn = wave % 2;
     const int g = lane / 16, u = lane % 16;
     const int col = w.tn * BN + wn * (BN / 2) + u;
     const int row0 = w.tm * BM + wm * (BM / 2) + 4 * g;
-    const int part = 2 * w.tn + wn;
-    const float scale = p.alpha * kLog2e;
+    CeStat *to = p.stats + (int64_t)row0 * p.parts + 2 * w.tn + wn;
     static_for<FM>([&](auto i_c) {
         constexpr int i = decltype(i_c)::value;
+        float v[4][FN], top[4], sum[4];
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-            float v[FN], top = -__builtin_inff();
+            top[r] = -__builtin_inff();
 #pragma unroll
             for (int j = 0; j < FN; ++j) {
-                v[j] = col + 16 * j < p.n ? acc[i][j][r] * scale : -__builtin_inff();
-                top = fmaxf(top, v[j]);
+                v[r][j] = kPlain ? acc[i][j][r] : (col + 16 * j < p.n ? acc[i][j][r] * scale : -__builtin_inff());
+                top[r] = fmaxf(top[r], v[r][j]);
             }
-            top = row_max16(top);
-            const float base = stat_base(top);
-            float sum = 0.0f;
-#pragma unroll
-            for (int j = 0; j < FN; ++j) sum += fast_exp2(v[j] - base);
-            sum = row_sum16(sum);
-            const int row = row0 + 16 * i + r;
-            if (u == 0 && row < w.m) p.stats[(int64_t)row * p.parts + part] = CeStat{top, sum};
         }
+#pragma unroll
+        for (int r = 0; r < 4; ++r) top[r] = row_max16(top[r]);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            if (kPlain) top[r] *= scale;
+            const float base = stat_base(top[r]);
+            sum[r] = 0.0f;
+#pragma unroll
+            for (int j = 0; j < FN; ++j)
+                sum[r] += fast_exp2(kPlain ? __builtin_fmaf(v[r][j], scale, -base) : v[r][j] - base);
+        }
+#pragma unroll
+        for (int r = 0; r < 4; ++r) sum[r] = row_sum16(sum[r]);
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+            if (u == 0 && row0 + 16 * i + r < w.m) to[(int64_t)(16 * i + r) * p.parts] = CeStat{top[r], sum[r]};
     });
 }
 
@@ -258,7 +268,11 @@ void op_kernel(OpParams p) {
     int lane_e = lane;
     asm volatile("" : "+v"(lane_e));   // the epilogue's addresses are formed after the loop
     if constexpr (MODE == OP_CE_STATS) {
-        op_row_stats<FM, FN, T, T>(p, w, acc, wave, lane_e);
+        const float scale = p.alpha * kLog2e;
+        if ((w.tn + 1) * T <= p.n && scale > 0.0f)
+            op_row_stats<true, FM, FN, T, T>(p, w, acc, scale, wave, lane_e);
+        else
+            op_row_stats<false, FM, FN, T, T>(p, w, acc, scale, wave, lane_e);
     } else {
         __syncthreads();               // every wave's fragment reads are done: the LDS is free
         op_store_tile<IN, MODE, FM, FN, T, T>(p, w, acc, smem, wave, lane_e);
