@@ -24,47 +24,53 @@ __device__ __forceinline__ float sigmoid(float x) { return fast_rcp(1.0f + fast_
 __device__ __forceinline__ float cut(float z) { return __builtin_amdgcn_fmed3f(z, -30.0f, 30.0f); }
 
 // Phi(-|z|) of the normal distribution, and bell = exp(-z^2 / 2).  With x = |z| / sqrt(2) and
-// t = 1 / (1 + p x), erfc(x) = exp(-x^2) t q(t), q a polynomial fitted to erfcx(x) in relative
-// minimax over x in [0, 12]; its coefficients are halved here.  The lower tail keeps its relative
-// accuracy, as 1 + erf would not.  Of degree 7 (p = 0.43): 2e-7, and 5e-7 as evaluated in FP32.  Of
-// degree 5 (p = 0.44): 5e-6, an eightieth of half a step of FP16's; what is stored in 16 bits is
-// taken from that one (two of 23 instruction slots less).
-template <bool SHORT>
+// t = 1 / (1 + 0.43 x), erfc(x) = exp(-x^2) t q(t), q a polynomial of degree 7 fitted to erfcx(x) in
+// relative minimax over x in [0, 12] (2e-7, 5e-7 as evaluated in FP32); its coefficients are
+// halved here.  The lower tail keeps its relative accuracy, as 1 + erf would not.
 __device__ __forceinline__ float normal_tail(float z, float &bell) {
-    const float t = fast_rcp(__builtin_fmaf(__builtin_fabsf(z), (SHORT ? 0.44f : 0.43f) * 0.70710678118654752f, 1.0f));
+    const float t = fast_rcp(__builtin_fmaf(__builtin_fabsf(z), 0.43f * 0.70710678118654752f, 1.0f));
     bell = fast_exp2(z * (-0.5f * kLog2e) * z);
-    float q;
-    if constexpr (SHORT) {
-        q = -0.5f * 0.14610657632724167f;
-        q = __builtin_fmaf(q, t, 0.5f * 0.350655200165003f);
-        q = __builtin_fmaf(q, t, 0.5f * 0.04072797427306728f);
-        q = __builtin_fmaf(q, t, 0.5f * 0.26358810029300594f);
-        q = __builtin_fmaf(q, t, 0.5f * 0.24256906750537888f);
-        q = __builtin_fmaf(q, t, 0.5f * 0.24856106715653906f);
-    } else {
-        q = 0.5f * 0.07090955117377087f;
-        q = __builtin_fmaf(q, t, -0.5f * 0.2990298556651683f);
-        q = __builtin_fmaf(q, t, 0.5f * 0.36473237500049616f);
-        q = __builtin_fmaf(q, t, -0.5f * 0.06881683436104556f);
-        q = __builtin_fmaf(q, t, 0.5f * 0.2382076128012132f);
-        q = __builtin_fmaf(q, t, 0.5f * 0.20746980043114047f);
-        q = __builtin_fmaf(q, t, 0.5f * 0.24398845434153432f);
-        q = __builtin_fmaf(q, t, 0.5f * 0.2425387182165695f);
-    }
+    float q = 0.5f * 0.07090955117377087f;
+    q = __builtin_fmaf(q, t, -0.5f * 0.2990298556651683f);
+    q = __builtin_fmaf(q, t, 0.5f * 0.36473237500049616f);
+    q = __builtin_fmaf(q, t, -0.5f * 0.06881683436104556f);
+    q = __builtin_fmaf(q, t, 0.5f * 0.2382076128012132f);
+    q = __builtin_fmaf(q, t, 0.5f * 0.20746980043114047f);
+    q = __builtin_fmaf(q, t, 0.5f * 0.24398845434153432f);
+    q = __builtin_fmaf(q, t, 0.5f * 0.2425387182165695f);
     return bell * (q * t);
+}
+
+// The same without bell, for what is stored in 16 bits: exp2 of a polynomial of degree 7 fitted to
+// log2 Phi(-a) over a in [0, 6], 6.5e-6 relative there (an eightieth of half a step of FP16's); beyond,
+// where Phi < 1e-9, it goes on falling.  11 instruction slots instead of 20 (a transcendental takes four).
+__device__ __forceinline__ float normal_tail_short(float z) {
+    const float a = __builtin_fabsf(z);
+    float e = -1.8348151e-6f;
+    e = __builtin_fmaf(e, a, 6.159837e-5f);
+    e = __builtin_fmaf(e, a, -9.305254e-4f);
+    e = __builtin_fmaf(e, a, 8.507893e-3f);
+    e = __builtin_fmaf(e, a, -5.3960074e-2f);
+    e = __builtin_fmaf(e, a, -4.5846438e-1f);
+    e = __builtin_fmaf(e, a, -1.1512511f);
+    e = __builtin_fmaf(e, a, -9.999953e-1f);
+    return fast_exp2(e);
 }
 
 constexpr float kGeluC = 0.79788456080286536f;   // sqrt(2 / pi)
 constexpr float kGeluA = 0.044715f;
 
-// SHORT: the value is stored in 16 bits (see normal_tail).
+// SHORT: the value is stored in 16 bits (see normal_tail_short).
 template <int ACT, bool SHORT>
 __device__ __forceinline__ float act_value(float z) {
     if constexpr (ACT == ACT_RELU) return z <= 0.0f ? 0.0f : z;   // NaN stays NaN
     // z Phi(z) = max(z, 0) - |z| Phi(-|z|); |z| is cut where the tail is 0, for infinite z
     if constexpr (ACT == ACT_GELU) {
-        float bell;
-        const float tail = normal_tail<SHORT>(z, bell);
+        float bell, tail;
+        if constexpr (SHORT)
+            tail = normal_tail_short(z);
+        else
+            tail = normal_tail(z, bell);
         return __builtin_fmaf(-__builtin_fminf(__builtin_fabsf(z), 30.0f), tail, __builtin_fmaxf(z, 0.0f));
     }
     // 0.5 z (1 + tanh u) = z / (1 + exp(-2u))
@@ -74,13 +80,13 @@ __device__ __forceinline__ float act_value(float z) {
     return z;
 }
 
-template <int ACT, bool SHORT>
+template <int ACT>
 __device__ __forceinline__ float act_slope(float z) {
     if constexpr (ACT == ACT_RELU) return z > 0.0f ? 1.0f : 0.0f;
     if constexpr (ACT == ACT_NONE) return 1.0f;
     if constexpr (ACT == ACT_GELU) {
         float bell;
-        const float tail = normal_tail<SHORT>(z, bell);
+        const float tail = normal_tail(z, bell);
         return __builtin_fmaf(cut(z) * 0.39894228040143268f, bell, z > 0.0f ? 1.0f - tail : tail);
     }
     if constexpr (ACT == ACT_GELU_TANH) {
@@ -271,13 +277,12 @@ __device__ __forceinline__ void rows_finish(const OpParams &p, float alpha, cons
         float z[G][8];
 #pragma unroll
         for (int i = 0; i < G; ++i) widen8<IN>(in[i].lo, z[i]);
-        // (FP32 sums are taken of what is stored in 16 bits: those have the longer form, too)
-        with_act(p.act, p.d_f32 || p.colsum != nullptr, [&](auto a, auto s) {
+        with_act(p.act, true, [&](auto a, auto) {
 #pragma unroll
             for (int i = 0; i < G; ++i) {
 #pragma unroll
                 for (int q = 0; q < 8; ++q)
-                    v[i][q] = alpha * v[i][q] * act_slope<decltype(a)::value, decltype(s)::value>(z[i][q]);
+                    v[i][q] = alpha * v[i][q] * act_slope<decltype(a)::value>(z[i][q]);
                 if (i % 2 == 1) __builtin_amdgcn_sched_barrier(0);
             }
         });
