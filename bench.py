@@ -52,10 +52,12 @@ DEFAULT_WORKLOAD = "bf16_8192_nn"
 def kernel_source_digest(sparse: bool = False) -> str:
     """First 16 hex digits of a SHA-256 over the sources a workload's kernel is built from: all
     of csrc/ for the 2:4 sparse kernel, all but the sparse kernel's own files (sp24*) for the
-    dense kernels, so that a change to one family leaves the other's recorded counters valid."""
+    dense kernels, so that a change to one family leaves the other's recorded counters valid.
+    The files of the products of language models belong to no workload here."""
     h = hashlib.sha256()
+    other = ("mpgemm_ops", "mpgemm_skinny", "ops_", "skinny_")
     for p in sorted(glob.glob(os.path.join(ROOT, "mixed_precision_dense_amd", "csrc", "*"))):
-        if not sparse and os.path.basename(p).startswith("sp24"):
+        if os.path.basename(p).startswith(other) or (not sparse and os.path.basename(p).startswith("sp24")):
             continue
         with open(p, "rb") as f:
             h.update(os.path.basename(p).encode())
