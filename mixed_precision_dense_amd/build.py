@@ -21,7 +21,7 @@ SOURCES = ["mpgemm_host.cpp", "mpgemm_api.hip", "kern_f16.hip", "kern_bf16.hip",
            "sp24.hip", "sp24_f16.hip", "sp24_bf16.hip", "sp24_i8.hip", "sp24_fp8_fp8.hip",
            "sp24_fp8_bf8.hip", "sp24_bf8_fp8.hip", "sp24_bf8_bf8.hip", "mpgemm_ops_host.cpp",
            "mpgemm_ops_api.hip", "ops_forward_f16.hip", "ops_forward_bf16.hip", "ops_slope_f16.hip",
-           "ops_slope_bf16.hip", "ops_ce.hip", "skinny_f16.hip", "skinny_bf16.hip", "ops_misc.hip"]
+           "ops_slope_bf16.hip", "ops_ce.hip", "skinny_f16.hip", "skinny_bf16.hip", "ops_misc.hip", "ops_outer.hip"]
 ARCH = "gfx950"
 
 # Packed FP32 instructions are kept out of all generated code.

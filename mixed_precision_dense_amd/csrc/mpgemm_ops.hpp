@@ -80,6 +80,8 @@ int launch_slope_bf16(bool ta, bool tb, int tile, const OpParams &p, void *strea
 int launch_ce(bool bf16, int tile, const OpParams &p, void *stream);
 int launch_skinny_f16(bool ta, bool tb, int fm, int w, int waves, const OpParams &p, void *stream);
 int launch_skinny_bf16(bool ta, bool tb, int fm, int w, int waves, const OpParams &p, void *stream);
+// D = alpha A^T B in the inputs' type for p.k <= 128, A and B stored k x m and k x n; no other operand
+int launch_outer(bool bf16, const OpParams &p, void *stream);
 // dbias from the tiles' partial column sums (rows_per_tile partial rows a tile)
 int launch_colsum(const OpParams &p, int tile_rows, int rows_per_tile, float *dbias, void *stream);
 // loss and log-sum-exp from the row statistics; X and W give the target's logit

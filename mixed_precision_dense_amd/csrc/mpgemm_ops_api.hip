@@ -275,7 +275,7 @@ mpgemm_status_t mpgemm_run_linear_ce_grad(mpgemm_handle_t handle, int64_t m, int
             q.scale = rows.scale;
             q.count = count;
             q.count_k = 1;
-            MPGEMM_TRY(launch(plan, bf16, true, false, q, stream));
+            MPGEMM_TRY(L.outer ? queued(mpg::launch_outer(bf16, q, stream)) : launch(plan, bf16, true, false, q, stream));
         }
         if (dX) {
             mpg::OpParams q = product(L.dx, m, k, have, 1.0f, probs, L.piece, w, ldw, part, true, ld_part);

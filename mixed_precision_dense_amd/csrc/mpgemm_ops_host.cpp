@@ -130,6 +130,13 @@ int64_t colsum_rows(int64_t groups, int64_t m) {
     return m / 16 + 2 * (groups > 0 ? groups : 1);
 }
 
+// dW over few rows is bound by its stores (us, tiles / the kernel for few summed rows):
+//   24 x 100112 x 1781 165 / 108; 16 x 100112 x 2048 177 / 87; 64 x 32000 x 4096 111 / 72;
+//   96 x 32000 x 4096 117 / 80; 128 x 32000 x 4096 119 / 96; 128 x 4096 x 1024 8.3 / 6.3
+// More rows leave it one wave per SIMD (160 x 32000 x 4096 137 / 141).  Its grid is a multiple of
+// eight times k's strips.
+static bool outer_plan(int64_t m, int64_t k) { return m <= 128 && k <= ((int64_t)1 << 20); }
+
 bool ce_layout(int64_t m, int64_t n, int64_t k, bool train, CeLayout &L) {
     if (m < 0 || n < 1 || k < 0 || m > kOpMaxSize || n > kOpMaxSize || k > kOpMaxSize) return false;
     auto up = [](uint64_t v) { return (v + 255) / 256 * 256; };
@@ -141,6 +148,7 @@ bool ce_layout(int64_t m, int64_t n, int64_t k, bool train, CeLayout &L) {
     L.splits = 1;
     L.k_split = n;
     L.listed = false;
+    L.outer = false;
     L.off_lse = L.off_target = L.off_source = L.off_place = L.off_scale = L.off_x = L.off_probs = L.off_dx = 0;
     L.total = stats;
     if (!train || m == 0) return true;
@@ -153,27 +161,24 @@ bool ce_layout(int64_t m, int64_t n, int64_t k, bool train, CeLayout &L) {
     L.pieces = ceil_div(n, L.piece);
     L.logits = op_plan(m, L.piece, k, true, kProbsWeight);
     L.dw = op_plan(L.piece, k, m, false, 0.0);
+    L.outer = outer_plan(m, k);
     // dX sums over a whole piece, which is cut into ranges where its tiles do not fill the CUs; their
     // FP32 parts are written and read once more, at 4 TB/s.
     const int64_t have = n < L.piece ? n : L.piece;
     const int64_t most_splits = ceil_div(have, 512) < 32 ? ceil_div(have, 512) : 32;
-    L.dx = op_plan(m, k, have, false, 1.4);
-    if (L.dx.skinny) {
-        const int64_t fill = 3 * kCus / at_least1(L.dx.tiles_m * L.dx.tiles_n);
-        L.splits = (int)(fill < 1 ? 1 : (fill > most_splits ? most_splits : fill));
-    } else {
-        double least = 0.0;
-        for (int e = 256; e >= 64; e /= 2)
-            for (int64_t s = 1; s <= most_splits; ++s) {
-                const double t = tiles_time(e, ceil_div(m, e) * ceil_div(k, e) * s, ceil_div(have, s), 1.4) +
-                                 (double)s * (double)m * (double)k * 8.0 / 4.0e6;
-                if (least == 0.0 || t < least) {
-                    least = t;
-                    L.dx = tiled(m, k, e);
-                    L.splits = (int)s;
-                }
+    // (The few rows' kernel needs as many ranges and reads lines by halves: 24 rows, k = 1781, 100112 columns
+    // 115 us with 13 ranges, 83 with 64-wide tiles and 16; 16 rows, 4096, 32000: 44 against 42.)
+    double least = 0.0;
+    for (int e = 256; e >= 64; e /= 2)
+        for (int64_t s = 1; s <= most_splits; ++s) {
+            const double t = tiles_time(e, ceil_div(m, e) * ceil_div(k, e) * s, ceil_div(have, s), 1.4) +
+                             (double)s * (double)m * (double)k * 8.0 / 4.0e6;
+            if (least == 0.0 || t < least) {
+                least = t;
+                L.dx = tiled(m, k, e);
+                L.splits = (int)s;
             }
-    }
+        }
     L.k_split = ceil_div(ceil_div(have, L.splits), 64) * 64;
     L.splits = (int)ceil_div(have, L.k_split);
     // (fewer rows than two tiles: nothing to win)

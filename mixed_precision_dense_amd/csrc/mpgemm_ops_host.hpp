@@ -38,6 +38,7 @@ struct CeLayout {
     int parts;                // row statistics per row
     int64_t piece, pieces;    // vocabulary columns per piece of the gradient
     OpPlan dx, dw;
+    bool outer;               // dW by the kernel for few summed rows instead of dw
     int splits;               // of the piece, in dX's product
     int64_t k_split;
     // Gradients of many rows first list those whose target counts and gather their X, so that rows

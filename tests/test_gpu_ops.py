@@ -369,6 +369,18 @@ def test_linear_ce_listed_rows(t, m, ignored):
     run_ce(m, 300, 75, t, ignored=ignored, seed=m)
 
 
+@pytest.mark.parametrize("t", ["bf16", "f16"])
+@pytest.mark.parametrize("m,n,k", [(2, 5, 3), (31, 700, 263), (32, 130, 520), (33, 65, 64), (64, 127, 257), (65, 1000, 40),
+                                   (96, 64, 319), (127, 300, 1030), (128, 193, 72), (129, 193, 72)])
+def test_linear_ce_few_rows(t, m, n, k):
+    """The weights' gradient of at most 128 rows has a kernel of its own; the rows' gradient is summed in ranges."""
+    run_ce(m, n, k, t, alpha=0.75, seed=m + n + k)
+
+
+def test_linear_ce_few_rows_of_a_large_vocabulary():
+    run_ce(40, 60000, 72, "bf16", seed=6)
+
+
 def test_linear_ce_small_weights_and_large_logits():
     run_ce(100, 2000, 64, "f16", weight=1e-4, seed=1)     # gradients far below FP16's normal range
     run_ce(100, 2000, 64, "f16", weight=6e4, seed=2)
