@@ -165,12 +165,12 @@ bool ce_layout(int64_t m, int64_t n, int64_t k, bool train, CeLayout &L) {
     // dX sums over a whole piece, which is cut into ranges where its tiles do not fill the CUs; their
     // FP32 parts are written and read once more, at 4 TB/s.
     const int64_t have = n < L.piece ? n : L.piece;
-    const int64_t most_splits = ceil_div(have, 512) < 32 ? ceil_div(have, 512) : 32;
+    const int64_t most_splits = ceil_div(have, 512) < 128 ? ceil_div(have, 512) : 128;
     // (The few rows' kernel needs as many ranges and reads lines by halves: 24 rows, k = 1781, 100112 columns
     // 115 us with 13 ranges, 83 with 64-wide tiles and 16; 16 rows, 4096, 32000: 44 against 42.)
     double least = 0.0;
     for (int e = 256; e >= 64; e /= 2)
-        for (int64_t s = 1; s <= most_splits; ++s) {
+        for (int64_t s = 1; s <= most_splits; s += 1 + s / 8) {
             const double t = tiles_time(e, ceil_div(m, e) * ceil_div(k, e) * s, ceil_div(have, s), 1.4) +
                              (double)s * (double)m * (double)k * 8.0 / 4.0e6;
             if (least == 0.0 || t < least) {
