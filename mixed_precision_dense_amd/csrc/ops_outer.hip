@@ -88,6 +88,17 @@ void outer_kernel(OpParams p, int steps, int strips) {
     }
 }
 
+// (instantiated explicitly: host code that only reaches a kernel through an inlined launcher does not
+// reliably emit its launch stub)
+template __global__ void outer_kernel<IN_F16, 1>(OpParams, int, int);
+template __global__ void outer_kernel<IN_F16, 2>(OpParams, int, int);
+template __global__ void outer_kernel<IN_F16, 3>(OpParams, int, int);
+template __global__ void outer_kernel<IN_F16, 4>(OpParams, int, int);
+template __global__ void outer_kernel<IN_BF16, 1>(OpParams, int, int);
+template __global__ void outer_kernel<IN_BF16, 2>(OpParams, int, int);
+template __global__ void outer_kernel<IN_BF16, 3>(OpParams, int, int);
+template __global__ void outer_kernel<IN_BF16, 4>(OpParams, int, int);
+
 template <int IN, int KS>
 int launch_steps(const OpParams &p, hipStream_t stream) {
     const int strips = (p.n + kStrip * kOuterWaves - 1) / (kStrip * kOuterWaves), rows = (p.m + kRows - 1) / kRows;
@@ -96,8 +107,10 @@ int launch_steps(const OpParams &p, hipStream_t stream) {
     parts = parts < 1 ? 1 : (parts > rows ? rows : parts);
     const int steps = (rows + parts - 1) / parts;
     parts = ((rows + steps - 1) / steps + 7) / 8 * 8;   // (whole turns over the XCDs; surplus parts have no rows)
-    outer_kernel<IN, KS><<<(unsigned)(strips * parts), 64 * kOuterWaves, 0, stream>>>(p, steps, strips);
-    return (int)hipGetLastError();
+    // (its own status: an error that the caller left pending on the thread is neither reported nor cleared)
+    void *args[] = {const_cast<OpParams *>(&p), const_cast<int *>(&steps), const_cast<int *>(&strips)};
+    return (int)hipLaunchKernel(reinterpret_cast<const void *>(&outer_kernel<IN, KS>), dim3((unsigned)(strips * parts)),
+                                dim3(64 * kOuterWaves), args, 0, stream);
 }
 
 template <int IN>

@@ -1,5 +1,7 @@
 """The products of language models as a program uses them: captured into a graph, on streams, with large
-offsets, shared weights, offsets outside the contract, and all together in the example's training."""
+offsets, shared weights, offsets outside the contract, after an error that the caller left pending, and
+all together in the example's training."""
+import ctypes
 import os
 import sys
 
@@ -103,6 +105,33 @@ def test_streams_and_repeats():
     for (_, out, _), w in zip((first, second), want):
         for name, v in out.items():
             assert torch.equal(v, w[name]), name
+
+
+@pytest.mark.parametrize("m", [64, 300])
+def test_error_left_pending_by_the_caller_does_not_fail_a_call(m):
+    """A HIP error the caller left pending on the thread (from hipSetDevice on a device that does not
+    exist) is not returned as a call's status, stops no call half way through and stays pending."""
+    say(f"[gpu ops] pending error, {m} rows")
+    hip = ctypes.CDLL("libamdhip64.so.7", mode=os.RTLD_NOLOAD)   # the runtime already loaded
+    queue, out, _ = calls(m, 264, 128, 5, m)
+    queue()
+    torch.cuda.synchronize()
+    want = {name: v.clone() for name, v in out.items()}
+    for v in out.values():
+        v.zero_()
+    stream = torch.cuda.current_stream().cuda_stream
+    torch.cuda.synchronize()
+    bad = hip.hipSetDevice(ctypes.c_int(1 << 20))
+    assert bad != 0
+    try:
+        queue(stream=stream)                                     # (raises for any other status)
+        left = hip.hipGetLastError()
+    finally:
+        hip.hipGetLastError()                                    # leave nothing pending for torch's own launch checks
+    torch.cuda.synchronize()
+    for name, v in out.items():
+        assert torch.equal(v, want[name]), name
+    assert left == bad
 
 
 def test_offsets_past_32_bits():
