@@ -1,7 +1,8 @@
 """The products of language models as a program uses them: captured into a graph, on streams, with large
-offsets, shared weights, offsets outside the contract, after an error that the caller left pending, and
-all together in the example's training."""
+offsets, shared weights, offsets outside the contract, after an error that the caller left pending, with
+more rows than a launch has workgroups, and all together in the example's training."""
 import ctypes
+import math
 import os
 import sys
 
@@ -174,6 +175,56 @@ def test_offsets_past_32_bits():
         ref.assert_within(D[r], z, err + ref.rounding(z, "f32"), f"D of expert {e}")
         v, err = ref.product64(X[r].t(), A[r], cut[e + 1] - cut[e])
         ref.assert_within(B[e * far:e * far + n * k].view(n, k), v, err + ref.rounding(v, "f16"), f"dV of expert {e}")
+
+
+@pytest.mark.parametrize("t", ["bf16", "f16"])
+@pytest.mark.parametrize("m,k", [(70000, 24), (9000, 15000), ((1 << 24) + 3, 8)])
+def test_cross_entropy_past_a_grid(t, m, k):
+    """Rows and row blocks past the workgroups of one launch, without any rounding: X and W are small integers in
+    columns of their own, so that every logit is 0, P a multiple of 1/16 and each sum exact in FP32."""
+    say(f"[gpu ops] linear_ce past a grid {m}x16x{k} {t}")
+    n, dt = 16, ref.TYPES[t]
+    g = torch.Generator("cuda").manual_seed(m)
+    X = torch.zeros(m, k, dtype=dt, device="cuda")
+    W = torch.zeros(n, k, dtype=dt, device="cuda")
+    X[:, :k // 2] = torch.randint(-3, 4, (m, k // 2), generator=g, device="cuda").to(dt)
+    W[:, k // 2:] = torch.randint(-3, 4, (n, k - k // 2), generator=g, device="cuda").to(dt)
+    target = torch.randint(0, n, (m,), generator=g, device="cuda")
+    target[3::5] = -100
+    counts = target >= 0
+    grad = torch.where(counts, torch.ones(m, device="cuda"), torch.full((m,), float("nan"), device="cuda"))
+    size = mp.mpgemm_linear_ce_workspace_size(m, n, k, t, True)
+    ws = torch.empty(size, dtype=torch.uint8, device="cuda")
+    loss, lse = torch.full((m,), ref.SENTINEL, device="cuda"), torch.full((m,), ref.SENTINEL, device="cuda")
+    mp.mpgemm_run_linear_ce(handle().h, m, n, k, 1.0, X, t, k, W, k, target, loss, lse, ws, size)
+    torch.cuda.synchronize()
+    # exponentials of 0 are exact; the logarithm and its product with log 2 are off by a unit each
+    assert float((lse.double() - math.log(n)).abs().max()) <= 2.0 ** -21
+    assert torch.equal(loss, torch.where(counts, lse, torch.zeros_like(lse)))
+    dX, dW = torch.full_like(X, ref.SENTINEL), torch.full_like(W, ref.SENTINEL)
+    mp.mpgemm_run_linear_ce_grad(handle().h, m, n, k, 1.0, X, t, k, W, k, target, lse, grad, dX, k, dW, k, ws, size)
+    torch.cuda.synchronize()
+    del ws
+    p = torch.full((m, n), 1.0 / n, device="cuda")
+    p[torch.arange(m, device="cuda")[counts], target[counts]] -= 1
+    p[~counts] = 0
+    want = torch.zeros(n, k, dtype=torch.float64, device="cuda")
+    for r in range(0, m, 1 << 20):
+        x = slice(r, min(m, r + (1 << 20)))
+        assert torch.equal(dX[x], (p[x].double() @ W.double()).to(dt))
+        want += p[x].double().t().contiguous() @ X[x].double()
+    assert torch.equal(dW, want.to(dt))
+
+
+@pytest.mark.parametrize("n", [5_000_003, (1 << 30) + 100])
+def test_column_sums_past_a_grid(n):
+    """The sum of no rows, over more columns than one launch's workgroups take at a time."""
+    b = torch.full((n,), 3.0, device="cuda")
+    ld = -(-n // 8) * 8
+    mp.mpgemm_run_epilogue_grad(handle().h, False, True, 0, n, 8, 1.0, None, "f16", 8, None, "f16", 8, "silu", None, ld, None, "f32",
+                                ld, b, None, 0)
+    torch.cuda.synchronize()
+    assert not bool(b.any())
 
 
 @pytest.mark.parametrize("rows", [20, 600])

@@ -229,6 +229,15 @@ def test_workspaces():
         assert mp.mpgemm_linear_ce_workspace_size(*args, True) == 0
 
 
+def test_sizes_past_one_launch():
+    """Rows and blocks past the workgroups of one launch are walked by the kernels beside the products."""
+    big = dict(workspace_bytes=1 << 61)
+    for m in ((1 << 24) - 1, 1 << 24, 20_000_000):
+        assert ce(m=m, n=16, k=64, **big) == OK and ce_grad(m=m, n=16, k=64, **big) == OK
+    assert ce_grad(m=1 << 22, n=16, k=8192, ldx=8192, ldw=8192, lddx=8192, lddw=8192, **big) == OK
+    assert epilogue_grad(m=0, n=(1 << 30) + 64, ldd=1 << 31, ldz=1 << 31, A=None, B=None, D=None, Z=None) == OK
+
+
 def test_unknown_handles():
     for run, args in ((mp.mpgemm_run_epilogue, EPILOGUE), (mp.mpgemm_run_epilogue_grad, GRAD), (mp.mpgemm_run_grouped, GROUPED),
                       (mp.mpgemm_run_grouped_grad, GROUPED_GRAD), (mp.mpgemm_run_grouped_wgrad, WGRAD),
