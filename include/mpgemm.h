@@ -399,7 +399,8 @@ mpgemm_status_t mpgemm_run_linear_ce(mpgemm_handle_t handle, int64_t m, int64_t 
  * rows whose target does not count,
  *   dX = alpha * P W,   dW = alpha * P^T X      (type's; either may be NULL and is then skipped).
  *   lse: as mpgemm_run_linear_ce wrote it.  grad: m FP32 values, the gradient of each row's loss.
- *   From 512 rows on, rows whose target does not count are left out of the products.
+ *   Rows whose target does not count add nothing to dW, whatever X and grad hold there, and their
+ *   dX is 0; above 128 rows they are left out of the products.
  *   P is computed in pieces of the vocabulary and rounded to the inputs' type for the products,
  *   after division by the largest |grad(i)| (FP16: and scaling by 2^13, so that small
  *   probabilities stay normal).

@@ -80,7 +80,8 @@ int launch_slope_bf16(bool ta, bool tb, int tile, const OpParams &p, void *strea
 int launch_ce(bool bf16, int tile, const OpParams &p, void *stream);
 int launch_skinny_f16(bool ta, bool tb, int fm, int w, int waves, const OpParams &p, void *stream);
 int launch_skinny_bf16(bool ta, bool tb, int fm, int w, int waves, const OpParams &p, void *stream);
-// D = alpha A^T B in the inputs' type for p.k <= 128, A and B stored k x m and k x n; no other operand
+// D = alpha A^T B in the inputs' type for p.k <= 128, A and B stored k x m and k x n; rows of B whose
+// p.target is negative are taken as zeros; no other operand
 int launch_outer(bool bf16, const OpParams &p, void *stream);
 // dbias from the tiles' partial column sums (rows_per_tile partial rows a tile)
 int launch_colsum(const OpParams &p, int tile_rows, int rows_per_tile, float *dbias, void *stream);
@@ -91,9 +92,10 @@ int launch_ce_merge(bool bf16, const CeStat *stats, int parts, int m, int n, int
 // What the cross entropy's gradient takes from its rows, m entries each.
 struct CeRows {
     float *weight, *lse;   // of a row; weight 0: its target does not count
-    int64_t *target;
-    int *source, *place;   // nullptr: rows stay where they are.  Else only those that count are listed:
-                           // entry j is row source[j], row r is entry place[r] (-1: none)
+    int64_t *target;       // -1: does not count
+    int *place;            // row r is entry place[r] (-1: its target does not count)
+    int *source;           // nullptr: rows stay where they are.  Else only those that count are listed: entry j is
+                           // row source[j]
     float *scale;          // one factor common to the weights
     int *count;            // number of entries
 };
@@ -102,8 +104,8 @@ int launch_ce_rows(bool bf16, int m, int n, const int64_t *target, const float *
 // out row j (16-byte blocks, ld_out) = in row source[j], for count[0] rows of at most m
 int launch_gather_rows(const void *in, int64_t ld_in, const int *source, const int *count, int m, int k, void *out, int64_t ld_out,
                        void *stream);
-// out (rows x cols, 16 bit) = alpha * scale[0] * sum of `splits` FP32 parts; with place, row r's are in
-// row place[r], and a row without one is 0
+// out (rows x cols, 16 bit) = alpha * scale[0] * sum of `splits` FP32 parts; row r's are in row place[r], and
+// a row without one is 0
 int launch_sum_parts(bool bf16, const float *parts, int splits, int64_t stride, int64_t ld_part, const int *place, int rows,
                      int cols, float alpha, const float *scale, void *out, int64_t ld_out, void *stream);
 

@@ -241,12 +241,9 @@ mpgemm_status_t mpgemm_run_linear_ce_grad(mpgemm_handle_t handle, int64_t m, int
     CeLayout L;
     if (!ce_layout(m, n, k, true, L)) return MPGEMM_STATUS_INTERNAL_ERROR;   // checked above
     char *ws = (char *)workspace;
-    mpg::CeRows rows = {(float *)ws, (float *)(ws + L.off_lse), (int64_t *)(ws + L.off_target), nullptr, nullptr,
-                        (float *)(ws + L.off_scale), (int *)(ws + L.off_scale) + 1};
-    if (L.listed) {
-        rows.source = (int *)(ws + L.off_source);
-        rows.place = (int *)(ws + L.off_place);
-    }
+    const mpg::CeRows rows = {(float *)ws, (float *)(ws + L.off_lse), (int64_t *)(ws + L.off_target), (int *)(ws + L.off_place),
+                              L.listed ? (int *)(ws + L.off_source) : nullptr, (float *)(ws + L.off_scale),
+                              (int *)(ws + L.off_scale) + 1};
     float *part = (float *)(ws + L.off_dx);
     void *probs = ws + L.off_probs;
     const int64_t ld_part = round8(k);
@@ -275,6 +272,7 @@ mpgemm_status_t mpgemm_run_linear_ce_grad(mpgemm_handle_t handle, int64_t m, int
             q.scale = rows.scale;
             q.count = count;
             q.count_k = 1;
+            q.target = rows.target;
             MPGEMM_TRY(L.outer ? queued(mpg::launch_outer(bf16, q, stream)) : launch(plan, bf16, true, false, q, stream));
         }
         if (dX) {

@@ -41,8 +41,8 @@ struct CeLayout {
     bool outer;               // dW by the kernel for few summed rows instead of dw
     int splits;               // of the piece, in dX's product
     int64_t k_split;
-    // Gradients of many rows first list those whose target counts and gather their X, so that rows
-    // that do not (padding, a prompt) cost nothing in the products.
+    // Gradients of more rows first list those whose target counts and gather their X, so that rows
+    // that do not (padding, a prompt) cost nothing in the products and nothing of their X reaches dW.
     bool listed;
     uint64_t off_lse, off_target, off_source, off_place, off_scale, off_x, off_probs, off_dx;   // bytes; weights at 0
     uint64_t total;           // also covers the row statistics of the forward pass, which start at 0

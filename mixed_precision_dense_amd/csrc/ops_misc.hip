@@ -116,7 +116,8 @@ __global__ __launch_bounds__(kMergeThreads) void ce_merge_kernel(const CeStat *s
 // summation averages out (relative error of dX and dW in BF16 0.0034 where it is now 0.0017).
 //
 // With lists (rows.source), the rows that count are also numbered in their order, so that the products
-// after this one take only them; their number stays on the device.
+// after this one take only them; their number stays on the device.  Nothing of a row that does not
+// count may reach the gradients: an X of NaN there (padding) would, as 0 * NaN, through a P of 0.
 constexpr int kRowThreads = 1024;
 __global__ __launch_bounds__(kRowThreads) void ce_rows_kernel(int bf16, int m, int n, const int64_t *target, const float *lse,
                                                               const float *grad, CeRows rows) {
@@ -156,13 +157,13 @@ __global__ __launch_bounds__(kRowThreads) void ce_rows_kernel(int bf16, int m, i
             at = before + own + __popcll(mask & (((uint64_t)1 << lane) - 1));
             before += sum;
             __syncthreads();                                // found is written again in the next turn
-            if (r < m) rows.place[r] = counts ? (int)at : -1;
             if (counts) rows.source[at] = (int)r;
         }
+        if (r < m) rows.place[r] = counts ? (int)at : -1;
         if (r < m && (counts || rows.source == nullptr)) {
             rows.weight[at] = weight;
             rows.lse[at] = lse[r];
-            rows.target[at] = t;
+            rows.target[at] = counts ? t : -1;
         }
     }
     if (threadIdx.x == 0) rows.count[0] = rows.source != nullptr ? before : m;
@@ -190,7 +191,7 @@ __global__ __launch_bounds__(256) void sum_parts_kernel(const float *parts, int 
         float v[8];
 #pragma unroll
         for (int q = 0; q < 8; ++q) v[q] = 0.0f;
-        const int64_t from = place != nullptr ? place[row] : row;
+        const int64_t from = place[row];
         const int own = from < 0 ? 0 : splits;
         const float *at = parts + from * ld_part + col;   // (rows of whole 8-column blocks)
         // eight parts on their way at a time (one after the other, 32 parts of 16 x 776 took 11 us)

@@ -19,6 +19,14 @@ constexpr int kStrip = 64;      // columns of D of a wave
 constexpr int kRows = 32;       // rows per step (with 64, a second wave per SIMD finds no registers: 128 x 32000 x 4096 110 us, not 96)
 constexpr int kOuterWaves = 4;  // neighbouring column strips share their rows of A in the caches
 
+// A fragment with the elements of rows that do not take part zeroed (row i of the lane's eight: bit i).
+__device__ __forceinline__ u32x4 keep_rows(u32x4 x, uint32_t live) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+        x[q] &= (live >> (2 * q) & 1 ? 0xFFFFu : 0u) | (live >> (2 * q + 1) & 1 ? 0xFFFF0000u : 0u);
+    return x;
+}
+
 template <int IN, int KS>   // KS: MFMA steps of 32 summed rows
 __global__ __launch_bounds__(64 * kOuterWaves)
 void outer_kernel(OpParams p, int steps, int strips) {
@@ -32,6 +40,10 @@ void outer_kernel(OpParams p, int steps, int strips) {
     const uint32_t lda_b = (uint32_t)(2 * p.lda), ldb_b = (uint32_t)(2 * p.ldb);
     using S = Strip<false, kRows / 16>;
     using SB = Strip<false, 2>;
+    // rows that take part, a bit each
+    uint64_t live[(KS + 1) / 2];
+#pragma unroll
+    for (int h = 0; h < (KS + 1) / 2; ++h) live[h] = __ballot(64 * h + lane < p.k && p.target[64 * h + lane] >= 0);
     u32x4 fb[KS][4];
 #pragma unroll
     for (int s = 0; s < KS; ++s)
@@ -41,7 +53,7 @@ void outer_kernel(OpParams p, int steps, int strips) {
             x.load(make_rsrc((const char *)p.B + 2 * ((int64_t)32 * s * p.ldb + col0 + 32 * h)), lane, ldb_b, p.n - col0 - 32 * h,
                    32 * s, p.k);
 #pragma unroll
-            for (int j = 0; j < 2; ++j) fb[s][2 * h + j] = x.frag(j, lane, 32 * s, p.k);
+            for (int j = 0; j < 2; ++j) fb[s][2 * h + j] = keep_rows(x.frag(j, lane, 32 * s, p.k), (uint32_t)(live[s / 2] >> (32 * (s % 2) + 8 * (lane / 16))));
         }
     const float alpha = op_alpha(p);
     const int first = part * steps;

@@ -370,6 +370,43 @@ def test_linear_ce_listed_rows(t, m, ignored):
 
 
 @pytest.mark.parametrize("t", ["bf16", "f16"])
+@pytest.mark.parametrize("m", [3, 32, 64, 100, 128, 129, 300, 511, 512, 700])
+def test_linear_ce_rows_that_do_not_count_may_hold_anything(t, m):
+    """NaN and infinities in X and grad of rows that do not count: the gradients are those without them, and 0 there."""
+    n, k = 190, 75
+    say(f"[gpu ops] linear_ce ignored rows of NaN, {m} rows {t}")
+    g = rng(m)
+    X, W = ref.matrix(g, m, k, t), ref.matrix(g, n, k, t, k ** -0.5)
+    target = torch.randint(0, n, (m,), generator=g)
+    target[1::3], target[5::9] = -100, n
+    out = ((target < 0) | (target >= n)).cuda()
+    target = target.cuda()
+    grad = torch.randn(m, generator=g).cuda()
+    plain = X.clone()
+    plain[out] = 0
+    X[out, 0::2], X[out, 1::4], X[out, 3::4] = float("nan"), float("inf"), float("-inf")
+    loss, lse = torch.full((m,), ref.SENTINEL, device="cuda"), torch.full((m,), ref.SENTINEL, device="cuda")
+    size = mp.mpgemm_linear_ce_workspace_size(m, n, k, t, True)
+    ws = torch.full((size + 256,), 0xFF, dtype=torch.uint8, device="cuda")
+    mp.mpgemm_run_linear_ce(handle().h, m, n, k, 1.0, X, t, X.stride(0), W, W.stride(0), target, loss, lse, ws, size)
+    torch.cuda.synchronize()
+    want, want_lse, err, lse_err, _, _ = ref.cross_entropy64(plain, W, target, 1.0, k)
+    ref.assert_within(loss, want, err, "loss")
+    ref.assert_within(lse[~out], want_lse[~out.cpu()], lse_err[~out.cpu()], "lse")
+    xbuf, dX = ref.output(m, k, t)
+    wbuf, dW = ref.output(n, k, t)
+    grad[out] = float("nan")
+    mp.mpgemm_run_linear_ce_grad(handle().h, m, n, k, 1.0, X, t, X.stride(0), W, W.stride(0), target, lse, grad, dX, dX.stride(0), dW,
+                                 dW.stride(0), ws, size)
+    torch.cuda.synchronize()
+    dx, dx_err, dw, dw_err = ref.cross_entropy_grad64(plain, W, target, grad, 1.0, k, t)
+    ref.assert_within(dX, dx, dx_err, "dX")
+    ref.assert_within(dW, dw, dw_err, "dW")
+    assert bool((dX[out] == 0).all())
+    assert ref.untouched(xbuf, m, k) and ref.untouched(wbuf, n, k) and bool((ws[size:] == 0xFF).all())
+
+
+@pytest.mark.parametrize("t", ["bf16", "f16"])
 @pytest.mark.parametrize("m,n,k", [(2, 5, 3), (31, 700, 263), (32, 130, 520), (33, 65, 64), (64, 127, 257), (65, 1000, 40),
                                    (96, 64, 319), (127, 300, 1030), (128, 193, 72), (129, 193, 72)])
 def test_linear_ce_few_rows(t, m, n, k):
