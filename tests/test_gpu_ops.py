@@ -86,6 +86,26 @@ def test_epilogue_without_a_product(m):
     assert ref.untouched(dbuf, m, n)
 
 
+@pytest.mark.parametrize("t,out", [("bf16", "bf16"), ("f16", "f16"), ("bf16", "f32")])
+@pytest.mark.parametrize("m", [3, 100])
+def test_gelu_keeps_its_tail(m, t, out):
+    """GELU over -13 .. 13, where |z| Phi(-|z|) falls to 1e-37: relative to the value.  exp(-z^2 / 2) takes an argument
+    of up to 124 in units of log 2, off by two roundings (2 * 2^-24 * 124, times log 2: 2^-16.6); the short form for
+    16-bit values is within 6.5e-6 (2^-17.2); 2^-16 covers both and the roundings after them."""
+    say(f"[gpu ops] gelu's tail {t}->{out} {m} rows")
+    z = torch.cat([torch.linspace(-13, -5.5, 700), torch.linspace(-5.5, 13, 300), torch.tensor([-6.0, -6.0000005, -5.9999995])])
+    z = z[torch.randperm(z.numel(), generator=rng(7))]
+    n = z.numel()
+    dbuf, D = ref.output(m, n, out)
+    mp.mpgemm_run_epilogue(handle().h, False, False, m, n, 0, 1.0, None, t, 8, None, t, 1008, mp.Epilogue(act="gelu", bias=z.cuda()),
+                           0.0, None, out, 1008, D, out, D.stride(0))
+    torch.cuda.synchronize()
+    x = z.double()
+    want = (x * 0.5 * torch.erfc(-x * 2 ** -0.5)).expand(m, n)
+    ref.assert_within(D, want, 2.0 ** -16 * want.abs() + ref.rounding(want, out), "D")
+    assert ref.untouched(dbuf, m, n)
+
+
 @pytest.mark.parametrize("m", [5, 90])
 def test_epilogue_in_place_and_nonfinite(m):
     """D == C; infinities and NaN reach exactly the outputs they belong to."""
