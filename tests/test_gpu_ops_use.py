@@ -280,6 +280,14 @@ def test_the_example_learns():
     assert losses[-1] < 0.5 * losses[0]
 
 
+def test_the_example_answers():
+    """Single tokens through the trained weights: a row whose loss is below log 2 has the right answer, so that a mean
+    loss of 0.05 leaves at most one in fourteen wrong."""
+    import train_experts
+    losses, right = train_experts.train(steps=60)
+    assert losses[-1] < 0.05 and right > 0.9, (losses[-1], right)
+
+
 def test_the_example_gradients_are_differences_of_its_loss():
     """The loss along the gradient of every weight, against differences in FP64 steps of the masters."""
     import train_experts
