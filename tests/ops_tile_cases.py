@@ -23,6 +23,11 @@ def cross_entropy(m, n, k, t, kernels, train=True, ignored="some"):
     return dict(locals())
 
 
+def few(m, n, k, tb, kernel, groups=0):
+    """A product of few rows (of `groups` experts, where there are any)."""
+    return dict(locals())
+
+
 T64, T128, T256 = ("tile", 64), ("tile", 128), ("tile", 256)
 
 FORWARD = [
@@ -83,4 +88,20 @@ CE = [
 PIECES = [
     cross_entropy(4096, 32768, 2048, "bf16", dict(logits=T256, dw=T256, dx=T256, splits=2, pieces=2)),
     cross_entropy(4096, 32768, 4096, "f16", dict(logits=T256, dw=T256, dx=T256, splits=1, pieces=2)),
+]
+
+# every kernel for few rows: ("few", row blocks of 16, column blocks of 16, waves)
+FEW = [
+    few(3, 520, 300, True, ("few", 1, 1, 8)), few(16, 9001, 203, True, ("few", 1, 1, 4)),
+    few(13, 24603, 300, True, ("few", 1, 4, 4)), few(20, 523, 1030, True, ("few", 2, 2, 8)),
+    few(29, 16501, 203, True, ("few", 2, 2, 4)), few(50, 1003, 300, True, ("few", 4, 2, 8)),
+    few(7, 523, 300, False, ("few", 1, 2, 8)), few(15, 16501, 203, False, ("few", 1, 2, 4)),
+    few(17, 523, 1030, False, ("few", 2, 2, 8)), few(32, 16501, 203, False, ("few", 2, 2, 4)),
+    few(64, 1003, 300, False, ("few", 4, 2, 8)),
+]
+FEW_OF_EXPERTS = [
+    few(50, 203, 300, True, ("few", 1, 1, 8), groups=20), few(200, 1003, 203, True, ("few", 1, 1, 4), groups=40),
+    few(280, 1003, 203, True, ("few", 1, 4, 4), groups=40), few(200, 203, 300, True, ("few", 2, 2, 8), groups=9),
+    few(50, 203, 300, False, ("few", 1, 2, 8), groups=20), few(200, 555, 203, False, ("few", 1, 2, 4), groups=40),
+    few(200, 1003, 203, False, ("few", 1, 4, 4), groups=40), few(200, 203, 300, False, ("few", 2, 2, 8), groups=9),
 ]

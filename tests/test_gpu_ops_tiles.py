@@ -1,5 +1,6 @@
-"""The products of language models at every tile edge, against the same in 64 bits: sizes that the rules give
-to 64-, 128- and 256-wide tiles, whole tiles and edges, with outputs whose rows are whole lines and not.
+"""The products of language models in every kernel, against the same in 64 bits: sizes that the rules give to
+64-, 128- and 256-wide tiles, whole tiles and edges, with outputs whose rows are whole lines and not, and to
+each shape of the few rows' kernel.
 What lies past the operands' rows is NaN, what lies past the outputs' must stay, and a second call gives
 the same bits."""
 import math
@@ -10,7 +11,8 @@ import torch
 import mixed_precision_dense_amd as mp
 from tests import ops_reference as ref, ops_tile_cases as cases
 from tests.gpu_harness import handle, say
-from tests.test_gpu_ops import DIVISIONS, experts, experts_of, operands, rng
+from tests.test_gpu_ops import (DIVISIONS, experts, experts_of, operands, rng, run_ce, run_epilogue, run_grad, run_grouped,
+                                run_grouped_grad)
 
 pytestmark = pytest.mark.gpu
 
@@ -270,3 +272,27 @@ def test_cross_entropy_of_no_features(m):
     want[1] = 0
     ref.assert_within(loss[:m], want, torch.where(want == 0, 0 * want, 2.0 ** -18 + 0 * want), "loss")
     assert bool((loss[m:] == ref.SENTINEL).all()) and bool((lse[m:] == ref.SENTINEL).all())
+
+
+@pytest.mark.parametrize("ta", [False, True])
+@pytest.mark.parametrize("t,out", [("bf16", "f32"), ("f16", "f16")])
+@pytest.mark.parametrize("c", cases.FEW, ids=name_of)
+def test_few_rows(c, t, out, ta):
+    m, n, k, tb = (c[x] for x in ("m", "n", "k", "tb"))
+    run_epilogue(m, n, k, t, out, ta, tb, "gelu", bias=t, aux=True, beta=0.5, seed=m)
+    run_grad(m, n, k, t, out, ta, tb, "silu", seed=n)
+
+
+@pytest.mark.parametrize("t", ["bf16", "f16"])
+@pytest.mark.parametrize("c", [c for c in cases.FEW if c["tb"]], ids=name_of)
+def test_cross_entropy_of_few_rows(c, t):
+    run_ce(c["m"], c["n"], c["k"], t, seed=c["n"])
+
+
+@pytest.mark.parametrize("division", ["even", "gaps"])
+@pytest.mark.parametrize("t,out", [("bf16", "bf16"), ("f16", "f32")])
+@pytest.mark.parametrize("c", cases.FEW_OF_EXPERTS, ids=name_of)
+def test_few_rows_of_experts(c, t, out, division):
+    rows, groups, n, k, tb = (c[x] for x in ("m", "groups", "n", "k", "tb"))
+    run_grouped(rows, groups, n, k, t, out, tb, "silu", division, seed=rows)
+    run_grouped_grad(rows, groups, n, k, t, out, tb, "silu", division, seed=rows + 1)

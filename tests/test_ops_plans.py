@@ -45,6 +45,25 @@ def test_cross_entropy_cases(c):
         assert ops_plans.cross_entropy(c["m"], c["n"], c["k"], False)["logits"][0] == "tile"
 
 
+@pytest.mark.parametrize("c", cases.FEW)
+def test_few_rows_cases(c):
+    assert ops_plans.forward(c["m"], c["n"], c["k"], c["tb"], "gelu", True, True) == c["kernel"]
+    assert ops_plans.slope(c["m"], c["n"], c["k"], c["tb"], "silu") == c["kernel"]
+
+
+@pytest.mark.parametrize("c", cases.FEW_OF_EXPERTS)
+def test_few_rows_of_experts_cases(c):
+    assert ops_plans.grouped(c["m"], c["groups"], c["n"], c["k"], c["tb"], "silu", True) == c["kernel"]
+    assert ops_plans.grouped_grad(c["m"], c["groups"], c["n"], c["k"], c["tb"], "silu") == c["kernel"]
+
+
+@pytest.mark.parametrize("t", ["F16", "BF16"])
+def test_every_few_rows_kernel_has_a_case(t):
+    cased = {(word(ta), word(c["tb"]), *map(str, c["kernel"][1:])) for c in cases.FEW for ta in (False, True)}
+    cased |= {("false", word(c["tb"]), *map(str, c["kernel"][1:])) for c in cases.FEW_OF_EXPERTS}
+    assert cased == instances([f"skinny_{t.lower()}.hip"], rf"skinny_kernel<IN_{t}, (\w+), (\w+), (\d), (\d), (\d)>")
+
+
 def test_every_edge_is_reached_by_every_kind():
     edges = {64, 128, 256}
     for kind in (cases.FORWARD, cases.SLOPE, cases.GROUPED):
