@@ -331,6 +331,50 @@ def test_grouped_wgrad(rows, groups, m, n, t, out, division, beta):
     assert ref.untouched(dbuf, groups * m, n)
 
 
+@pytest.mark.parametrize("t,out", [("bf16", "bf16"), ("f16", "f32")])
+@pytest.mark.parametrize("tb", [False, True])
+@pytest.mark.parametrize("rows,n,k", [(37, 72, 96), (300, 137, 200), (2100, 1503, 2008)])
+def test_rows_of_one_expert_do_not_reach_another(rows, n, k, tb, t, out):
+    """NaN in one expert's rows, and in rows of no expert: what belongs to the others is as without them."""
+    say(f"[gpu ops] NaN rows of one expert, {rows}x{n}x{k} {t} tb={tb}")
+    g, groups = rng(rows), 4
+    off = [rows // 10, rows // 3, rows // 2 + 1, rows - 7, rows - 3]     # (rows before the first and after the last are no expert's)
+    e = experts_of(rows, off)
+    bad = ((e == 1) | (e < 0)).cuda()
+    A, X, Z = ref.matrix(g, rows, k, t), ref.matrix(g, rows, n, t), ref.matrix(g, rows, n, t)
+    A[bad], X[bad], Z[bad] = float("nan"), float("inf"), float("nan")
+    B, ldb, stride = experts(g, groups, n, k, t, tb)
+    offsets = torch.tensor(off, dtype=torch.int32, device="cuda")
+    h = handle().h
+    dbuf, D = ref.output(rows, n, out)
+    mp.mpgemm_run_grouped(h, tb, groups, rows, n, k, 1.0, A, t, A.stride(0), offsets, B, t, ldb, stride, mp.Epilogue(act="silu"), D, out,
+                          D.stride(0))
+    gbuf, G = ref.output(rows, n, out)
+    db = torch.full((groups, n), ref.SENTINEL, device="cuda")
+    size = mp.mpgemm_epilogue_grad_workspace_size(groups, rows, n)
+    ws = torch.full((size,), 0xFF, dtype=torch.uint8, device="cuda")
+    mp.mpgemm_run_grouped_grad(h, tb, groups, rows, n, k, 1.0, A, t, A.stride(0), offsets, B, t, ldb, stride, "gelu", Z, Z.stride(0), G,
+                               out, G.stride(0), db, ws, size)
+    vbuf, V = ref.output(groups * k, n, out)
+    mp.mpgemm_run_grouped_wgrad(h, groups, rows, k, n, 1.0, A, t, A.stride(0), X, t, X.stride(0), offsets, 0.0, V, out, V.stride(0),
+                                k * V.stride(0))
+    torch.cuda.synchronize()
+    for i in (0, 2, 3):
+        r = (e == i).cuda()
+        z, z_err = ref.product64(A[r], B[i, :n, :k].t() if tb else B[i, :k, :n], k)
+        d, err, _, _ = ref.forward64(z, z_err, "silu")
+        ref.assert_within(D[r], d, err + ref.rounding(d.abs() + err, out), f"D of expert {i}")
+        d, err = ref.slope64(z, z_err, "gelu", Z[r])
+        ref.assert_within(G[r], d, err + ref.rounding(d.abs() + err, out), f"dZ of expert {i}")
+        s, s_err = ref.column_sums64(d, err)
+        ref.assert_within(db[i], s, s_err, f"dbias of expert {i}")
+        v, err = ref.product64(A[r].t(), X[r], int(r.sum()))
+        ref.assert_within(V[i * k:(i + 1) * k], v, err + ref.rounding(v.abs() + err, out), f"dV of expert {i}")
+    none = (e < 0).cuda()
+    assert bool((D[none] == ref.SENTINEL).all()) and bool((G[none] == ref.SENTINEL).all())
+    assert ref.untouched(dbuf, rows, n) and ref.untouched(gbuf, rows, n) and ref.untouched(vbuf, groups * k, n)
+
+
 # ----------------------------------------------------------------------------- cross entropy
 def run_ce(m, n, k, t, alpha=1.0, ignored="some", seed=0, scale=2.0, train=True, weight=1.0):
     say(f"[gpu ops] linear_ce {m}x{n}x{k} {t} alpha={alpha} ignored={ignored}")
