@@ -403,7 +403,8 @@ mpgemm_status_t mpgemm_run_linear_ce(mpgemm_handle_t handle, int64_t m, int64_t 
  *   dX is 0; above 128 rows they are left out of the products.
  *   P is computed in pieces of the vocabulary and rounded to the inputs' type for the products,
  *   after division by the largest |grad(i)| (FP16: and scaling by 2^13, so that small
- *   probabilities stay normal).
+ *   probabilities stay normal; the scale is one for the call, and an entry of P below 2^-27 of
+ *   the largest |grad(i)| has fewer bits, so that rows far below the largest lose some of theirs).
  *   workspace: mpgemm_linear_ce_workspace_size(m, n, k, type, 1) bytes, which is also enough for
  *   mpgemm_run_linear_ce. */
 mpgemm_status_t mpgemm_run_linear_ce_grad(mpgemm_handle_t handle, int64_t m, int64_t n, int64_t k,
