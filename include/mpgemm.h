@@ -422,7 +422,120 @@ uint64_t mpgemm_epilogue_grad_workspace_size(int64_t groups, int64_t m, int64_t 
 uint64_t mpgemm_linear_ce_workspace_size(int64_t m, int64_t n, int64_t k, mpgemm_dtype_t type,
                                          int train);
 
+/* ---------------------------------------------------------------------------------------
+ * Gated products: the first half of a gated feed-forward block, both projections, the activation and
+ * the product of the two in one call, and the gradient that comes back to it.  Types, storage and
+ * everything else are as above; A is stored m x k.
+ *
+ * Pairs.  Two matrices of the same shape, type and leading dimension, the gate's and the up
+ * projection's, are given by the gate's address and the elements from there to the up projection's:
+ * stride_up for the weights, stride_kept for G and U, stride_d for dG and dU.  Side by side in
+ * each row and one after the other are both such pairs.  Strides are multiples of 8 elements, not
+ * negative; a pair that is written must not overlap itself: stride >= n and stride + n <= the leading
+ * dimension, or stride >= (m - 1) * the leading dimension + n.  A pair of weights lies in one
+ * allocation: the memory between the two is read too (its values have no effect), and 256 rows of
+ * ldb and stride_up together span less than 2^31 bytes.
+ * --------------------------------------------------------------------------------------- */
+typedef struct {
+    int act;                  /* an mpgemm_act_t */
+    const void *bias_gate;    /* n values each, added to every row; NULL: none */
+    const void *bias_up;
+    int bias_type;            /* an mpgemm_dtype_t: the inputs' type or MPGEMM_R_32F */
+    int64_t bias_stride;      /* grouped products: elements between two experts' biases (0: one for
+                                 all); otherwise ignored */
+    void *kept;               /* receives G and U (m x n each, the inputs' type); NULL: not kept */
+    int64_t ld_kept;
+    int64_t stride_kept;
+} mpgemm_gated_t;
+
+typedef struct {
+    int act;                  /* an mpgemm_act_t */
+    const void *kept;         /* G and U (m x n each, the inputs' type), as the forward call kept them */
+    int64_t ld_kept;
+    int64_t stride_kept;
+    void *H;                  /* receives act(G) U (m x n, the inputs' type); NULL: not formed */
+    int64_t ldh;
+    float *dbias;             /* receives the column sums of dG (n values) and of dU (n values), for
+                                 each expert; NULL: not computed */
+} mpgemm_gated_grad_t;
+
+/* Queue  G = alpha * A * op(Bg) + bias_gate,  U = alpha * A * op(Bu) + bias_up,  D = act(G) U.
+ *   Bg and Bu: the pair at B (k x n for transb == N, n x k for transb == T).
+ *   D is formed from G and U before their rounding.  k == 0 gives G and U their biases. */
+mpgemm_status_t mpgemm_run_gated(mpgemm_handle_t handle, mpgemm_op_t transb, int64_t m, int64_t n,
+                                 int64_t k, const float *alpha, const void *A,
+                                 mpgemm_dtype_t a_type, int64_t lda, const void *B,
+                                 mpgemm_dtype_t b_type, int64_t ldb, int64_t stride_up,
+                                 const mpgemm_gated_t *gated, void *D, mpgemm_dtype_t d_type,
+                                 int64_t ldd, void *stream);
+
+/* Queue the gradient that comes back through a gated product: with E = alpha * A * op(B), the gradient
+ * of its D (A the block's output gradient, B the down projection's weights),
+ *   dG = E U act'(G),  dU = E act(G),  H = act(G) U,
+ * with dG and dU the pair at D, and the column sums of both, summed in FP32 before the rounding in a
+ * fixed order.  m == 0 gives dbias = 0.
+ *   workspace: mpgemm_gated_grad_workspace_size(1, m, n) bytes (none without dbias). */
+mpgemm_status_t mpgemm_run_gated_grad(mpgemm_handle_t handle, mpgemm_op_t transb, int64_t m,
+                                      int64_t n, int64_t k, const float *alpha, const void *A,
+                                      mpgemm_dtype_t a_type, int64_t lda, const void *B,
+                                      mpgemm_dtype_t b_type, int64_t ldb,
+                                      const mpgemm_gated_grad_t *grad, void *D,
+                                      mpgemm_dtype_t d_type, int64_t ldd, int64_t stride_d,
+                                      void *workspace, uint64_t workspace_bytes, void *stream);
+
+/* The same for each expert's rows (see mpgemm_run_grouped for the offsets, and what becomes of rows of
+ * no expert): expert e's weights are at B + e * stride_b elements, its biases at e * bias_stride, its
+ * dbias at e * 2n.  workspace: mpgemm_gated_grad_workspace_size(groups, rows, n) bytes. */
+mpgemm_status_t mpgemm_run_grouped_gated(mpgemm_handle_t handle, mpgemm_op_t transb, int64_t groups,
+                                         int64_t rows, int64_t n, int64_t k, const float *alpha,
+                                         const void *A, mpgemm_dtype_t a_type, int64_t lda,
+                                         const int32_t *offsets, const void *B,
+                                         mpgemm_dtype_t b_type, int64_t ldb, int64_t stride_b,
+                                         int64_t stride_up, const mpgemm_gated_t *gated, void *D,
+                                         mpgemm_dtype_t d_type, int64_t ldd, void *stream);
+mpgemm_status_t mpgemm_run_grouped_gated_grad(mpgemm_handle_t handle, mpgemm_op_t transb,
+                                              int64_t groups, int64_t rows, int64_t n, int64_t k,
+                                              const float *alpha, const void *A,
+                                              mpgemm_dtype_t a_type, int64_t lda,
+                                              const int32_t *offsets, const void *B,
+                                              mpgemm_dtype_t b_type, int64_t ldb, int64_t stride_b,
+                                              const mpgemm_gated_grad_t *grad, void *D,
+                                              mpgemm_dtype_t d_type, int64_t ldd, int64_t stride_d,
+                                              void *workspace, uint64_t workspace_bytes,
+                                              void *stream);
+
+/* Workspace bytes of the gradients for dbias (groups == 1 for mpgemm_run_gated_grad); 0 for sizes
+ * outside the contract.  Host-only. */
+uint64_t mpgemm_gated_grad_workspace_size(int64_t groups, int64_t m, int64_t n);
+
 /* Host-only argument checks of the entry points above (as mpgemm_check is for mpgemm_run). */
+mpgemm_status_t mpgemm_check_gated(mpgemm_op_t transb, int64_t m, int64_t n, int64_t k,
+                                   const float *alpha, const void *A, mpgemm_dtype_t a_type,
+                                   int64_t lda, const void *B, mpgemm_dtype_t b_type, int64_t ldb,
+                                   int64_t stride_up, const mpgemm_gated_t *gated, const void *D,
+                                   mpgemm_dtype_t d_type, int64_t ldd);
+mpgemm_status_t mpgemm_check_gated_grad(mpgemm_op_t transb, int64_t m, int64_t n, int64_t k,
+                                        const float *alpha, const void *A, mpgemm_dtype_t a_type,
+                                        int64_t lda, const void *B, mpgemm_dtype_t b_type,
+                                        int64_t ldb, const mpgemm_gated_grad_t *grad, const void *D,
+                                        mpgemm_dtype_t d_type, int64_t ldd, int64_t stride_d,
+                                        const void *workspace, uint64_t workspace_bytes);
+mpgemm_status_t mpgemm_check_grouped_gated(mpgemm_op_t transb, int64_t groups, int64_t rows,
+                                           int64_t n, int64_t k, const float *alpha, const void *A,
+                                           mpgemm_dtype_t a_type, int64_t lda,
+                                           const int32_t *offsets, const void *B,
+                                           mpgemm_dtype_t b_type, int64_t ldb, int64_t stride_b,
+                                           int64_t stride_up, const mpgemm_gated_t *gated,
+                                           const void *D, mpgemm_dtype_t d_type, int64_t ldd);
+mpgemm_status_t mpgemm_check_grouped_gated_grad(mpgemm_op_t transb, int64_t groups, int64_t rows,
+                                                int64_t n, int64_t k, const float *alpha,
+                                                const void *A, mpgemm_dtype_t a_type, int64_t lda,
+                                                const int32_t *offsets, const void *B,
+                                                mpgemm_dtype_t b_type, int64_t ldb,
+                                                int64_t stride_b, const mpgemm_gated_grad_t *grad,
+                                                const void *D, mpgemm_dtype_t d_type, int64_t ldd,
+                                                int64_t stride_d, const void *workspace,
+                                                uint64_t workspace_bytes);
 mpgemm_status_t mpgemm_check_epilogue(mpgemm_op_t transa, mpgemm_op_t transb, int64_t m, int64_t n,
                                       int64_t k, const float *alpha, const void *A,
                                       mpgemm_dtype_t a_type, int64_t lda, const void *B,

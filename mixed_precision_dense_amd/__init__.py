@@ -64,6 +64,7 @@ SIGNATURES = {
     "mpgemm_bf16x3_workspace_size": (_u64, [_i32, _i32, _i64, _i64, _i64]),
     "mpgemm_epilogue_grad_workspace_size": (_u64, [_i64, _i64, _i64]),
     "mpgemm_linear_ce_workspace_size": (_u64, [_i64, _i64, _i64, _i32, _i32]),
+    "mpgemm_gated_grad_workspace_size": (_u64, [_i64, _i64, _i64]),
 }
 # Arguments of the products of language models: the check's, and the run's with the handle before
 # and the stream after them.
@@ -78,6 +79,13 @@ _OPS = {
                      _i32, _vp, _i64, _vp, _i32, _i64, _vp, _vp, _u64],
     "grouped_wgrad": [_i64, _i64, _i64, _i64, _vp, _vp, _i32, _i64, _vp, _i32, _i64, _vp, _vp, _vp,
                       _i32, _i64, _i64],
+    "gated": [_i32, _i64, _i64, _i64, _vp, _vp, _i32, _i64, _vp, _i32, _i64, _i64, _vp, _vp, _i32, _i64],
+    "gated_grad": [_i32, _i64, _i64, _i64, _vp, _vp, _i32, _i64, _vp, _i32, _i64, _vp, _vp, _i32, _i64, _i64,
+                   _vp, _u64],
+    "grouped_gated": [_i32, _i64, _i64, _i64, _i64, _vp, _vp, _i32, _i64, _vp, _vp, _i32, _i64, _i64, _i64,
+                      _vp, _vp, _i32, _i64],
+    "grouped_gated_grad": [_i32, _i64, _i64, _i64, _i64, _vp, _vp, _i32, _i64, _vp, _vp, _i32, _i64, _i64,
+                           _vp, _vp, _i32, _i64, _i64, _vp, _u64],
     "linear_ce": [_i64, _i64, _i64, _vp, _vp, _i32, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _u64],
     "linear_ce_grad": [_i64, _i64, _i64, _vp, _vp, _i32, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _i64,
                        _vp, _i64, _vp, _u64],
@@ -310,7 +318,7 @@ def _f32(v):
 _F32 = {v: ctypes.byref(ctypes.c_float(v)) for v in (1.0, 0.0)}   # (equal keys: 0.0 stands for -0.0 too)
 
 
-def _epi(e: Optional[Epilogue]):
+def _epi(e):
     return None if e is None else ctypes.byref(e.struct)
 
 
@@ -454,6 +462,122 @@ def mpgemm_run_linear_ce_grad(handle, m, n, k, alpha, X, dtype, ldx, W, ldw, tar
 
 def mpgemm_check_linear_ce_grad(*args) -> int:
     return load().mpgemm_check_linear_ce_grad(*_linear_ce_grad_args(*args))
+
+
+class _GatedStruct(ctypes.Structure):
+    _fields_ = [("act", _i32), ("bias_gate", _vp), ("bias_up", _vp), ("bias_type", _i32), ("bias_stride", _i64),
+                ("kept", _vp), ("ld_kept", _i64), ("stride_kept", _i64)]
+
+
+class _GatedGradStruct(ctypes.Structure):
+    _fields_ = [("act", _i32), ("kept", _vp), ("ld_kept", _i64), ("stride_kept", _i64), ("H", _vp), ("ldh", _i64),
+                ("dbias", _vp)]
+
+
+class Gated:
+    """mpgemm_gated_t: activation, the biases of the two projections (of ``bias_type``, ``bias_stride``
+    elements from one expert's to the next's) and where G and, ``stride_kept`` elements further, U are
+    kept.  Holds its tensors."""
+
+    __slots__ = ("struct", "held")
+
+    def __init__(self, act="none", bias_gate=None, bias_up=None, bias_type="f32", bias_stride=0, kept=None,
+                 ld_kept=0, stride_kept=0):
+        self.held = (bias_gate, bias_up, kept)
+        self.struct = _GatedStruct(_act(act), _ptr(bias_gate), _ptr(bias_up), _dtype(bias_type), bias_stride,
+                                   _ptr(kept), ld_kept, stride_kept)
+
+
+class GatedGrad:
+    """mpgemm_gated_grad_t: activation, the kept G and U, where H = act(G) U goes and where the column
+    sums of dG and dU go (2 n values for each expert); the last two may be None.  Holds its tensors."""
+
+    __slots__ = ("struct", "held")
+
+    def __init__(self, act="none", kept=None, ld_kept=0, stride_kept=0, H=None, ldh=0, dbias=None):
+        self.held = (kept, H, dbias)
+        self.struct = _GatedGradStruct(_act(act), _ptr(kept), ld_kept, stride_kept, _ptr(H), ldh, _ptr(dbias))
+
+
+def _gated_args(transb, m, n, k, alpha, A, a_type, lda, B, b_type, ldb, stride_up, gated, D, d_type, ldd):
+    return (_op(transb), m, n, k, _f32(alpha), _ptr(A), _dtype(a_type), lda, _ptr(B), _dtype(b_type), ldb,
+            stride_up, _epi(gated), _ptr(D), _dtype(d_type), ldd)
+
+
+def mpgemm_run_gated(handle, transb, m, n, k, alpha, A, a_type, lda, B, b_type, ldb, stride_up, gated, D, d_type,
+                     ldd, stream=None, check: bool = True) -> int:
+    """Queue D = act(G) U with G = alpha A op(Bg) + bias_gate, U = alpha A op(Bu) + bias_up, Bu stride_up
+    elements after Bg in one allocation."""
+    return _run("mpgemm_run_gated", handle,
+                _gated_args(transb, m, n, k, alpha, A, a_type, lda, B, b_type, ldb, stride_up, gated, D, d_type, ldd),
+                stream, check)
+
+
+def mpgemm_check_gated(*args) -> int:
+    return load().mpgemm_check_gated(*_gated_args(*args))
+
+
+def _gated_grad_args(transb, m, n, k, alpha, A, a_type, lda, B, b_type, ldb, grad, D, d_type, ldd, stride_d,
+                     workspace, workspace_bytes):
+    return (_op(transb), m, n, k, _f32(alpha), _ptr(A), _dtype(a_type), lda, _ptr(B), _dtype(b_type), ldb,
+            _epi(grad), _ptr(D), _dtype(d_type), ldd, stride_d, _ptr(workspace), workspace_bytes)
+
+
+def mpgemm_run_gated_grad(handle, transb, m, n, k, alpha, A, a_type, lda, B, b_type, ldb, grad, D, d_type, ldd,
+                          stride_d, workspace, workspace_bytes, stream=None, check: bool = True) -> int:
+    """Queue dG = E U act'(G) to D and dU = E act(G) stride_d elements after it, E = alpha A op(B); on
+    request H = act(G) U and the column sums of both."""
+    return _run("mpgemm_run_gated_grad", handle,
+                _gated_grad_args(transb, m, n, k, alpha, A, a_type, lda, B, b_type, ldb, grad, D, d_type, ldd,
+                                 stride_d, workspace, workspace_bytes), stream, check)
+
+
+def mpgemm_check_gated_grad(*args) -> int:
+    return load().mpgemm_check_gated_grad(*_gated_grad_args(*args))
+
+
+def _grouped_gated_args(transb, groups, rows, n, k, alpha, A, a_type, lda, offsets, B, b_type, ldb, stride_b,
+                        stride_up, gated, D, d_type, ldd):
+    return (_op(transb), groups, rows, n, k, _f32(alpha), _ptr(A), _dtype(a_type), lda, _ptr(offsets), _ptr(B),
+            _dtype(b_type), ldb, stride_b, stride_up, _epi(gated), _ptr(D), _dtype(d_type), ldd)
+
+
+def mpgemm_run_grouped_gated(handle, transb, groups, rows, n, k, alpha, A, a_type, lda, offsets, B, b_type, ldb,
+                             stride_b, stride_up, gated, D, d_type, ldd, stream=None, check: bool = True) -> int:
+    """mpgemm_run_gated for the rows of every expert."""
+    return _run("mpgemm_run_grouped_gated", handle,
+                _grouped_gated_args(transb, groups, rows, n, k, alpha, A, a_type, lda, offsets, B, b_type, ldb,
+                                    stride_b, stride_up, gated, D, d_type, ldd), stream, check)
+
+
+def mpgemm_check_grouped_gated(*args) -> int:
+    return load().mpgemm_check_grouped_gated(*_grouped_gated_args(*args))
+
+
+def _grouped_gated_grad_args(transb, groups, rows, n, k, alpha, A, a_type, lda, offsets, B, b_type, ldb, stride_b,
+                             grad, D, d_type, ldd, stride_d, workspace, workspace_bytes):
+    return (_op(transb), groups, rows, n, k, _f32(alpha), _ptr(A), _dtype(a_type), lda, _ptr(offsets), _ptr(B),
+            _dtype(b_type), ldb, stride_b, _epi(grad), _ptr(D), _dtype(d_type), ldd, stride_d, _ptr(workspace),
+            workspace_bytes)
+
+
+def mpgemm_run_grouped_gated_grad(handle, transb, groups, rows, n, k, alpha, A, a_type, lda, offsets, B, b_type,
+                                  ldb, stride_b, grad, D, d_type, ldd, stride_d, workspace, workspace_bytes,
+                                  stream=None, check: bool = True) -> int:
+    """mpgemm_run_gated_grad for the rows of every expert."""
+    return _run("mpgemm_run_grouped_gated_grad", handle,
+                _grouped_gated_grad_args(transb, groups, rows, n, k, alpha, A, a_type, lda, offsets, B, b_type, ldb,
+                                         stride_b, grad, D, d_type, ldd, stride_d, workspace, workspace_bytes),
+                stream, check)
+
+
+def mpgemm_check_grouped_gated_grad(*args) -> int:
+    return load().mpgemm_check_grouped_gated_grad(*_grouped_gated_grad_args(*args))
+
+
+def mpgemm_gated_grad_workspace_size(groups: int, m: int, n: int) -> int:
+    """Workspace bytes of mpgemm_run_gated_grad (groups = 1) and mpgemm_run_grouped_gated_grad for dbias."""
+    return load().mpgemm_gated_grad_workspace_size(groups, m, n)
 
 
 def mpgemm_epilogue_grad_workspace_size(groups: int, m: int, n: int) -> int:

@@ -205,9 +205,24 @@ __device__ __forceinline__ u32x4 keep_first_bytes(u32x4 v, int nbytes) {
 // columns outside m x n only reaches accumulators of outputs that are never stored.  Chunks
 // beyond K within a row are the exception -- they would reach every output -- and are zeroed
 // in LDS once they have landed (fix_k_tail).
+//
+//   PW: 0, or the columns of a wave where the operand is a pair (gated products): two matrices of
+//   the same shape and leading dimension, the second up_off bytes after the first.  A wave's first
+//   PW / 2 columns are then columns of the first, the others the same columns of the second, so
+//   that both factors of an output lie in one wave.  mn_left counts the columns of one of the two.
+//   All of it, and the memory between the two, is one readable range, so that the clamps above
+//   hold with the second's end as the end; what lies past K in the first may be anything, k-rows
+//   included, and is zeroed in LDS.
 // ---------------------------------------------------------------------------------------
-template <int EB, bool KC, int NS, int R = 1>
+template <int EB, bool KC, int NS, int R = 1, int PW = 0>
 struct Operand {
+    static_assert(PW == 0 || (EB == 2 && PW % 32 == 0), "pairs of 16-wide blocks");
+    // Column of its matrix that the tile's column x stands for, and whether that is the second.
+    static __device__ __forceinline__ int column(int x) {
+        return PW == 0 ? x : x / (PW > 0 ? PW : 1) * (PW / 2) + x % (PW > 0 ? PW / 2 : 1);
+    }
+    static __device__ __forceinline__ bool second(int x) { return PW > 0 && x % (PW > 0 ? PW : 1) >= PW / 2; }
+
     static_assert(NS == 2 || NS == 4 || NS == 8, "sub-tile count");
     static_assert((R == 1 || R == 2) && NS % R == 0, "waves per quarter slot");
     static constexpr int kStageBytes = NS * kSubTileBytes;
@@ -256,15 +271,17 @@ struct Operand {
     // uses offset j mod kGroupBlocks: a place known only at run time would turn the offsets into
     // an array in memory (64 x 64 tiles, MN-contiguous operand: 840 x 728 x 168 in 15 us, not 5).
     __device__ __forceinline__ void init(int wave, int hi, int lane, int64_t ld, int mn_left,
-                                         uint32_t lds_base, int first_blk = 0) {
+                                         uint32_t lds_base, int first_blk = 0, uint32_t up_off = 0) {
         const uint32_t row_bytes = (uint32_t)(ld * EB);
         const int g = lane / 16, u = lane % 16;
         if constexpr (KC) {
             const int r = wave * 8 + lane / 8;                      // row within the sub-tile
             const int c = (lane % 8) ^ kc_swz(r);                   // logical chunk of phys lane % 8
 #pragma unroll
-            for (int i = 0; i < kSlots; ++i)
-                voff[i] = (uint32_t)min(32 * (i * R + hi) + r, mn_left - 1) * row_bytes + 16u * c;
+            for (int i = 0; i < kSlots; ++i) {
+                const int x = 32 * (i * R + hi) + r;
+                voff[i] = (uint32_t)min(column(x), mn_left - 1) * row_bytes + 16u * c + (second(x) ? up_off : 0u);
+            }
             // fragment: lane reads row u of its 16-row block, chunk g of the 64-byte k step
 #pragma unroll
             for (int ks = 0; ks < 2; ++ks)
@@ -279,8 +296,9 @@ struct Operand {
 #pragma unroll
             for (int i = 0; i < kSlots; ++i) {
                 const int o = i * R + hi;                           // sub-tile position
+                const int x = (o / kSlotsPerGroup) * (128 / EB) + (16 / EB) * c;
                 voff[i] = (uint32_t)(32 * (o % kSlotsPerGroup) + kr) * row_bytes +
-                          (uint32_t)min((o / kSlotsPerGroup) * 128 + 16 * c, col_max);
+                          (uint32_t)min(column(x) * EB, col_max) + (second(x) ? up_off : 0u);
             }
             if constexpr (EB == 2) {
                 // tr16: lane 4 s + q of group g reads k-row 8 g + s (+4 for the high half),
@@ -327,6 +345,17 @@ struct Operand {
                     typedef __attribute__((address_space(3))) u32x4 lds_u32x4;
                     lds_u32x4 *q = (lds_u32x4 *)(stage + i * R * 4096 + l_off);
                     *q = keep_first_bytes(*q, keep);
+                }
+            }
+        } else if constexpr (PW > 0) {
+            // a pair's k-rows past K lie before the second's end: they have been read
+            asm volatile("" : "+v"(lane));
+#pragma unroll
+            for (int i = 0; i < kSlots; ++i) {
+                const int o = i * R + hi;
+                if (32 * (o % kSlotsPerGroup) + wave * 8 + lane / 8 >= k_left) {
+                    typedef __attribute__((address_space(3))) u32x4 lds_u32x4;
+                    *(lds_u32x4 *)(stage + o * 4096 + wave * 1024 + lane * 16) = u32x4{0u, 0u, 0u, 0u};
                 }
             }
         }
@@ -891,10 +920,13 @@ constexpr int tile_lds_bytes() {
 // into acc; smem holds at least tile_lds_bytes() of LDS.  When it returns, this wave's loads have
 // landed and its accumulators can be read; other waves may still be reading fragments, so the
 // LDS is free for the epilogue only after a barrier.
+// PAIR: B is a pair of matrices, the second up_off bytes after the first (see Operand); the tile's BN
+// columns are then BN / 2 of each, from column n0 of p.n.
 // ---------------------------------------------------------------------------------------
-template <int IN, bool TA, bool TB, int BM, int BN, int NW>
+template <int IN, bool TA, bool TB, int BM, int BN, int NW, bool PAIR = false>
 __device__ __forceinline__ void tile_product(const Params &p, int m0, int n0, lds_char *smem,
-                                             typename MmaAcc<IN>::type (&acc)[BM / 32][BN / (8 * NW)]) {
+                                             typename MmaAcc<IN>::type (&acc)[BM / 32][BN / (8 * NW)],
+                                             uint32_t up_off = 0) {
     constexpr bool kF8 = is_fp8(IN);
     static_assert(NW == 4 || (NW == 8 && !kF8), "4 waves, or 8 for 2-byte and INT8 inputs");
     constexpr int EB = (IN == IN_I8 || kF8) ? 1 : 2;
@@ -903,7 +935,7 @@ __device__ __forceinline__ void tile_product(const Params &p, int m0, int n0, ld
     constexpr int FM = BM / 32, FN = BN / (8 * NW);
     constexpr int kStageK = kStageKBytes / EB;
     using OpA = Operand<EB, !TA, NSA, NW / 4>;
-    using OpB = Operand<EB, TB, NSB, NW / 4>;
+    using OpB = Operand<EB, TB, NSB, NW / 4, PAIR ? BN / (NW / 2) : 0>;
     using acc_t = typename MmaAcc<IN>::type;
     constexpr int A_BYTES = OpA::kStageBytes, B_BYTES = OpB::kStageBytes;
     constexpr int kLoadsPerStage = OpA::kSlots + OpB::kSlots;   // per wave
@@ -925,7 +957,7 @@ __device__ __forceinline__ void tile_product(const Params &p, int m0, int n0, ld
     OpA opa;
     OpB opb;
     opa.init(vq, hi, lane, p.lda, m_left, 0u, wm * FM);
-    opb.init(vq, hi, lane, p.ldb, n_left, (uint32_t)(kBuffers * A_BYTES), wn * FN);
+    opb.init(vq, hi, lane, p.ldb, n_left, (uint32_t)(kBuffers * A_BYTES), wn * FN, up_off);
 
     const int nk = (p.k + kStageK - 1) / kStageK;
     const int k_tail = p.k % kStageK;
@@ -938,7 +970,7 @@ __device__ __forceinline__ void tile_product(const Params &p, int m0, int n0, ld
         const int64_t ra = TA ? p.k : p.m, cla = TA ? p.m : p.k;
         const int64_t rb = TB ? p.n : p.k, clb = TB ? p.k : p.n;
         const int64_t end_a = (ra - 1) * p.lda * EB + ((cla * EB + 15) & ~(int64_t)15);
-        const int64_t end_b = (rb - 1) * p.ldb * EB + ((clb * EB + 15) & ~(int64_t)15);
+        const int64_t end_b = (rb - 1) * p.ldb * EB + ((clb * EB + 15) & ~(int64_t)15) + up_off;
         const int64_t off_a = TA ? (int64_t)m0 * EB : (int64_t)m0 * p.lda * EB;
         const int64_t off_b = TB ? (int64_t)n0 * p.ldb * EB : (int64_t)n0 * EB;
         ca.step = TA ? (int64_t)kStageK * p.lda * EB : kStageKBytes;

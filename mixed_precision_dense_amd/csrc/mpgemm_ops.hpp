@@ -18,6 +18,8 @@ enum OpMode {
     OP_SLOPE = 1,     // D = v act'(aux), column sums of D per tile
     OP_CE_STATS = 2,  // per row: maximum and sum of exponentials over the tile's columns
     OP_CE_PROBS = 3,  // D = (exp(v - lse) - [column == target]) * row weight
+    OP_GATED = 4,     // B is a pair: D = act(v + bias) * (v2 + bias2), both factors kept in aux
+    OP_GATED_GRAD = 5,  // D = v u act'(g) and v act(g) with g, u from aux, column sums of both per tile
 };
 // How the rows of a product are divided among experts.
 enum OpGroups {
@@ -68,6 +70,12 @@ struct OpParams {
     CeStat *stats;               // stats[row * parts + part]
     int parts;
     int col0;                    // vocabulary index of column 0
+    // gated products: elements from the gate's matrix to the up projection's of B, of aux (G, U), of D
+    // (OP_GATED_GRAD: dG, dU) and of colsum
+    int64_t stride_up, stride_aux, stride_du, stride_colsum;
+    const void *bias_up;         // of bias's type and stride
+    void *H;                     // OP_GATED_GRAD: receives act(g) u in the inputs' type, or nullptr
+    int64_t ldh;
 };
 
 // ------------------------------------------------------------------------------- launchers
@@ -80,11 +88,17 @@ int launch_slope_bf16(bool ta, bool tb, int tile, const OpParams &p, void *strea
 int launch_ce(bool bf16, int tile, const OpParams &p, void *stream);
 int launch_skinny_f16(bool ta, bool tb, int fm, int w, int waves, const OpParams &p, void *stream);
 int launch_skinny_bf16(bool ta, bool tb, int fm, int w, int waves, const OpParams &p, void *stream);
+int launch_gated_f16(bool tb, int tile, const OpParams &p, void *stream);
+int launch_gated_bf16(bool tb, int tile, const OpParams &p, void *stream);
+int launch_gated_grad_f16(bool tb, int tile, const OpParams &p, void *stream);
+int launch_gated_grad_bf16(bool tb, int tile, const OpParams &p, void *stream);
+int launch_gated_skinny(bool bf16, bool tb, int fm, int w, int waves, const OpParams &p, void *stream);
 // D = alpha A^T B in the inputs' type for p.k <= 128, A and B stored k x m and k x n; rows of B whose
 // p.target is negative are taken as zeros; no other operand
 int launch_outer(bool bf16, const OpParams &p, void *stream);
-// dbias from the tiles' partial column sums (rows_per_tile partial rows a tile)
-int launch_colsum(const OpParams &p, int tile_rows, int rows_per_tile, float *dbias, void *stream);
+// dbias from the tiles' partial column sums (rows_per_tile partial rows a tile); halves: 2 for a gated
+// product, whose second sums lie stride_colsum further and whose dbias are n and n values an expert
+int launch_colsum(const OpParams &p, int tile_rows, int rows_per_tile, int halves, float *dbias, void *stream);
 // loss and log-sum-exp from the row statistics; X and W give the target's logit
 int launch_ce_merge(bool bf16, const CeStat *stats, int parts, int m, int n, int k, float alpha,
                     const void *X, int64_t ldx, const void *W, int64_t ldw, const int64_t *target,

@@ -64,6 +64,12 @@ void set_slope(mpg::OpParams &p, mpgemm_act_t act, const void *Z, int64_t ldz, f
 mpgemm_status_t queued(int e) { return e == 0 ? MPGEMM_STATUS_SUCCESS : MPGEMM_STATUS_LAUNCH_FAILED; }
 
 mpgemm_status_t launch(const OpPlan &plan, bool bf16, bool ta, bool tb, const mpg::OpParams &p, void *stream) {
+    if (p.mode == mpg::OP_GATED) {
+        if (plan.skinny) return queued(mpg::launch_gated_skinny(bf16, tb, plan.fm, plan.w, plan.waves, p, stream));
+        return queued((bf16 ? mpg::launch_gated_bf16 : mpg::launch_gated_f16)(tb, plan.rows, p, stream));
+    }
+    if (p.mode == mpg::OP_GATED_GRAD)
+        return queued((bf16 ? mpg::launch_gated_grad_bf16 : mpg::launch_gated_grad_f16)(tb, plan.rows, p, stream));
     if (plan.skinny)
         return queued((bf16 ? mpg::launch_skinny_bf16 : mpg::launch_skinny_f16)(ta, tb, plan.fm, plan.w, plan.waves, p, stream));
     if (p.mode == mpg::OP_CE_STATS || p.mode == mpg::OP_CE_PROBS) return queued(mpg::launch_ce(bf16, plan.rows, p, stream));
@@ -73,7 +79,64 @@ mpgemm_status_t launch(const OpPlan &plan, bool bf16, bool ta, bool tb, const mp
 }
 
 mpgemm_status_t launch_dbias(const OpPlan &plan, const mpg::OpParams &p, float *dbias, void *stream) {
-    return queued(mpg::launch_colsum(p, plan.rows, plan.skinny ? 1 : 2, dbias, stream));
+    return queued(mpg::launch_colsum(p, plan.rows, plan.skinny ? 1 : 2, p.mode == mpg::OP_GATED_GRAD ? 2 : 1, dbias, stream));
+}
+
+void set_groups(mpg::OpParams &p, int64_t groups, const int32_t *offsets, int64_t stride_b) {
+    if (groups == 0) return;
+    p.groups_kind = mpg::GROUPS_ROWS;
+    p.groups = (int)groups;
+    p.offsets = offsets;
+    p.stride_b = stride_b;
+}
+
+// A checked gated product with something to compute; groups 0: one product.
+mpgemm_status_t run_gated(bool tb, int64_t groups, int64_t rows, int64_t n, int64_t k, float alpha, const void *A, mpgemm_dtype_t type,
+                          int64_t lda, const int32_t *offsets, const void *B, int64_t ldb, int64_t stride_b, int64_t stride_up,
+                          const mpgemm_gated_t *g, void *D, mpgemm_dtype_t d_type, int64_t ldd, void *stream) {
+    const OpPlan plan = gated_plan(groups, rows, n, k, tb, gated_weight(g->act, g->kept != nullptr));
+    mpg::OpParams p = product(plan, rows, n, k, alpha, A, lda, B, ldb, D, d_type == MPGEMM_R_32F, ldd);
+    p.mode = mpg::OP_GATED;
+    p.act = g->act;
+    p.stride_up = stride_up;
+    p.bias = g->bias_gate;
+    p.bias_up = g->bias_up;
+    p.bias_f32 = g->bias_type == MPGEMM_R_32F;
+    p.bias_stride = g->bias_stride;
+    p.aux = g->kept;
+    p.ld_aux = g->ld_kept;
+    p.stride_aux = g->stride_kept;
+    if (g->kept && (!lines(g->kept, g->ld_kept, 2) || g->stride_kept % 64)) p.lines = 0;
+    set_groups(p, groups, offsets, stride_b);
+    return launch(plan, type == MPGEMM_R_16BF, false, tb, p, stream);
+}
+
+mpgemm_status_t run_gated_grad(bool tb, int64_t groups, int64_t rows, int64_t n, int64_t k, float alpha, const void *A,
+                               mpgemm_dtype_t type, int64_t lda, const int32_t *offsets, const void *B, int64_t ldb, int64_t stride_b,
+                               const mpgemm_gated_grad_t *g, void *D, mpgemm_dtype_t d_type, int64_t ldd, int64_t stride_d,
+                               void *workspace, void *stream) {
+    const OpPlan plan = gated_grad_plan(groups, rows, n, k, gated_grad_weight(g->act, g->H != nullptr));
+    mpg::OpParams p = product(plan, rows, n, k, alpha, A, lda, B, ldb, D, d_type == MPGEMM_R_32F, ldd);
+    p.mode = mpg::OP_GATED_GRAD;
+    p.act = g->act;
+    p.aux = const_cast<void *>(g->kept);
+    p.ld_aux = g->ld_kept;
+    p.stride_aux = g->stride_kept;
+    p.stride_du = stride_d;
+    p.H = g->H;
+    p.ldh = g->ldh;
+    if ((stride_d * (p.d_f32 ? 4 : 2)) % 128 || (g->H && !lines(g->H, g->ldh, 2))) p.lines = 0;
+    p.colsum = g->dbias ? (float *)workspace : nullptr;
+    p.ld_colsum = round8(n);
+    p.stride_colsum = colsum_rows(groups > 0 ? groups : 1, rows) * p.ld_colsum;
+    set_groups(p, groups, offsets, stride_b);
+    if (rows == 0) {
+        p.tiles_m = 0;   // no rows: only their sums are written
+    } else {
+        const mpgemm_status_t st = launch(plan, type == MPGEMM_R_16BF, false, tb, p, stream);
+        if (st != MPGEMM_STATUS_SUCCESS) return st;
+    }
+    return g->dbias ? launch_dbias(plan, p, g->dbias, stream) : MPGEMM_STATUS_SUCCESS;
 }
 
 }  // namespace
@@ -293,6 +356,61 @@ mpgemm_status_t mpgemm_run_linear_ce_grad(mpgemm_handle_t handle, int64_t m, int
     if (!dX) return MPGEMM_STATUS_SUCCESS;
     return queued(mpg::launch_sum_parts(bf16, part, L.splits, m * ld_part, ld_part, rows.place, (int)m, (int)k, *alpha, rows.scale, dX,
                                         lddx, stream));
+}
+
+mpgemm_status_t mpgemm_run_gated(mpgemm_handle_t handle, mpgemm_op_t transb, int64_t m, int64_t n, int64_t k, const float *alpha,
+                                 const void *A, mpgemm_dtype_t a_type, int64_t lda, const void *B, mpgemm_dtype_t b_type,
+                                 int64_t ldb, int64_t stride_up, const mpgemm_gated_t *gated, void *D, mpgemm_dtype_t d_type,
+                                 int64_t ldd, void *stream) {
+    if (!handle || !handle_live(handle)) return MPGEMM_STATUS_NOT_INITIALIZED;
+    MPGEMM_TRY(mpgemm_check_gated(transb, m, n, k, alpha, A, a_type, lda, B, b_type, ldb, stride_up, gated, D, d_type, ldd));
+    if (m == 0 || n == 0) return MPGEMM_STATUS_SUCCESS;
+    MPGEMM_TRY(handle_on_device(handle));
+    return run_gated(transb == MPGEMM_OP_T, 0, m, n, k, *alpha, A, a_type, lda, nullptr, B, ldb, 0, stride_up, gated, D, d_type, ldd,
+                     stream);
+}
+
+mpgemm_status_t mpgemm_run_grouped_gated(mpgemm_handle_t handle, mpgemm_op_t transb, int64_t groups, int64_t rows, int64_t n,
+                                         int64_t k, const float *alpha, const void *A, mpgemm_dtype_t a_type, int64_t lda,
+                                         const int32_t *offsets, const void *B, mpgemm_dtype_t b_type, int64_t ldb,
+                                         int64_t stride_b, int64_t stride_up, const mpgemm_gated_t *gated, void *D,
+                                         mpgemm_dtype_t d_type, int64_t ldd, void *stream) {
+    if (!handle || !handle_live(handle)) return MPGEMM_STATUS_NOT_INITIALIZED;
+    MPGEMM_TRY(mpgemm_check_grouped_gated(transb, groups, rows, n, k, alpha, A, a_type, lda, offsets, B, b_type, ldb, stride_b,
+                                          stride_up, gated, D, d_type, ldd));
+    if (groups == 0 || rows == 0 || n == 0) return MPGEMM_STATUS_SUCCESS;
+    MPGEMM_TRY(handle_on_device(handle));
+    return run_gated(transb == MPGEMM_OP_T, groups, rows, n, k, *alpha, A, a_type, lda, offsets, B, ldb, stride_b, stride_up, gated, D,
+                     d_type, ldd, stream);
+}
+
+mpgemm_status_t mpgemm_run_gated_grad(mpgemm_handle_t handle, mpgemm_op_t transb, int64_t m, int64_t n, int64_t k,
+                                      const float *alpha, const void *A, mpgemm_dtype_t a_type, int64_t lda, const void *B,
+                                      mpgemm_dtype_t b_type, int64_t ldb, const mpgemm_gated_grad_t *grad, void *D,
+                                      mpgemm_dtype_t d_type, int64_t ldd, int64_t stride_d, void *workspace,
+                                      uint64_t workspace_bytes, void *stream) {
+    if (!handle || !handle_live(handle)) return MPGEMM_STATUS_NOT_INITIALIZED;
+    MPGEMM_TRY(mpgemm_check_gated_grad(transb, m, n, k, alpha, A, a_type, lda, B, b_type, ldb, grad, D, d_type, ldd, stride_d,
+                                       workspace, workspace_bytes));
+    if (n == 0 || (m == 0 && !grad->dbias)) return MPGEMM_STATUS_SUCCESS;
+    MPGEMM_TRY(handle_on_device(handle));
+    return run_gated_grad(transb == MPGEMM_OP_T, 0, m, n, k, *alpha, A, a_type, lda, nullptr, B, ldb, 0, grad, D, d_type, ldd, stride_d,
+                          workspace, stream);
+}
+
+mpgemm_status_t mpgemm_run_grouped_gated_grad(mpgemm_handle_t handle, mpgemm_op_t transb, int64_t groups, int64_t rows, int64_t n,
+                                              int64_t k, const float *alpha, const void *A, mpgemm_dtype_t a_type, int64_t lda,
+                                              const int32_t *offsets, const void *B, mpgemm_dtype_t b_type, int64_t ldb,
+                                              int64_t stride_b, const mpgemm_gated_grad_t *grad, void *D, mpgemm_dtype_t d_type,
+                                              int64_t ldd, int64_t stride_d, void *workspace, uint64_t workspace_bytes,
+                                              void *stream) {
+    if (!handle || !handle_live(handle)) return MPGEMM_STATUS_NOT_INITIALIZED;
+    MPGEMM_TRY(mpgemm_check_grouped_gated_grad(transb, groups, rows, n, k, alpha, A, a_type, lda, offsets, B, b_type, ldb, stride_b,
+                                               grad, D, d_type, ldd, stride_d, workspace, workspace_bytes));
+    if (groups == 0 || n == 0 || (rows == 0 && !grad->dbias)) return MPGEMM_STATUS_SUCCESS;
+    MPGEMM_TRY(handle_on_device(handle));
+    return run_gated_grad(transb == MPGEMM_OP_T, groups, rows, n, k, *alpha, A, a_type, lda, offsets, B, ldb, stride_b, grad, D, d_type,
+                          ldd, stride_d, workspace, stream);
 }
 
 }  // extern "C"

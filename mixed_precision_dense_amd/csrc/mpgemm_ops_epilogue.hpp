@@ -101,6 +101,31 @@ __device__ __forceinline__ float act_slope(float z) {
     return __builtin_fmaf(__builtin_fmaf(-g, g, g), cut(z), g);
 }
 
+// Both at once, from one exponential and one reciprocal.  z may have been kept in 16 bits, where a large
+// negative value is -infinity: a factor that the sigmoid's 0 multiplies is cut, so that the value is 0 and
+// no 0 * inf (NaN comes through the sigmoid).
+template <int ACT>
+__device__ __forceinline__ void act_both(float z, float &value, float &slope) {
+    if constexpr (ACT == ACT_GELU) {
+        float bell;
+        const float tail = normal_tail(z, bell);
+        value = __builtin_fmaf(-__builtin_fminf(__builtin_fabsf(z), 30.0f), tail, __builtin_fmaxf(z, 0.0f));
+        slope = __builtin_fmaf(cut(z) * 0.39894228040143268f, bell, z > 0.0f ? 1.0f - tail : tail);
+    } else if constexpr (ACT == ACT_GELU_TANH) {
+        const float g = sigmoid(z * __builtin_fmaf(2.0f * kGeluC * kGeluA * z, z, 2.0f * kGeluC));
+        const float c = cut(z);
+        value = __builtin_fmaxf(z, -1.0e4f) * g;
+        slope = __builtin_fmaf(__builtin_fmaf(-g, g, g) * c, __builtin_fmaf(6.0f * kGeluC * kGeluA * c, c, 2.0f * kGeluC), g);
+    } else if constexpr (ACT == ACT_SILU) {
+        const float g = sigmoid(z);
+        value = __builtin_fmaxf(z, -1.0e4f) * g;
+        slope = __builtin_fmaf(__builtin_fmaf(-g, g, g), cut(z), g);
+    } else {
+        value = act_value<ACT, false>(z);
+        slope = act_slope<ACT>(z);
+    }
+}
+
 // Calls f(std::integral_constant<int, ACT>, std::bool_constant<SHORT>) for the activation named at
 // run time and whether its long form is needed (both uniform).
 template <typename F>
@@ -170,7 +195,7 @@ struct OpTile {
 };
 
 // What an epilogue reads besides the product: eight columns of C or of the kept Z, as stored (hi: the
-// last four of FP32 values).
+// last four of FP32 values), or of a gated product's kept G and U (hi).
 struct ChunkIn {
     u32x4 lo, hi;
 };
@@ -249,16 +274,20 @@ __device__ __forceinline__ void store8(const OpOut &o, int f32, int row, int c, 
 }
 
 // The bias of columns col .. col + 7 (zeros where there is none).
-template <int IN, int MODE>
-__device__ __forceinline__ void bias_load(const OpParams &p, int expert, int col, float (&b)[8]) {
+template <int IN>
+__device__ __forceinline__ void bias_of(const OpParams &p, const void *bias, int expert, int col, float (&b)[8]) {
 #pragma unroll
     for (int q = 0; q < 8; ++q) b[q] = 0.0f;
-    if (MODE != OP_FORWARD || p.bias == nullptr) return;
+    if (bias == nullptr) return;
     const int64_t at = (int64_t)expert * p.bias_stride + col;
 #pragma unroll
     for (int q = 0; q < 8; ++q)
         if (col + q < p.n)
-            b[q] = p.bias_f32 ? ((const float *)p.bias)[at + q] : widen<IN>(((const uint16_t *)p.bias)[at + q]);
+            b[q] = p.bias_f32 ? ((const float *)bias)[at + q] : widen<IN>(((const uint16_t *)bias)[at + q]);
+}
+template <int IN, int MODE>
+__device__ __forceinline__ void bias_load(const OpParams &p, int expert, int col, float (&b)[8]) {
+    bias_of<IN>(p, MODE == OP_FORWARD ? p.bias : nullptr, expert, col, b);
 }
 
 // alpha, times the device factor where there is one.
@@ -370,6 +399,82 @@ __device__ __forceinline__ void rows_finish(const OpParams &p, float alpha, cons
     }
 #pragma unroll
     for (int i = 0; i < G; ++i) store8<IN>(d, p.d_f32, row(i), c, ncol(i), whole, nt, v[i]);
+}
+
+// ------------------------------------------------------------------------------- gated products
+// The outputs of a gated product's tile: D and both kept factors, or dG, dU and H.
+struct GatedOut {
+    OpOut d, g, u;
+};
+
+// rows_finish for a gated product: v holds the gate's products, x the up projection's.  D is stored to
+// out.d, the factors (where p.aux is set) to out.g and out.u.
+template <int IN, int G, typename Row, typename Cols>
+__device__ __forceinline__ void gated_finish(const OpParams &p, const GatedOut &out, int c, bool whole, bool nt, Row &&row,
+                                             Cols &&ncol, const float (&bias)[8], const float (&bias_up)[8], float (&v)[G][8],
+                                             float (&x)[G][8]) {
+#pragma unroll
+    for (int i = 0; i < G; ++i)
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+            v[i][q] = __builtin_fmaf(p.alpha, v[i][q], bias[q]);
+            x[i][q] = __builtin_fmaf(p.alpha, x[i][q], bias_up[q]);
+        }
+    if (p.aux != nullptr) {
+#pragma unroll
+        for (int i = 0; i < G; ++i) {
+            store8<IN>(out.g, 0, row(i), c, ncol(i), whole, nt, v[i]);
+            store8<IN>(out.u, 0, row(i), c, ncol(i), whole, nt, x[i]);
+        }
+    }
+    // (GELU in its long form throughout: the other factor may be large, so that a tail that 16 bits would
+    // round to nothing by itself is not nothing in the product)
+    with_act(p.act, true, [&](auto a, auto) {
+#pragma unroll
+        for (int i = 0; i < G; ++i) {
+#pragma unroll
+            for (int q = 0; q < 8; ++q) v[i][q] = act_value<decltype(a)::value, false>(v[i][q]) * x[i][q];
+            if (i % 2 == 1) __builtin_amdgcn_sched_barrier(0);
+        }
+    });
+#pragma unroll
+    for (int i = 0; i < G; ++i) store8<IN>(out.d, p.d_f32, row(i), c, ncol(i), whole, nt, v[i]);
+}
+
+// The gradient: v holds the products E, in the kept G and U (lo, hi).  dG goes to out.d, dU to out.u and
+// H (where p.H is set) to out.g; sums and sums_up add up dG and dU before their rounding.
+template <int IN, int G, typename Row, typename Cols>
+__device__ __forceinline__ void gated_grad_finish(const OpParams &p, const GatedOut &out, int c, bool whole, bool nt, Row &&row,
+                                                  Cols &&ncol, const ChunkIn (&in)[G], float (&v)[G][8], float (&sums)[8],
+                                                  float (&sums_up)[8]) {
+#pragma unroll
+    for (int i = 0; i < G; ++i) {
+        float g[8], u[8], du[8], h[8];
+        widen8<IN>(in[i].lo, g);
+        widen8<IN>(in[i].hi, u);
+        with_act(p.act, true, [&](auto a, auto) {
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+                float value, slope;
+                act_both<decltype(a)::value>(g[q], value, slope);
+                const float e = p.alpha * v[i][q];
+                du[q] = e * value;
+                h[q] = value * u[q];
+                v[i][q] = e * u[q] * slope;
+            }
+        });
+        if (p.colsum != nullptr) {
+            const bool live = whole || ncol(i) > 0;
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+                sums[q] += live ? v[i][q] : 0.0f;
+                sums_up[q] += live ? du[q] : 0.0f;
+            }
+        }
+        store8<IN>(out.d, p.d_f32, row(i), c, ncol(i), whole, nt, v[i]);
+        store8<IN>(out.u, p.d_f32, row(i), c, ncol(i), whole, nt, du);
+        if (p.H != nullptr) store8<IN>(out.g, 0, row(i), c, ncol(i), whole, nt, h);
+    }
 }
 
 // ------------------------------------------------------------------------------- experts' rows

@@ -120,6 +120,33 @@ OpPlan grouped_plan(int64_t rows, int64_t groups, int64_t n, int64_t k, bool tb,
     return p;
 }
 
+double gated_weight(int act, bool kept) { return 0.5 * forward_weight(act, false, false) + (kept ? 0.7 : 0.0); }
+double gated_grad_weight(int act, bool h) { return slope_weight(act) + 1.5 + (h ? 0.7 : 0.0); }
+
+OpPlan gated_plan(int64_t groups, int64_t rows, int64_t n, int64_t k, bool tb, double weight) {
+    const int64_t owners = groups < rows ? groups : rows;   // an expert's last tile may be short
+    const int64_t mean = groups > 0 ? ceil_div(rows, groups) : rows;
+    auto few = [&](int fm, int w) { return skinny(groups > 0 ? rows / (16 * fm) + owners : 1, n, fm, w); };
+    if (mean <= (groups > 0 ? 10 : 16) && n <= ((int64_t)1 << 22)) return few(1, tb ? 1 : 2);
+    if (mean <= 32 && few(2, 2).tiles_m * ceil_div(n, 32) <= 384) return few(2, 2);
+    if (groups == 0 && rows <= 64 && ceil_div(n, 32) <= kCus) return few(4, 2);
+    // (an edge's tile holds half as many outputs a row; half a tile per expert is lost on average)
+    const int e = best_edge(k, weight, [&](int64_t t) {
+        return (groups > 0 ? rows / t + owners / 2 : ceil_div(rows, t)) * ceil_div(n, t / 2);
+    });
+    return OpPlan{false, 0, 0, 0, e, e / 2, groups > 0 ? rows / e + owners : ceil_div(rows, e), ceil_div(n, e / 2)};
+}
+
+OpPlan gated_grad_plan(int64_t groups, int64_t rows, int64_t n, int64_t k, double weight) {
+    const int64_t owners = groups < rows ? groups : rows;
+    const int e = best_edge(k, weight, [&](int64_t t) {
+        return (groups > 0 ? rows / t + owners / 2 : ceil_div(rows, t)) * ceil_div(n, t);
+    });
+    OpPlan p = tiled(rows, n, e);
+    if (groups > 0) p.tiles_m = rows / e + owners;
+    return p;
+}
+
 OpPlan wgrad_plan(int64_t groups, int64_t rows, int64_t m, int64_t n) {
     return tiled(m, n, best_edge(rows / (groups > 0 ? groups : 1), 0.0,
                                  [&](int64_t e) { return groups * ceil_div(m, e) * ceil_div(n, e); }));
@@ -399,6 +426,141 @@ mpgemm_status_t mpgemm_check_linear_ce_grad(int64_t m, int64_t n, int64_t k, con
     if (dX && (!aligned(dX, 16) || !stride_ok(lddx, 2))) return MPGEMM_STATUS_NOT_SUPPORTED;
     if (dW && (!aligned(dW, 16) || !stride_ok(lddw, 2))) return MPGEMM_STATUS_NOT_SUPPORTED;
     return m == 0 ? MPGEMM_STATUS_SUCCESS : check_workspace(workspace, workspace_bytes, L.total);
+}
+
+namespace {
+
+// A pair of matrices `stride` elements apart: how far, and (for one that is written) that it does not overlap itself.
+constexpr int64_t kMaxStride = INT64_MAX / 131072;
+mpgemm_status_t check_pair(int64_t m, int64_t n, int64_t ld, int64_t stride, int eb, bool written) {
+    if (stride < 0) return MPGEMM_STATUS_INVALID_VALUE;
+    if (stride > kMaxStride || (stride * eb) % 16) return MPGEMM_STATUS_NOT_SUPPORTED;
+    if (!written) return MPGEMM_STATUS_SUCCESS;
+    // (of sizes and leading dimensions that have been checked: no overflow)
+    const bool beside = stride >= n && stride <= ld - n, after = stride >= (m - 1) * ld + n;
+    return beside || after ? MPGEMM_STATUS_SUCCESS : MPGEMM_STATUS_INVALID_VALUE;
+}
+
+// What the four gated calls share: sizes, types, operands and where D goes.  groups < 0: one product.
+struct GatedArgs {
+    mpgemm_op_t transb;
+    int64_t groups, rows, n, k;
+    const float *alpha;
+    const void *A;
+    mpgemm_dtype_t a_type;
+    int64_t lda;
+    const int32_t *offsets;
+    const void *B;
+    mpgemm_dtype_t b_type;
+    int64_t ldb, stride_b;
+    const void *D;
+    mpgemm_dtype_t d_type;
+    int64_t ldd;
+    bool empty() const { return groups == 0 || rows == 0 || n == 0; }
+};
+
+mpgemm_status_t check_gated_sizes(const GatedArgs &a) {
+    if (!op_valid(a.transb) || a.rows < 0 || a.n < 0 || a.k < 0 || !a.alpha || a.stride_b < 0) return MPGEMM_STATUS_INVALID_VALUE;
+    MPGEMM_TRY(check_types(a.a_type, a.b_type, a.d_type));
+    const bool tb = a.transb == MPGEMM_OP_T;
+    if (a.lda < at_least1(a.k) || a.ldb < at_least1(tb ? a.k : a.n) || a.ldd < at_least1(a.n)) return MPGEMM_STATUS_INVALID_VALUE;
+    return MPGEMM_STATUS_SUCCESS;
+}
+
+mpgemm_status_t check_gated_operands(const GatedArgs &a, const OpPlan &plan) {
+    if (!a.D || (a.groups > 0 && !a.offsets) || (a.k > 0 && (!a.A || !a.B))) return MPGEMM_STATUS_INVALID_VALUE;
+    if (a.rows > kOpMaxSize || a.n > kOpMaxSize || a.k > kOpMaxSize || a.groups > 65535 || !launchable(plan, 1))
+        return MPGEMM_STATUS_NOT_SUPPORTED;
+    if ((a.k > 0 && (!aligned(a.A, 16) || !aligned(a.B, 16))) || !aligned(a.D, 16) || (a.groups > 0 && !aligned(a.offsets, 4)))
+        return MPGEMM_STATUS_NOT_SUPPORTED;
+    if (!stride_ok(a.lda, 2) || !stride_ok(a.ldb, 2) || !stride_ok(a.ldd, elem_bytes(a.d_type)) || a.stride_b % 8 ||
+        a.stride_b > kMaxStride)
+        return MPGEMM_STATUS_NOT_SUPPORTED;
+    return MPGEMM_STATUS_SUCCESS;
+}
+
+mpgemm_status_t check_gated_call(const GatedArgs &a, int64_t stride_up, const mpgemm_gated_t *g) {
+    MPGEMM_TRY(check_gated_sizes(a));
+    if (!g || !act_valid(g->act) || stride_up < 0) return MPGEMM_STATUS_INVALID_VALUE;
+    if ((g->bias_gate || g->bias_up) && !out_type(g->bias_type, a.a_type)) return MPGEMM_STATUS_NOT_SUPPORTED;
+    if ((g->bias_gate || g->bias_up) && a.groups >= 0 && g->bias_stride < 0) return MPGEMM_STATUS_INVALID_VALUE;
+    if (g->kept && g->ld_kept < at_least1(a.n)) return MPGEMM_STATUS_INVALID_VALUE;
+    if (a.empty()) return MPGEMM_STATUS_SUCCESS;
+    const bool sized = a.rows <= kOpMaxSize && a.n <= kOpMaxSize && a.k <= kOpMaxSize && a.groups <= 65535;
+    if (!sized) return a.D ? MPGEMM_STATUS_NOT_SUPPORTED : MPGEMM_STATUS_INVALID_VALUE;
+    const int64_t groups = a.groups > 0 ? a.groups : 0;
+    MPGEMM_TRY(check_gated_operands(a, gated_plan(groups, a.rows, a.n, a.k, a.transb == MPGEMM_OP_T, gated_weight(g->act, g->kept != nullptr))));
+    if (stride_up % 8 || stride_up > ((int64_t)1 << 30) || 256 * 2 * a.ldb + 2 * stride_up > ((int64_t)1 << 31) - 4096)
+        return MPGEMM_STATUS_NOT_SUPPORTED;
+    const unsigned be = g->bias_type == MPGEMM_R_32F ? 4 : 2;
+    if (!aligned(g->bias_gate, be) || !aligned(g->bias_up, be) || ((g->bias_gate || g->bias_up) && g->bias_stride > kMaxStride && a.groups > 0))
+        return MPGEMM_STATUS_NOT_SUPPORTED;
+    if (!g->kept) return MPGEMM_STATUS_SUCCESS;
+    if (!aligned(g->kept, 16) || !stride_ok(g->ld_kept, 2)) return MPGEMM_STATUS_NOT_SUPPORTED;
+    return check_pair(a.rows, a.n, g->ld_kept, g->stride_kept, 2, true);
+}
+
+mpgemm_status_t check_gated_grad_call(const GatedArgs &a, const mpgemm_gated_grad_t *g, int64_t stride_d, const void *workspace,
+                                      uint64_t workspace_bytes) {
+    MPGEMM_TRY(check_gated_sizes(a));
+    if (!g || !act_valid(g->act)) return MPGEMM_STATUS_INVALID_VALUE;
+    if (g->ld_kept < at_least1(a.n) || (g->H && g->ldh < at_least1(a.n))) return MPGEMM_STATUS_INVALID_VALUE;
+    if (a.groups == 0 || a.n == 0 || (a.rows == 0 && !g->dbias)) return MPGEMM_STATUS_SUCCESS;
+    if (a.rows > kOpMaxSize || a.n > kOpMaxSize || a.k > kOpMaxSize || a.groups > 65535 || !aligned(g->dbias, 4))
+        return MPGEMM_STATUS_NOT_SUPPORTED;
+    if (a.rows == 0)   // (the sum of no rows is written)
+        return a.groups > 0 && !a.offsets ? MPGEMM_STATUS_INVALID_VALUE : MPGEMM_STATUS_SUCCESS;
+    if (!g->kept) return MPGEMM_STATUS_INVALID_VALUE;
+    const int64_t groups = a.groups > 0 ? a.groups : 0;
+    MPGEMM_TRY(check_gated_operands(a, gated_grad_plan(groups, a.rows, a.n, a.k, gated_grad_weight(g->act, g->H != nullptr))));
+    if (!aligned(g->kept, 16) || !stride_ok(g->ld_kept, 2) || (g->H && (!aligned(g->H, 16) || !stride_ok(g->ldh, 2))))
+        return MPGEMM_STATUS_NOT_SUPPORTED;
+    MPGEMM_TRY(check_pair(a.rows, a.n, g->ld_kept, g->stride_kept, 2, false));
+    MPGEMM_TRY(check_pair(a.rows, a.n, a.ldd, stride_d, elem_bytes(a.d_type), true));
+    return g->dbias ? check_workspace(workspace, workspace_bytes, mpgemm_gated_grad_workspace_size(a.groups > 0 ? a.groups : 1, a.rows, a.n))
+                    : MPGEMM_STATUS_SUCCESS;
+}
+
+}  // namespace
+
+uint64_t mpgemm_gated_grad_workspace_size(int64_t groups, int64_t m, int64_t n) {
+    return 2 * mpgemm_epilogue_grad_workspace_size(groups, m, n);
+}
+
+mpgemm_status_t mpgemm_check_gated(mpgemm_op_t transb, int64_t m, int64_t n, int64_t k, const float *alpha, const void *A,
+                                   mpgemm_dtype_t a_type, int64_t lda, const void *B, mpgemm_dtype_t b_type, int64_t ldb,
+                                   int64_t stride_up, const mpgemm_gated_t *gated, const void *D, mpgemm_dtype_t d_type,
+                                   int64_t ldd) {
+    return check_gated_call({transb, -1, m, n, k, alpha, A, a_type, lda, nullptr, B, b_type, ldb, 0, D, d_type, ldd}, stride_up, gated);
+}
+
+mpgemm_status_t mpgemm_check_grouped_gated(mpgemm_op_t transb, int64_t groups, int64_t rows, int64_t n, int64_t k,
+                                           const float *alpha, const void *A, mpgemm_dtype_t a_type, int64_t lda,
+                                           const int32_t *offsets, const void *B, mpgemm_dtype_t b_type, int64_t ldb,
+                                           int64_t stride_b, int64_t stride_up, const mpgemm_gated_t *gated, const void *D,
+                                           mpgemm_dtype_t d_type, int64_t ldd) {
+    if (groups < 0) return MPGEMM_STATUS_INVALID_VALUE;
+    return check_gated_call({transb, groups, rows, n, k, alpha, A, a_type, lda, offsets, B, b_type, ldb, stride_b, D, d_type, ldd},
+                            stride_up, gated);
+}
+
+mpgemm_status_t mpgemm_check_gated_grad(mpgemm_op_t transb, int64_t m, int64_t n, int64_t k, const float *alpha, const void *A,
+                                        mpgemm_dtype_t a_type, int64_t lda, const void *B, mpgemm_dtype_t b_type, int64_t ldb,
+                                        const mpgemm_gated_grad_t *grad, const void *D, mpgemm_dtype_t d_type, int64_t ldd,
+                                        int64_t stride_d, const void *workspace, uint64_t workspace_bytes) {
+    return check_gated_grad_call({transb, -1, m, n, k, alpha, A, a_type, lda, nullptr, B, b_type, ldb, 0, D, d_type, ldd}, grad, stride_d,
+                                 workspace, workspace_bytes);
+}
+
+mpgemm_status_t mpgemm_check_grouped_gated_grad(mpgemm_op_t transb, int64_t groups, int64_t rows, int64_t n, int64_t k,
+                                                const float *alpha, const void *A, mpgemm_dtype_t a_type, int64_t lda,
+                                                const int32_t *offsets, const void *B, mpgemm_dtype_t b_type, int64_t ldb,
+                                                int64_t stride_b, const mpgemm_gated_grad_t *grad, const void *D,
+                                                mpgemm_dtype_t d_type, int64_t ldd, int64_t stride_d, const void *workspace,
+                                                uint64_t workspace_bytes) {
+    if (groups < 0) return MPGEMM_STATUS_INVALID_VALUE;
+    return check_gated_grad_call({transb, groups, rows, n, k, alpha, A, a_type, lda, offsets, B, b_type, ldb, stride_b, D, d_type, ldd},
+                                 grad, stride_d, workspace, workspace_bytes);
 }
 
 }  // extern "C"

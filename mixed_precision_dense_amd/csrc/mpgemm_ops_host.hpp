@@ -26,6 +26,11 @@ OpPlan op_plan(int64_t m, int64_t n, int64_t k, bool tb, double weight);
 // A product of `rows` rows divided among `groups` experts; tiles_m is the most row tiles that
 // any division can take.
 OpPlan grouped_plan(int64_t rows, int64_t groups, int64_t n, int64_t k, bool tb, double weight);
+// A gated product of n outputs a row, and its gradient; groups 0: one product, else of experts' rows.
+OpPlan gated_plan(int64_t groups, int64_t rows, int64_t n, int64_t k, bool tb, double weight);
+OpPlan gated_grad_plan(int64_t groups, int64_t rows, int64_t n, int64_t k, double weight);
+double gated_weight(int act, bool kept);
+double gated_grad_weight(int act, bool h);
 // The products of each expert's rows summed: D is m x n for each.
 OpPlan wgrad_plan(int64_t groups, int64_t rows, int64_t m, int64_t n);
 

@@ -11,8 +11,13 @@
 // wave per SIMD nothing else covers a step's latencies (8192 x 8192 x 2048 without an activation:
 // 264 us step by step, 227 in groups, 207 with the present stores).
 //
-// What the epilogue reads (C, or the kept Z) comes by direct-to-LDS loads through a ring in the
-// wave's region, up to four groups ahead of its use and without holding a register.
+// What the epilogue reads (C, the kept Z, or a gated product's kept G and U) comes by direct-to-LDS
+// loads through a ring in the wave's region, up to four groups ahead of its use and without holding a
+// register.
+//
+// A gated product's tile takes half its columns from the gate's weights and half from the up
+// projection's, so that a 256-wide tile is the same product with the same K loop and its outputs are 256 x
+// 128: each wave holds both factors of 64 columns, which meet in its staged rows.
 #pragma once
 
 #include "mpgemm_ops_epilogue.hpp"
@@ -67,15 +72,16 @@ __device__ __forceinline__ void op_store_tile(const OpParams &p, const OpTile &w
     auto cols_of = [&](int row) { return full ? 8 : (row < w.m ? ncol : 0); };
 
     // The ring: a step's 16 bytes a lane (16-bit values) or twice that (FP32 C, half as many groups).
-    const bool read_c = MODE == OP_FORWARD && p.C != nullptr, read_z = MODE == OP_SLOPE && p.aux != nullptr;
-    const bool wide = read_c && p.c_f32;
+    constexpr bool kPair = MODE == OP_GATED_GRAD;               // two 16-byte pieces from two places
+    const bool read_c = MODE == OP_FORWARD && p.C != nullptr, read_z = kPair || (MODE == OP_SLOPE && p.aux != nullptr);
+    const bool wide = kPair || (read_c && p.c_f32);
     const int loads = read_c || read_z ? (wide ? 2 : 1) : 0;    // per step
     const int depth = wide ? (kDepth > 1 ? kDepth / 2 : 1) : kDepth;
     const int64_t src_ld = read_c ? p.ldc : p.ld_aux;
-    const int src_bytes = wide ? 4 : 2;
+    const int src_bytes = !kPair && wide ? 4 : 2;
     const char *src = (const char *)(read_c ? p.C : p.aux) +
                       ((read_c ? w.d_off : 0) + ((int64_t)w.row0 + row_t) * src_ld + w.tn * BN + wn * WC) * src_bytes;
-    const i32x4 rs = make_rsrc_words(src);
+    const i32x4 rs = make_rsrc_words(src), rs_up = make_rsrc_words(src + (kPair ? p.stride_aux * 2 : 0));
     const uint32_t ring_addr = (uint32_t)(uintptr_t)ring;
     auto fetch = [&](int group) {                  // loads of a group into its place of the ring
         const uint32_t at = ring_addr + (uint32_t)(group % depth * G * loads) * 1024u;
@@ -85,7 +91,10 @@ __device__ __forceinline__ void op_store_tile(const OpParams &p, const OpTile &w
             const uint32_t off = (uint32_t)row * (uint32_t)(src_ld * src_bytes) + (uint32_t)(8 * c * src_bytes);
             const int nc = cols_of(row_t + row);
             dma16(rs, nc > 0 ? off : kOobOffset, 0u, at + (uint32_t)(q * loads) * 1024u);
-            if (wide) dma16(rs, nc > 4 ? off + 16u : kOobOffset, 0u, at + (uint32_t)(q * loads + 1) * 1024u);
+            if (kPair)
+                dma16(rs_up, nc > 0 ? off : kOobOffset, 0u, at + (uint32_t)(q * loads + 1) * 1024u);
+            else if (wide)
+                dma16(rs, nc > 4 ? off + 16u : kOobOffset, 0u, at + (uint32_t)(q * loads + 1) * 1024u);
         }
     };
     // the wave's sub-tile of D and of the Z that is kept
@@ -93,11 +102,13 @@ __device__ __forceinline__ void op_store_tile(const OpParams &p, const OpTile &w
     const int col_d = w.tn * BN + wn * WC;
     const OpOut out_d = op_out(p.D, w.d_off + row_d * p.ldd + col_d, p.ldd, p.d_f32 ? 4 : 2);
     const OpOut out_z = op_out(p.aux, row_d * p.ld_aux + col_d, p.ld_aux, 2);
+    const GatedOut out_pair = {out_d, op_out(p.H, row_d * p.ldh + col_d, p.ldh, 2),
+                               op_out(p.D, p.stride_du + row_d * p.ldd + col_d, p.ldd, p.d_f32 ? 4 : 2)};
     const float alpha = op_alpha(p);
-    float bias[8], sums[8];
+    float bias[8], sums[8], sums_up[8];
     bias_load<IN, MODE>(p, w.expert, col, bias);
 #pragma unroll
-    for (int q = 0; q < 8; ++q) sums[q] = 0.0f;
+    for (int q = 0; q < 8; ++q) sums[q] = sums_up[q] = 0.0f;
     // The loads below are counted: nothing the compiler has issued may be waited for later on.
     if (loads > 0) {
         wait_vmem<0>();
@@ -128,7 +139,8 @@ __device__ __forceinline__ void op_store_tile(const OpParams &p, const OpTile &w
     }
     // Operations that may be in flight when a group's loads have landed: the loads of the groups
     // after it and, in a whole tile (where none is masked off), the stores since.
-    const int stores = full && loads > 0 ? G * ((p.d_f32 ? 2 : 1) + (MODE == OP_FORWARD && p.aux != nullptr ? 1 : 0)) : 0;
+    const int kept = (MODE == OP_FORWARD && p.aux != nullptr) || (kPair && p.H != nullptr) ? 1 : 0;
+    const int stores = full && loads > 0 ? G * ((p.d_f32 ? 2 : 1) * (kPair ? 2 : 1) + kept) : 0;
 
 #pragma unroll 1
     for (int pass = 0; pass < FM / kBR; ++pass) {
@@ -185,26 +197,108 @@ __device__ __forceinline__ void op_store_tile(const OpParams &p, const OpTile &w
                 }
             }
             const int row_s = (pass * kSteps + s) * RI + rr;
-            rows_finish<IN, MODE, G>(
-                p, alpha, out_d, out_z, 8 * c, full, nt, [&](int q) { return row_s + q * RI; },
-                [&](int q) { return cols_of(row_t + row_s + q * RI); }, in, scale, bias, v, sums);
+            auto row_at = [&](int q) { return row_s + q * RI; };
+            auto cols_at = [&](int q) { return cols_of(row_t + row_s + q * RI); };
+            if constexpr (kPair)
+                gated_grad_finish<IN, G>(p, out_pair, 8 * c, full, nt, row_at, cols_at, in, v, sums, sums_up);
+            else
+                rows_finish<IN, MODE, G>(p, alpha, out_d, out_z, 8 * c, full, nt, row_at, cols_at, in, scale, bias, v, sums);
             if (loads > 0 && group + depth < kGroups) {
                 wait_lds<0>();                     // the group's place has been read
                 fetch(group + depth);
             }
         }
     }
-    if (MODE == OP_SLOPE && p.colsum != nullptr && w.tile < p.tiles_m) {
+    if ((MODE == OP_SLOPE || kPair) && p.colsum != nullptr && w.tile < p.tiles_m) {
+        auto join = [&](float (&s)[8], int64_t half) {
 #pragma unroll
-        for (int q = 0; q < 8; ++q)
+            for (int q = 0; q < 8; ++q)
 #pragma unroll
-            for (int d = CH; d < 64; d *= 2) sums[q] += __shfl_xor(sums[q], d, 64);
-        if (rr == 0 && ncol > 0) {
-            // (rows of whole 8-column blocks: the last one is written past n)
-            float *to = p.colsum + (int64_t)(2 * w.tile + wm) * p.ld_colsum + col;
-            *(f32x4 *)to = f32x4{sums[0], sums[1], sums[2], sums[3]};
-            *(f32x4 *)(to + 4) = f32x4{sums[4], sums[5], sums[6], sums[7]};
+                for (int d = CH; d < 64; d *= 2) s[q] += __shfl_xor(s[q], d, 64);
+            if (rr == 0 && ncol > 0) {
+                // (rows of whole 8-column blocks: the last one is written past n)
+                float *to = p.colsum + half + (int64_t)(2 * w.tile + wm) * p.ld_colsum + col;
+                *(f32x4 *)to = f32x4{s[0], s[1], s[2], s[3]};
+                *(f32x4 *)(to + 4) = f32x4{s[4], s[5], s[6], s[7]};
+            }
+        };
+        join(sums, 0);
+        if constexpr (kPair) join(sums_up, p.stride_colsum);
+    }
+}
+
+// The forward epilogue of a gated product: the wave's columns are WC / 2 of the gate, then the same of
+// the up projection, staged side by side and read back eight of each a lane.
+template <int IN, int FM, int FN, int BM, int BN>
+__device__ __forceinline__ void op_store_gated(const OpParams &p, const OpTile &w, f32x4 (&acc)[FM][FN], lds_char *smem,
+                                               int wave, int lane) {
+    constexpr int WR = BM / 2, WC = BN / 2, HC = WC / 2;   // the wave's sub-tile, its outputs' columns
+    constexpr int kBR = 2;                         // block rows per pass
+    constexpr int RS = WC * 4 + 16;                // bytes of a staged row
+    constexpr int CH = HC / 8;                     // lanes per row
+    constexpr int RI = 64 / CH;                    // rows per step
+    constexpr int kSteps = 16 * kBR / RI;          // steps per pass, whose arithmetic runs together
+    static_assert(4 * 16 * kBR * RS <= tile_lds_bytes<IN, BM, BN>(), "staging fits the stages");
+    static_assert(kSteps >= 1 && FM % kBR == 0, "whole steps and passes");
+    typedef __attribute__((address_space(3))) float lds_float;
+    typedef __attribute__((address_space(3))) f32x4 lds_f32x4;
+
+    const int wm = wave / 2, wn = wave % 2;
+    lds_char *region = smem + wave * (16 * kBR * RS);
+    const int g = lane / 16, u = lane % 16;
+    lds_char *wr = region + (4 * g) * RS + u * 4;
+    const int c = lane % CH, rr = lane / CH;
+    const lds_char *rd = region + rr * RS + c * 32;
+    const int col_t = w.tn * (BN / 2) + wn * HC;   // the wave's first column
+    const int col = col_t + 8 * c, ncol = p.n - col;
+    const int row_t = w.tm * BM + wm * WR;         // the wave's first row of its product
+    const bool full = (w.tm + 1) * BM <= w.m && (w.tn + 1) * (BN / 2) <= p.n;
+    const int64_t row_d = (int64_t)w.row0 + row_t;
+    const GatedOut out = {op_out(p.D, row_d * p.ldd + col_t, p.ldd, p.d_f32 ? 4 : 2),
+                          op_out(p.aux, row_d * p.ld_aux + col_t, p.ld_aux, 2),
+                          op_out(p.aux, p.stride_aux + row_d * p.ld_aux + col_t, p.ld_aux, 2)};
+    float bias[8], bias_up[8];
+    bias_of<IN>(p, p.bias, w.expert, col, bias);
+    bias_of<IN>(p, p.bias_up, w.expert, col, bias_up);
+
+#pragma unroll 1
+    for (int pass = 0; pass < FM / kBR; ++pass) {
+        if (pass > 0) wait_lds<0>();               // the previous pass has been read back
+        static_for<FM / kBR>([&](auto pass_c) {
+            constexpr int at = decltype(pass_c)::value;
+            if (pass == at) {
+                // (a statement of its own in each branch: merged, they would index the accumulators at run time)
+                asm volatile("; pass %0" : : "i"(at));
+                static_for<kBR>([&](auto i_c) {
+                    constexpr int i = decltype(i_c)::value;
+                    static_for<FN>([&](auto j_c) {
+                        constexpr int j = decltype(j_c)::value;
+#pragma unroll
+                        for (int r = 0; r < 4; ++r)
+                            *(lds_float *)(wr + (16 * i + r) * RS + 64 * j) = acc[at * kBR + i][j][r];
+                    });
+                });
+                asm volatile("; staged %0" : : "i"(at));
+            }
+        });
+        float v[kSteps][8], x[kSteps][8];
+#pragma unroll
+        for (int q = 0; q < kSteps; ++q) {
+            const lds_char *at = rd + q * RI * RS;
+            const f32x4 a = *(const lds_f32x4 *)at, b = *(const lds_f32x4 *)(at + 16);
+            const f32x4 d = *(const lds_f32x4 *)(at + 4 * HC), e = *(const lds_f32x4 *)(at + 4 * HC + 16);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                v[q][i] = a[i];
+                v[q][i + 4] = b[i];
+                x[q][i] = d[i];
+                x[q][i + 4] = e[i];
+            }
         }
+        const int row_s = pass * 16 * kBR + rr;
+        gated_finish<IN, kSteps>(
+            p, out, 8 * c, full, full && p.lines, [&](int q) { return row_s + q * RI; },
+            [&](int q) { return full ? 8 : (row_t + row_s + q * RI < w.m ? ncol : 0); }, bias, bias_up, v, x);
     }
 }
 
@@ -264,7 +358,10 @@ void op_kernel(OpParams p) {
     if (!locate<T>(p, blockIdx.x, blockIdx.y, lane, w)) return;
     const Params q = op_operands<TA, TB>(p, w);
     f32x4 acc[FM][FN];
-    tile_product<IN, TA, TB, T, T, 4>(q, w.tm * T, w.tn * T, smem, acc);
+    if constexpr (MODE == OP_GATED)
+        tile_product<IN, TA, TB, T, T, 4, true>(q, w.tm * T, w.tn * (T / 2), smem, acc, (uint32_t)(2 * p.stride_up));
+    else
+        tile_product<IN, TA, TB, T, T, 4>(q, w.tm * T, w.tn * T, smem, acc);
     int lane_e = lane;
     asm volatile("" : "+v"(lane_e));   // the epilogue's addresses are formed after the loop
     if constexpr (MODE == OP_CE_STATS) {
@@ -273,8 +370,11 @@ void op_kernel(OpParams p) {
             op_row_stats<true, FM, FN, T, T>(p, w, acc, scale, wave, lane_e);
         else
             op_row_stats<false, FM, FN, T, T>(p, w, acc, scale, wave, lane_e);
-    } else {
+    } else if constexpr (MODE == OP_GATED) {
         __syncthreads();               // every wave's fragment reads are done: the LDS is free
+        op_store_gated<IN, FM, FN, T, T>(p, w, acc, smem, wave, lane_e);
+    } else {
+        __syncthreads();
         op_store_tile<IN, MODE, FM, FN, T, T>(p, w, acc, smem, wave, lane_e);
     }
 }

@@ -18,6 +18,7 @@ __global__ __launch_bounds__(256) void colsum_kernel(OpParams p, int tile_rows, 
     __shared__ float share[4][kSumCols];
     const int lane = threadIdx.x % 64, part = threadIdx.x / 64;
     const int e = blockIdx.y;
+    const int64_t out = ((int64_t)e * gridDim.z + blockIdx.z) * p.n;
     int64_t first = 0;
     int tiles = p.tiles_m;
     if (p.groups_kind == GROUPS_ROWS) {
@@ -29,13 +30,13 @@ __global__ __launch_bounds__(256) void colsum_kernel(OpParams p, int tile_rows, 
         const int64_t col = c0 + lane;
         float s = 0.0f;
         if (col < p.n) {
-            const float *at = p.colsum + first * rows_per_tile * p.ld_colsum + col;
+            const float *at = p.colsum + blockIdx.z * p.stride_colsum + first * rows_per_tile * p.ld_colsum + col;
             for (int r = part; r < tiles * rows_per_tile; r += 4) s += at[(int64_t)r * p.ld_colsum];
         }
         share[part][lane] = s;
         __syncthreads();
         if (part == 0 && col < p.n)
-            dbias[(int64_t)e * p.n + col] = (share[0][lane] + share[1][lane]) + (share[2][lane] + share[3][lane]);
+            dbias[out + col] = (share[0][lane] + share[1][lane]) + (share[2][lane] + share[3][lane]);
         __syncthreads();   // share is written again
     }
 }
@@ -236,13 +237,13 @@ int launch_1d(const void *kernel, int64_t blocks, unsigned threads, void **args,
 
 }  // namespace
 
-int launch_colsum(const OpParams &p, int tile_rows, int rows_per_tile, float *dbias, void *stream) {
+int launch_colsum(const OpParams &p, int tile_rows, int rows_per_tile, int halves, float *dbias, void *stream) {
     OpParams q = p;
     void *args[] = {&q, &tile_rows, &rows_per_tile, &dbias};
     const int64_t blocks = ((int64_t)p.n + kSumCols - 1) / kSumCols;
     return (int)hipLaunchKernel(reinterpret_cast<const void *>(&colsum_kernel),
                                 dim3((unsigned)(blocks < kMostBlocks ? blocks : kMostBlocks),
-                                     p.groups_kind == GROUPS_ROWS ? (unsigned)p.groups : 1u),
+                                     p.groups_kind == GROUPS_ROWS ? (unsigned)p.groups : 1u, (unsigned)halves),
                                 dim3(256), args, 0, (hipStream_t)stream);
 }
 
