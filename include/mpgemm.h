@@ -423,6 +423,76 @@ uint64_t mpgemm_linear_ce_workspace_size(int64_t m, int64_t n, int64_t k, mpgemm
                                          int train);
 
 /* ---------------------------------------------------------------------------------------
+ * Distillation: the loss of a linear layer's softmax against a teacher's top logits, and its
+ * gradients, without storing the logits.  Types, storage and everything else are as for
+ * mpgemm_run_linear_ce.
+ * --------------------------------------------------------------------------------------- */
+typedef struct {
+    int64_t top;              /* entries of each row, 1 .. 1024 */
+    const int64_t *index;     /* m x top (ld) device integers: the entries' columns; one outside
+                                 0 .. n - 1 (-1, as a rule) does not count */
+    const float *logit;       /* m x top (ld): the teacher's logits there */
+    int64_t ld;               /* >= top; picked's too */
+    float scale;              /* of the teacher's logits: 1 / its temperature */
+    const float *lse;         /* m log-sum-exps of the teacher's scaled logits over all columns; NULL:
+                                 over the entries that count */
+} mpgemm_teacher_t;
+
+/* Queue, with z(i, v) = alpha * X(i, :) . W(v, :) and over the entries j of row i that count,
+ *   q(i, j) = exp(scale * logit(i, j) - teacher's lse(i)),     lse(i) = log(sum over v of exp(z(i, v))),
+ *   loss(i) = sum over j of q(i, j) * (log q(i, j) - z(i, index(i, j)) + lse(i)).
+ * A temperature of the student is part of alpha.  Without the teacher's lse the q of a row sum to 1
+ * and the loss is the divergence of the student from the teacher's top entries; with it, the part of
+ * that divergence that lies in them.  Entries of the same column add up as they stand.  A logit of
+ * -infinity has no mass; a row none of whose entries has any does not count and has loss 0.
+ *   loss, lse: m FP32 values each.  picked: m x top (teacher->ld) FP32 values, z at the entries'
+ *   columns (0 where an entry does not count), which the gradient takes.
+ *   workspace: mpgemm_linear_distill_workspace_size(m, n, k, top, type, 0) bytes. */
+mpgemm_status_t mpgemm_run_linear_distill(mpgemm_handle_t handle, int64_t m, int64_t n, int64_t k,
+                                          const float *alpha, const void *X, mpgemm_dtype_t type,
+                                          int64_t ldx, const void *W, int64_t ldw,
+                                          const mpgemm_teacher_t *teacher, float *loss, float *lse,
+                                          float *picked, void *workspace, uint64_t workspace_bytes,
+                                          void *stream);
+
+/* Queue its gradients: with Q(i) = sum over j of q(i, j) and
+ *   P(i, v) = grad(i) * (Q(i) * exp(z(i, v) - lse(i)) - sum over j with index(i, j) == v of q(i, j)),
+ * 0 in rows that do not count,
+ *   dX = alpha * P W,   dW = alpha * P^T X      (type's; either may be NULL and is then skipped).
+ *   lse, picked: as mpgemm_run_linear_distill wrote them.  grad: m FP32 values.
+ *   What is said of P and of rows that do not count at mpgemm_run_linear_ce_grad holds here.
+ *   workspace: mpgemm_linear_distill_workspace_size(m, n, k, top, type, 1) bytes, which is also
+ *   enough for mpgemm_run_linear_distill. */
+mpgemm_status_t mpgemm_run_linear_distill_grad(mpgemm_handle_t handle, int64_t m, int64_t n, int64_t k,
+                                               const float *alpha, const void *X, mpgemm_dtype_t type,
+                                               int64_t ldx, const void *W, int64_t ldw,
+                                               const mpgemm_teacher_t *teacher, const float *lse,
+                                               const float *picked, const float *grad, void *dX,
+                                               int64_t lddx, void *dW, int64_t lddw, void *workspace,
+                                               uint64_t workspace_bytes, void *stream);
+
+/* Workspace bytes of the two (train != 0: of the gradients too); 0 for sizes or types outside the
+ * contract.  Host-only. */
+uint64_t mpgemm_linear_distill_workspace_size(int64_t m, int64_t n, int64_t k, int64_t top,
+                                              mpgemm_dtype_t type, int train);
+
+/* Host-only argument checks (as mpgemm_check is for mpgemm_run). */
+mpgemm_status_t mpgemm_check_linear_distill(int64_t m, int64_t n, int64_t k, const float *alpha,
+                                            const void *X, mpgemm_dtype_t type, int64_t ldx,
+                                            const void *W, int64_t ldw,
+                                            const mpgemm_teacher_t *teacher, const float *loss,
+                                            const float *lse, const float *picked,
+                                            const void *workspace, uint64_t workspace_bytes);
+mpgemm_status_t mpgemm_check_linear_distill_grad(int64_t m, int64_t n, int64_t k, const float *alpha,
+                                                 const void *X, mpgemm_dtype_t type, int64_t ldx,
+                                                 const void *W, int64_t ldw,
+                                                 const mpgemm_teacher_t *teacher, const float *lse,
+                                                 const float *picked, const float *grad,
+                                                 const void *dX, int64_t lddx, const void *dW,
+                                                 int64_t lddw, const void *workspace,
+                                                 uint64_t workspace_bytes);
+
+/* ---------------------------------------------------------------------------------------
  * Gated products: the first half of a gated feed-forward block, both projections, the activation and
  * the product of the two in one call, and the gradient that comes back to it.  Types, storage and
  * everything else are as above; A is stored m x k.

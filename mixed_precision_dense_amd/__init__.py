@@ -65,6 +65,7 @@ SIGNATURES = {
     "mpgemm_epilogue_grad_workspace_size": (_u64, [_i64, _i64, _i64]),
     "mpgemm_linear_ce_workspace_size": (_u64, [_i64, _i64, _i64, _i32, _i32]),
     "mpgemm_gated_grad_workspace_size": (_u64, [_i64, _i64, _i64]),
+    "mpgemm_linear_distill_workspace_size": (_u64, [_i64, _i64, _i64, _i64, _i32, _i32]),
 }
 # Arguments of the products of language models: the check's, and the run's with the handle before
 # and the stream after them.
@@ -79,6 +80,9 @@ _OPS = {
                      _i32, _vp, _i64, _vp, _i32, _i64, _vp, _vp, _u64],
     "grouped_wgrad": [_i64, _i64, _i64, _i64, _vp, _vp, _i32, _i64, _vp, _i32, _i64, _vp, _vp, _vp,
                       _i32, _i64, _i64],
+    "linear_distill": [_i64, _i64, _i64, _vp, _vp, _i32, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _u64],
+    "linear_distill_grad": [_i64, _i64, _i64, _vp, _vp, _i32, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _i64,
+                            _vp, _i64, _vp, _u64],
     "gated": [_i32, _i64, _i64, _i64, _vp, _vp, _i32, _i64, _vp, _i32, _i64, _i64, _vp, _vp, _i32, _i64],
     "gated_grad": [_i32, _i64, _i64, _i64, _vp, _vp, _i32, _i64, _vp, _i32, _i64, _vp, _vp, _i32, _i64, _i64,
                    _vp, _u64],
@@ -462,6 +466,62 @@ def mpgemm_run_linear_ce_grad(handle, m, n, k, alpha, X, dtype, ldx, W, ldw, tar
 
 def mpgemm_check_linear_ce_grad(*args) -> int:
     return load().mpgemm_check_linear_ce_grad(*_linear_ce_grad_args(*args))
+
+
+class _TeacherStruct(ctypes.Structure):
+    _fields_ = [("top", _i64), ("index", _vp), ("logit", _vp), ("ld", _i64), ("scale", ctypes.c_float), ("lse", _vp)]
+
+
+class Teacher:
+    """mpgemm_teacher_t: a teacher's ``top`` logits of each row (``index`` int64, ``logit`` FP32, rows of
+    ``ld`` elements), their scale and, where they are not all of its mass, its log-sum-exps.  Holds its tensors."""
+
+    __slots__ = ("struct", "held")
+
+    def __init__(self, top, index, logit, ld, scale=1.0, lse=None):
+        self.held = (index, logit, lse)
+        self.struct = _TeacherStruct(top, _ptr(index), _ptr(logit), ld, scale, _ptr(lse))
+
+
+def _linear_distill_args(m, n, k, alpha, X, dtype, ldx, W, ldw, teacher, loss, lse, picked, workspace,
+                         workspace_bytes):
+    return (m, n, k, _f32(alpha), _ptr(X), _dtype(dtype), ldx, _ptr(W), ldw, _epi(teacher), _ptr(loss), _ptr(lse),
+            _ptr(picked), _ptr(workspace), workspace_bytes)
+
+
+def mpgemm_run_linear_distill(handle, m, n, k, alpha, X, dtype, ldx, W, ldw, teacher, loss, lse, picked, workspace,
+                              workspace_bytes, stream=None, check: bool = True) -> int:
+    """Queue each row's loss of the softmax of alpha X W^T against a teacher's top logits."""
+    return _run("mpgemm_run_linear_distill", handle,
+                _linear_distill_args(m, n, k, alpha, X, dtype, ldx, W, ldw, teacher, loss, lse, picked, workspace,
+                                     workspace_bytes), stream, check)
+
+
+def mpgemm_check_linear_distill(*args) -> int:
+    return load().mpgemm_check_linear_distill(*_linear_distill_args(*args))
+
+
+def _linear_distill_grad_args(m, n, k, alpha, X, dtype, ldx, W, ldw, teacher, lse, picked, grad, dX, lddx, dW, lddw,
+                              workspace, workspace_bytes):
+    return (m, n, k, _f32(alpha), _ptr(X), _dtype(dtype), ldx, _ptr(W), ldw, _epi(teacher), _ptr(lse), _ptr(picked),
+            _ptr(grad), _ptr(dX), lddx, _ptr(dW), lddw, _ptr(workspace), workspace_bytes)
+
+
+def mpgemm_run_linear_distill_grad(handle, m, n, k, alpha, X, dtype, ldx, W, ldw, teacher, lse, picked, grad, dX, lddx,
+                                   dW, lddw, workspace, workspace_bytes, stream=None, check: bool = True) -> int:
+    """Queue the gradients dX and dW (either may be None) of the rows' losses weighted by grad."""
+    return _run("mpgemm_run_linear_distill_grad", handle,
+                _linear_distill_grad_args(m, n, k, alpha, X, dtype, ldx, W, ldw, teacher, lse, picked, grad, dX, lddx,
+                                          dW, lddw, workspace, workspace_bytes), stream, check)
+
+
+def mpgemm_check_linear_distill_grad(*args) -> int:
+    return load().mpgemm_check_linear_distill_grad(*_linear_distill_grad_args(*args))
+
+
+def mpgemm_linear_distill_workspace_size(m: int, n: int, k: int, top: int, dtype, train: bool) -> int:
+    """Workspace bytes of mpgemm_run_linear_distill, with train of its gradients too."""
+    return load().mpgemm_linear_distill_workspace_size(m, n, k, top, _dtype(dtype), 1 if train else 0)
 
 
 class _GatedStruct(ctypes.Structure):

@@ -113,8 +113,27 @@ struct CeRows {
     float *scale;          // one factor common to the weights
     int *count;            // number of entries
 };
-int launch_ce_rows(bool bf16, int m, int n, const int64_t *target, const float *lse, const float *grad, const CeRows &rows,
-                   void *stream);
+// mass: nullptr, or what stands in for the targets: rows of mass 0 do not count, the others' exponentials are
+// multiplied by theirs and no column is a target (kNoColumn)
+int launch_ce_rows(bool bf16, int m, int n, const int64_t *target, const float *mass, const float *lse, const float *grad,
+                   const CeRows &rows, void *stream);
+constexpr int64_t kNoColumn = INT64_MAX / 2;
+// A teacher's top logits, as mpgemm_teacher_t gives them.
+struct Teacher {
+    int top;
+    const int64_t *index;
+    const float *logit;
+    int64_t ld;
+    float scale;
+    const float *lse;   // or nullptr
+};
+int launch_picked(bool bf16, const Teacher &t, int m, int n, int k, float alpha, const void *X, int64_t ldx, const void *W,
+                  int64_t ldw, float *picked, void *stream);
+int launch_distill_merge(const Teacher &t, const CeStat *stats, int parts, int m, int n, const float *picked, float *loss, float *lse,
+                         void *stream);
+int launch_mass(const Teacher &t, int m, int n, float *level, float *mass, void *stream);
+int launch_scatter(bool bf16, const Teacher &t, int m, int n, int first, int have, const float *level, const float *mass,
+                   const float *lse, const float *picked, const int *place, const float *weight, void *P, int64_t ldp, void *stream);
 // out row j (16-byte blocks, ld_out) = in row source[j], for count[0] rows of at most m
 int launch_gather_rows(const void *in, int64_t ld_in, const int *source, const int *count, int m, int k, void *out, int64_t ld_out,
                        void *stream);

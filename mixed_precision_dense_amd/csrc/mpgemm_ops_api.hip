@@ -139,13 +139,86 @@ mpgemm_status_t run_gated_grad(bool tb, int64_t groups, int64_t rows, int64_t n,
     return g->dbias ? launch_dbias(plan, p, g->dbias, stream) : MPGEMM_STATUS_SUCCESS;
 }
 
-}  // namespace
-
 #define MPGEMM_TRY(call)                              \
     do {                                              \
         const mpgemm_status_t st_ = (call);           \
         if (st_ != MPGEMM_STATUS_SUCCESS) return st_; \
     } while (0)
+
+// ---------------------------------------------------------------------------- gradients of a head
+// dW of no rows.
+mpgemm_status_t launch_no_rows(bool bf16, int64_t n, int64_t k, void *dW, int64_t lddw, void *stream) {
+    const OpPlan plan = op_plan(n, k, 0, false, 0.0);
+    return launch(plan, bf16, true, false, product(plan, n, k, 0, 0.0f, nullptr, 8, nullptr, 8, dW, false, lddw), stream);
+}
+
+mpg::CeRows head_rows(const CeLayout &L, void *workspace) {
+    char *ws = (char *)workspace;
+    return {(float *)ws, (float *)(ws + L.off_lse), (int64_t *)(ws + L.off_target), (int *)(ws + L.off_place),
+            L.listed ? (int *)(ws + L.off_source) : nullptr, (float *)(ws + L.off_scale), (int *)(ws + L.off_scale) + 1};
+}
+
+// dX and dW of a head from its prepared rows: P of one piece of the vocabulary at a time, which
+// finish(first column, columns, P, its leading dimension) completes, then both products of it.
+template <typename Finish>
+mpgemm_status_t head_grad(const CeLayout &L, const mpg::CeRows &rows, bool bf16, int64_t m, int64_t n, int64_t k, float alpha,
+                          const void *X, int64_t ldx, const void *W, int64_t ldw, void *dX, int64_t lddx, void *dW, int64_t lddw,
+                          void *workspace, void *stream, Finish &&finish) {
+    char *ws = (char *)workspace;
+    float *part = (float *)(ws + L.off_dx);
+    void *probs = ws + L.off_probs;
+    const int64_t ld_part = round8(k);
+    const int *count = L.listed ? rows.count : nullptr;
+    if (L.listed) {   // from here on X is its rows that count
+        MPGEMM_TRY(queued(mpg::launch_gather_rows(X, ldx, rows.source, rows.count, (int)m, (int)k, ws + L.off_x, round8(k), stream)));
+        X = ws + L.off_x;
+        ldx = round8(k);
+    }
+    for (int64_t c = 0; c < L.pieces; ++c) {
+        const int64_t first = c * L.piece, have = n - first < L.piece ? n - first : L.piece;
+        const char *w = (const char *)W + first * ldw * 2;
+        const OpPlan lp = op_plan(m, have, k, true, kProbsWeight);
+        mpg::OpParams p = product(lp, m, have, k, alpha, X, ldx, w, ldw, probs, false, L.piece);
+        p.mode = mpg::OP_CE_PROBS;
+        p.target = rows.target;
+        p.lse = rows.lse;
+        p.weight = rows.weight;
+        p.count = count;
+        p.col0 = (int)first;
+        MPGEMM_TRY(launch(lp, bf16, false, true, p, stream));
+        MPGEMM_TRY(finish((int)first, (int)have, probs, L.piece));
+        if (dW) {
+            const OpPlan plan = op_plan(have, k, m, false, 0.0);
+            mpg::OpParams q = product(plan, have, k, m, alpha, probs, L.piece, X, ldx, (char *)dW + first * lddw * 2, false, lddw);
+            q.scale = rows.scale;
+            q.count = count;
+            q.count_k = 1;
+            q.target = rows.target;
+            MPGEMM_TRY(L.outer ? queued(mpg::launch_outer(bf16, q, stream)) : launch(plan, bf16, true, false, q, stream));
+        }
+        if (dX) {
+            mpg::OpParams q = product(L.dx, m, k, have, 1.0f, probs, L.piece, w, ldw, part, true, ld_part);
+            q.splits = (int)((have + L.k_split - 1) / L.k_split);
+            q.k_split = (int)L.k_split;
+            q.stride_split = m * ld_part;
+            q.count = count;
+            if (c > 0) {   // added to what the pieces before have summed
+                q.beta = 1.0f;
+                q.C = part;
+                q.c_f32 = 1;
+                q.ldc = ld_part;
+            }
+            MPGEMM_TRY(launch(L.dx, bf16, false, false, q, stream));
+        }
+    }
+    if (!dX) return MPGEMM_STATUS_SUCCESS;
+    return queued(mpg::launch_sum_parts(bf16, part, L.splits, m * ld_part, ld_part, rows.place, (int)m, (int)k, alpha, rows.scale, dX,
+                                        lddx, stream));
+}
+
+mpg::Teacher teacher_of(const mpgemm_teacher_t *t) { return {(int)t->top, t->index, t->logit, t->ld, t->scale, t->lse}; }
+
+}  // namespace
 
 extern "C" {
 
@@ -297,65 +370,61 @@ mpgemm_status_t mpgemm_run_linear_ce_grad(mpgemm_handle_t handle, int64_t m, int
     if (k == 0 || (!dX && !dW) || (m == 0 && !dW)) return MPGEMM_STATUS_SUCCESS;
     MPGEMM_TRY(handle_on_device(handle));
     const bool bf16 = type == MPGEMM_R_16BF;
-    if (m == 0) {   // a sum over no rows
-        const OpPlan plan = op_plan(n, k, 0, false, 0.0);
-        return launch(plan, bf16, true, false, product(plan, n, k, 0, 0.0f, nullptr, 8, nullptr, 8, dW, false, lddw), stream);
-    }
+    if (m == 0) return launch_no_rows(bf16, n, k, dW, lddw, stream);
     CeLayout L;
     if (!ce_layout(m, n, k, true, L)) return MPGEMM_STATUS_INTERNAL_ERROR;   // checked above
-    char *ws = (char *)workspace;
-    const mpg::CeRows rows = {(float *)ws, (float *)(ws + L.off_lse), (int64_t *)(ws + L.off_target), (int *)(ws + L.off_place),
-                              L.listed ? (int *)(ws + L.off_source) : nullptr, (float *)(ws + L.off_scale),
-                              (int *)(ws + L.off_scale) + 1};
-    float *part = (float *)(ws + L.off_dx);
-    void *probs = ws + L.off_probs;
-    const int64_t ld_part = round8(k);
-    MPGEMM_TRY(queued(mpg::launch_ce_rows(bf16, (int)m, (int)n, target, lse, grad, rows, stream)));
-    const int *count = L.listed ? rows.count : nullptr;
-    if (L.listed) {   // from here on X is its rows that count
-        MPGEMM_TRY(queued(mpg::launch_gather_rows(X, ldx, rows.source, rows.count, (int)m, (int)k, ws + L.off_x, round8(k), stream)));
-        X = ws + L.off_x;
-        ldx = round8(k);
-    }
-    for (int64_t c = 0; c < L.pieces; ++c) {
-        const int64_t first = c * L.piece, have = n - first < L.piece ? n - first : L.piece;
-        const char *w = (const char *)W + first * ldw * 2;
-        const OpPlan lp = op_plan(m, have, k, true, kProbsWeight);
-        mpg::OpParams p = product(lp, m, have, k, *alpha, X, ldx, w, ldw, probs, false, L.piece);
-        p.mode = mpg::OP_CE_PROBS;
-        p.target = rows.target;
-        p.lse = rows.lse;
-        p.weight = rows.weight;
-        p.count = count;
-        p.col0 = (int)first;
-        MPGEMM_TRY(launch(lp, bf16, false, true, p, stream));
-        if (dW) {
-            const OpPlan plan = op_plan(have, k, m, false, 0.0);
-            mpg::OpParams q = product(plan, have, k, m, *alpha, probs, L.piece, X, ldx, (char *)dW + first * lddw * 2, false, lddw);
-            q.scale = rows.scale;
-            q.count = count;
-            q.count_k = 1;
-            q.target = rows.target;
-            MPGEMM_TRY(L.outer ? queued(mpg::launch_outer(bf16, q, stream)) : launch(plan, bf16, true, false, q, stream));
-        }
-        if (dX) {
-            mpg::OpParams q = product(L.dx, m, k, have, 1.0f, probs, L.piece, w, ldw, part, true, ld_part);
-            q.splits = (int)((have + L.k_split - 1) / L.k_split);
-            q.k_split = (int)L.k_split;
-            q.stride_split = m * ld_part;
-            q.count = count;
-            if (c > 0) {   // added to what the pieces before have summed
-                q.beta = 1.0f;
-                q.C = part;
-                q.c_f32 = 1;
-                q.ldc = ld_part;
-            }
-            MPGEMM_TRY(launch(L.dx, bf16, false, false, q, stream));
-        }
-    }
-    if (!dX) return MPGEMM_STATUS_SUCCESS;
-    return queued(mpg::launch_sum_parts(bf16, part, L.splits, m * ld_part, ld_part, rows.place, (int)m, (int)k, *alpha, rows.scale, dX,
-                                        lddx, stream));
+    const mpg::CeRows rows = head_rows(L, workspace);
+    MPGEMM_TRY(queued(mpg::launch_ce_rows(bf16, (int)m, (int)n, target, nullptr, lse, grad, rows, stream)));
+    return head_grad(L, rows, bf16, m, n, k, *alpha, X, ldx, W, ldw, dX, lddx, dW, lddw, workspace, stream,
+                     [](int, int, void *, int64_t) { return MPGEMM_STATUS_SUCCESS; });
+}
+
+mpgemm_status_t mpgemm_run_linear_distill(mpgemm_handle_t handle, int64_t m, int64_t n, int64_t k, const float *alpha, const void *X,
+                                          mpgemm_dtype_t type, int64_t ldx, const void *W, int64_t ldw,
+                                          const mpgemm_teacher_t *teacher, float *loss, float *lse, float *picked, void *workspace,
+                                          uint64_t workspace_bytes, void *stream) {
+    if (!handle || !handle_live(handle)) return MPGEMM_STATUS_NOT_INITIALIZED;
+    MPGEMM_TRY(mpgemm_check_linear_distill(m, n, k, alpha, X, type, ldx, W, ldw, teacher, loss, lse, picked, workspace,
+                                           workspace_bytes));
+    if (m == 0) return MPGEMM_STATUS_SUCCESS;
+    MPGEMM_TRY(handle_on_device(handle));
+    CeLayout L;
+    if (!ce_layout(m, n, k, false, L)) return MPGEMM_STATUS_INTERNAL_ERROR;   // checked above
+    const bool bf16 = type == MPGEMM_R_16BF;
+    const mpg::Teacher t = teacher_of(teacher);
+    mpg::OpParams p = product(L.logits, m, n, k, *alpha, X, ldx, W, ldw, nullptr, true, 0);
+    p.mode = mpg::OP_CE_STATS;
+    p.stats = (mpg::CeStat *)workspace;
+    p.parts = L.parts;
+    MPGEMM_TRY(launch(L.logits, bf16, false, true, p, stream));
+    MPGEMM_TRY(queued(mpg::launch_picked(bf16, t, (int)m, (int)n, (int)k, *alpha, X, ldx, W, ldw, picked, stream)));
+    return queued(mpg::launch_distill_merge(t, p.stats, L.parts, (int)m, (int)n, picked, loss, lse, stream));
+}
+
+mpgemm_status_t mpgemm_run_linear_distill_grad(mpgemm_handle_t handle, int64_t m, int64_t n, int64_t k, const float *alpha,
+                                               const void *X, mpgemm_dtype_t type, int64_t ldx, const void *W, int64_t ldw,
+                                               const mpgemm_teacher_t *teacher, const float *lse, const float *picked,
+                                               const float *grad, void *dX, int64_t lddx, void *dW, int64_t lddw, void *workspace,
+                                               uint64_t workspace_bytes, void *stream) {
+    if (!handle || !handle_live(handle)) return MPGEMM_STATUS_NOT_INITIALIZED;
+    MPGEMM_TRY(mpgemm_check_linear_distill_grad(m, n, k, alpha, X, type, ldx, W, ldw, teacher, lse, picked, grad, dX, lddx, dW, lddw,
+                                                workspace, workspace_bytes));
+    if (k == 0 || (!dX && !dW) || (m == 0 && !dW)) return MPGEMM_STATUS_SUCCESS;
+    MPGEMM_TRY(handle_on_device(handle));
+    const bool bf16 = type == MPGEMM_R_16BF;
+    if (m == 0) return launch_no_rows(bf16, n, k, dW, lddw, stream);
+    DistillLayout D;
+    if (!distill_layout(m, n, k, true, D)) return MPGEMM_STATUS_INTERNAL_ERROR;   // checked above
+    const mpg::Teacher t = teacher_of(teacher);
+    const mpg::CeRows rows = head_rows(D.ce, workspace);
+    float *level = (float *)((char *)workspace + D.off_level), *mass = (float *)((char *)workspace + D.off_mass);
+    MPGEMM_TRY(queued(mpg::launch_mass(t, (int)m, (int)n, level, mass, stream)));
+    MPGEMM_TRY(queued(mpg::launch_ce_rows(bf16, (int)m, (int)n, nullptr, mass, lse, grad, rows, stream)));
+    return head_grad(D.ce, rows, bf16, m, n, k, *alpha, X, ldx, W, ldw, dX, lddx, dW, lddw, workspace, stream,
+                     [&](int first, int have, void *probs, int64_t ld) {
+                         return queued(mpg::launch_scatter(bf16, t, (int)m, (int)n, first, have, level, mass, lse, picked, rows.place,
+                                                           rows.weight, probs, ld, stream));
+                     });
 }
 
 mpgemm_status_t mpgemm_run_gated(mpgemm_handle_t handle, mpgemm_op_t transb, int64_t m, int64_t n, int64_t k, const float *alpha,

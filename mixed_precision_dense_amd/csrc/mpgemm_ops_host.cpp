@@ -227,6 +227,14 @@ bool ce_layout(int64_t m, int64_t n, int64_t k, bool train, CeLayout &L) {
     return true;
 }
 
+bool distill_layout(int64_t m, int64_t n, int64_t k, bool train, DistillLayout &D) {
+    if (!ce_layout(m, n, k, train, D.ce)) return false;
+    D.off_level = (D.ce.total + 255) / 256 * 256;
+    D.off_mass = D.off_level + ((uint64_t)m * 4 + 255) / 256 * 256;
+    D.total = train && m > 0 ? D.off_mass + (uint64_t)m * 4 : D.ce.total;
+    return true;
+}
+
 }  // namespace mpg_host
 
 using namespace mpg_host;
@@ -561,6 +569,65 @@ mpgemm_status_t mpgemm_check_grouped_gated_grad(mpgemm_op_t transb, int64_t grou
     if (groups < 0) return MPGEMM_STATUS_INVALID_VALUE;
     return check_gated_grad_call({transb, groups, rows, n, k, alpha, A, a_type, lda, offsets, B, b_type, ldb, stride_b, D, d_type, ldd},
                                  grad, stride_d, workspace, workspace_bytes);
+}
+
+namespace {
+
+mpgemm_status_t check_teacher(const mpgemm_teacher_t *t) {
+    if (!t || t->top < 1 || t->ld < t->top) return MPGEMM_STATUS_INVALID_VALUE;
+    return t->top <= kMaxTop && t->ld <= kOpMaxSize ? MPGEMM_STATUS_SUCCESS : MPGEMM_STATUS_NOT_SUPPORTED;
+}
+
+mpgemm_status_t check_teacher_layout(const mpgemm_teacher_t *t) {
+    return aligned(t->index, 8) && aligned(t->logit, 4) && aligned(t->lse, 4) ? MPGEMM_STATUS_SUCCESS : MPGEMM_STATUS_NOT_SUPPORTED;
+}
+
+}  // namespace
+
+uint64_t mpgemm_linear_distill_workspace_size(int64_t m, int64_t n, int64_t k, int64_t top, mpgemm_dtype_t type, int train) {
+    DistillLayout D;
+    if (!half_type(type) || top < 1 || top > kMaxTop || !distill_layout(m, n, k, train != 0, D)) return 0;
+    return m == 0 ? 0 : D.total;
+}
+
+mpgemm_status_t mpgemm_check_linear_distill(int64_t m, int64_t n, int64_t k, const float *alpha, const void *X, mpgemm_dtype_t type,
+                                            int64_t ldx, const void *W, int64_t ldw, const mpgemm_teacher_t *teacher,
+                                            const float *loss, const float *lse, const float *picked, const void *workspace,
+                                            uint64_t workspace_bytes) {
+    if (m < 0 || n < 1 || k < 0 || !alpha) return MPGEMM_STATUS_INVALID_VALUE;
+    if (!half_type(type)) return MPGEMM_STATUS_NOT_SUPPORTED;
+    if (ldx < at_least1(k) || ldw < at_least1(k)) return MPGEMM_STATUS_INVALID_VALUE;
+    MPGEMM_TRY(check_teacher(teacher));
+    if (m == 0) return MPGEMM_STATUS_SUCCESS;
+    if ((k > 0 && (!X || !W)) || !teacher->index || !teacher->logit || !loss || !lse || !picked) return MPGEMM_STATUS_INVALID_VALUE;
+    DistillLayout D;
+    if (!distill_layout(m, n, k, false, D) || !launchable(D.ce.logits, 1)) return MPGEMM_STATUS_NOT_SUPPORTED;
+    if (k > 0 && (!aligned(X, 16) || !aligned(W, 16))) return MPGEMM_STATUS_NOT_SUPPORTED;
+    if (!stride_ok(ldx, 2) || !stride_ok(ldw, 2) || !aligned(loss, 4) || !aligned(lse, 4) || !aligned(picked, 4))
+        return MPGEMM_STATUS_NOT_SUPPORTED;
+    MPGEMM_TRY(check_teacher_layout(teacher));
+    return check_workspace(workspace, workspace_bytes, D.total);
+}
+
+mpgemm_status_t mpgemm_check_linear_distill_grad(int64_t m, int64_t n, int64_t k, const float *alpha, const void *X,
+                                                 mpgemm_dtype_t type, int64_t ldx, const void *W, int64_t ldw,
+                                                 const mpgemm_teacher_t *teacher, const float *lse, const float *picked,
+                                                 const float *grad, const void *dX, int64_t lddx, const void *dW, int64_t lddw,
+                                                 const void *workspace, uint64_t workspace_bytes) {
+    if (m < 0 || n < 1 || k < 0 || !alpha) return MPGEMM_STATUS_INVALID_VALUE;
+    if (!half_type(type)) return MPGEMM_STATUS_NOT_SUPPORTED;
+    MPGEMM_TRY(check_teacher(teacher));
+    const bool rows = m > 0 && k > 0 && (dX || dW);
+    if (rows && (!teacher->index || !teacher->logit || !picked)) return MPGEMM_STATUS_INVALID_VALUE;
+    // everything else is as for the cross entropy (whose targets the teacher's columns stand for)
+    DistillLayout D = {};
+    const bool fits = rows && distill_layout(m, n, k, true, D);
+    MPGEMM_TRY(mpgemm_check_linear_ce_grad(m, n, k, alpha, X, type, ldx, W, ldw, rows ? teacher->index : nullptr, lse, grad, dX, lddx, dW,
+                                           lddw, workspace, workspace_bytes));
+    if (!rows) return MPGEMM_STATUS_SUCCESS;
+    if (!fits || !aligned(picked, 4)) return MPGEMM_STATUS_NOT_SUPPORTED;
+    MPGEMM_TRY(check_teacher_layout(teacher));
+    return check_workspace(workspace, workspace_bytes, D.total);
 }
 
 }  // extern "C"

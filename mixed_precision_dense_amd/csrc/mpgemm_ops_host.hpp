@@ -54,4 +54,12 @@ struct CeLayout {
 };
 bool ce_layout(int64_t m, int64_t n, int64_t k, bool train, CeLayout &L);
 
+// The cross entropy's workspace, and behind it what the distillation's gradient takes from each row's teacher.
+struct DistillLayout {
+    CeLayout ce;
+    uint64_t off_level, off_mass, total;
+};
+bool distill_layout(int64_t m, int64_t n, int64_t k, bool train, DistillLayout &D);
+constexpr int64_t kMaxTop = 1024;   // entries of a teacher's row
+
 }  // namespace mpg_host

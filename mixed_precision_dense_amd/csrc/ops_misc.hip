@@ -120,15 +120,21 @@ __global__ __launch_bounds__(kMergeThreads) void ce_merge_kernel(const CeStat *s
 // after this one take only them; their number stays on the device.  Nothing of a row that does not
 // count may reach the gradients: an X of NaN there (padding) would, as 0 * NaN, through a P of 0.
 constexpr int kRowThreads = 1024;
-__global__ __launch_bounds__(kRowThreads) void ce_rows_kernel(int bf16, int m, int n, const int64_t *target, const float *lse,
-                                                              const float *grad, CeRows rows) {
+__global__ __launch_bounds__(kRowThreads) void ce_rows_kernel(int bf16, int m, int n, const int64_t *target, const float *mass,
+                                                              const float *lse, const float *grad, CeRows rows) {
     __shared__ float most[kRowThreads / 64];
     __shared__ int found[kRowThreads / 64];
     const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
+    // the column that a row's target takes, or -1: the row does not count
+    auto target_of = [&](int64_t r) -> int64_t {
+        if (mass != nullptr) return mass[r] == 0.0f ? -1 : kNoColumn;
+        const int64_t t = target[r];
+        return t >= 0 && t < n ? t : -1;
+    };
     float a = 0.0f;
     for (int64_t r = threadIdx.x; r < m; r += kRowThreads) {   // (m + kRowThreads may pass 31 bits)
-        const int64_t t = target[r];
-        if (t >= 0 && t < n) a = fmaxf(a, __builtin_fabsf(grad[r]));
+        // (entries of P are at most the weight, or the mass times it)
+        if (target_of(r) >= 0) a = fmaxf(a, __builtin_fabsf(grad[r]) * (mass != nullptr ? fmaxf(mass[r], 1.0f) : 1.0f));
     }
 #pragma unroll
     for (int d = 1; d < 64; d *= 2) a = fmaxf(a, __shfl_xor(a, d, 64));
@@ -141,8 +147,8 @@ __global__ __launch_bounds__(kRowThreads) void ce_rows_kernel(int bf16, int m, i
     int before = 0;                                         // entries of the rows before this turn's
     for (int64_t base = 0; base < m; base += kRowThreads) { // (the same number of turns for every wave)
         const int64_t r = base + threadIdx.x;
-        const int64_t t = r < m ? target[r] : -1;
-        const bool counts = t >= 0 && t < n;
+        const int64_t t = r < m ? target_of(r) : -1;
+        const bool counts = t >= 0;
         const float g = counts ? grad[r] : 0.0f;
         const float weight = usable ? g / a * top : g;
         int64_t at = r;
@@ -163,7 +169,7 @@ __global__ __launch_bounds__(kRowThreads) void ce_rows_kernel(int bf16, int m, i
         if (r < m) rows.place[r] = counts ? (int)at : -1;
         if (r < m && (counts || rows.source == nullptr)) {
             rows.weight[at] = weight;
-            rows.lse[at] = lse[r];
+            rows.lse[at] = counts && mass != nullptr ? lse[r] - __logf(mass[r]) : lse[r];
             rows.target[at] = counts ? t : -1;
         }
     }
@@ -256,11 +262,11 @@ int launch_ce_merge(bool bf16, const CeStat *stats, int parts, int m, int n, int
                      m, kMergeThreads, args, stream);
 }
 
-int launch_ce_rows(bool bf16, int m, int n, const int64_t *target, const float *lse, const float *grad, const CeRows &rows,
-                   void *stream) {
+int launch_ce_rows(bool bf16, int m, int n, const int64_t *target, const float *mass, const float *lse, const float *grad,
+                   const CeRows &rows, void *stream) {
     int b = bf16 ? 1 : 0;
     CeRows r = rows;
-    void *args[] = {&b, &m, &n, &target, &lse, &grad, &r};
+    void *args[] = {&b, &m, &n, &target, &mass, &lse, &grad, &r};
     return launch_1d(reinterpret_cast<const void *>(&ce_rows_kernel), 1, kRowThreads, args, stream);
 }
 
