@@ -493,6 +493,39 @@ mpgemm_status_t mpgemm_check_linear_distill_grad(int64_t m, int64_t n, int64_t k
                                                  uint64_t workspace_bytes);
 
 /* ---------------------------------------------------------------------------------------
+ * Log probabilities of stored logits (as a product has left them), in one pass over them.
+ * --------------------------------------------------------------------------------------- */
+
+/* Queue, for each row i of z = alpha * Z (m x n, n >= 1, type MPGEMM_R_16F, MPGEMM_R_16BF or MPGEMM_R_32F,
+ * read in whole aligned 16-byte blocks, 0 < alpha <= 1e30: 1 / a temperature):
+ *   lse(i) = log(sum over v of exp(z(i, v))),
+ *   logprob(i) = z(i, target(i)) - lse(i), 0 where the target is outside 0 .. n - 1,
+ *   entropy(i) = - sum over v of p log p with p = exp(z(i, v) - lse(i)),
+ *   top_index(i, j), top_logprob(i, j), j < top (0 .. 64): the columns of the row's largest logits and their
+ *     log probabilities, falling, equal logits by the lower column first; past n columns -1 and -infinity.
+ *   logprob (with target), lse, entropy: m FP32 values each, any NULL: not computed.  top_index: int64,
+ *   top_logprob: FP32, both with rows of ld_top >= top elements; not touched for top == 0.
+ *   A logit of -infinity has probability 0.  A row of nothing else has no distribution: lse, logprob and
+ *   top_logprob are -infinity, the entropy 0.  A NaN or +infinity makes the row's numbers NaN (its
+ *   top_index are columns in no particular order).
+ *   ldz goes up to 2^31.  workspace: mpgemm_logprobs_workspace_size(m, n, z_type, top) bytes. */
+mpgemm_status_t mpgemm_run_logprobs(mpgemm_handle_t handle, int64_t m, int64_t n, const float *alpha,
+                                    const void *Z, mpgemm_dtype_t z_type, int64_t ldz,
+                                    const int64_t *target, float *logprob, float *lse, float *entropy,
+                                    int64_t top, int64_t *top_index, float *top_logprob,
+                                    int64_t ld_top, void *workspace, uint64_t workspace_bytes,
+                                    void *stream);
+
+/* Workspace bytes (0 where none is needed, and for sizes or types outside the contract), and the
+ * argument check.  Host-only. */
+uint64_t mpgemm_logprobs_workspace_size(int64_t m, int64_t n, mpgemm_dtype_t z_type, int64_t top);
+mpgemm_status_t mpgemm_check_logprobs(int64_t m, int64_t n, const float *alpha, const void *Z,
+                                      mpgemm_dtype_t z_type, int64_t ldz, const int64_t *target,
+                                      const float *logprob, const float *lse, const float *entropy,
+                                      int64_t top, const int64_t *top_index, const float *top_logprob,
+                                      int64_t ld_top, const void *workspace, uint64_t workspace_bytes);
+
+/* ---------------------------------------------------------------------------------------
  * Gated products: the first half of a gated feed-forward block, both projections, the activation and
  * the product of the two in one call, and the gradient that comes back to it.  Types, storage and
  * everything else are as above; A is stored m x k.

@@ -65,6 +65,7 @@ SIGNATURES = {
     "mpgemm_epilogue_grad_workspace_size": (_u64, [_i64, _i64, _i64]),
     "mpgemm_linear_ce_workspace_size": (_u64, [_i64, _i64, _i64, _i32, _i32]),
     "mpgemm_gated_grad_workspace_size": (_u64, [_i64, _i64, _i64]),
+    "mpgemm_logprobs_workspace_size": (_u64, [_i64, _i64, _i32, _i64]),
     "mpgemm_linear_distill_workspace_size": (_u64, [_i64, _i64, _i64, _i64, _i32, _i32]),
 }
 # Arguments of the products of language models: the check's, and the run's with the handle before
@@ -83,6 +84,7 @@ _OPS = {
     "linear_distill": [_i64, _i64, _i64, _vp, _vp, _i32, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _u64],
     "linear_distill_grad": [_i64, _i64, _i64, _vp, _vp, _i32, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _i64,
                             _vp, _i64, _vp, _u64],
+    "logprobs": [_i64, _i64, _vp, _vp, _i32, _i64, _vp, _vp, _vp, _vp, _i64, _vp, _vp, _i64, _vp, _u64],
     "gated": [_i32, _i64, _i64, _i64, _vp, _vp, _i32, _i64, _vp, _i32, _i64, _i64, _vp, _vp, _i32, _i64],
     "gated_grad": [_i32, _i64, _i64, _i64, _vp, _vp, _i32, _i64, _vp, _i32, _i64, _vp, _vp, _i32, _i64, _i64,
                    _vp, _u64],
@@ -522,6 +524,30 @@ def mpgemm_check_linear_distill_grad(*args) -> int:
 def mpgemm_linear_distill_workspace_size(m: int, n: int, k: int, top: int, dtype, train: bool) -> int:
     """Workspace bytes of mpgemm_run_linear_distill, with train of its gradients too."""
     return load().mpgemm_linear_distill_workspace_size(m, n, k, top, _dtype(dtype), 1 if train else 0)
+
+
+def _logprobs_args(m, n, alpha, Z, z_type, ldz, target, logprob, lse, entropy, top, top_index, top_logprob, ld_top,
+                   workspace, workspace_bytes):
+    return (m, n, _f32(alpha), _ptr(Z), _dtype(z_type), ldz, _ptr(target), _ptr(logprob), _ptr(lse), _ptr(entropy), top,
+            _ptr(top_index), _ptr(top_logprob), ld_top, _ptr(workspace), workspace_bytes)
+
+
+def mpgemm_run_logprobs(handle, m, n, alpha, Z, z_type, ldz, target, logprob, lse, entropy, top, top_index, top_logprob,
+                        ld_top, workspace, workspace_bytes, stream=None, check: bool = True) -> int:
+    """Queue each row's log probability of its target, log-sum-exp, entropy and ``top`` largest
+    alternatives of the logits alpha Z; outputs that are None are not computed."""
+    return _run("mpgemm_run_logprobs", handle,
+                _logprobs_args(m, n, alpha, Z, z_type, ldz, target, logprob, lse, entropy, top, top_index, top_logprob,
+                               ld_top, workspace, workspace_bytes), stream, check)
+
+
+def mpgemm_check_logprobs(*args) -> int:
+    return load().mpgemm_check_logprobs(*_logprobs_args(*args))
+
+
+def mpgemm_logprobs_workspace_size(m: int, n: int, z_type, top: int) -> int:
+    """Workspace bytes of mpgemm_run_logprobs."""
+    return load().mpgemm_logprobs_workspace_size(m, n, _dtype(z_type), top)
 
 
 class _GatedStruct(ctypes.Structure):

@@ -23,7 +23,7 @@ SOURCES = ["mpgemm_host.cpp", "mpgemm_api.hip", "kern_f16.hip", "kern_bf16.hip",
            "mpgemm_ops_api.hip", "ops_forward_f16.hip", "ops_forward_bf16.hip", "ops_slope_f16.hip",
            "ops_slope_bf16.hip", "ops_ce.hip", "skinny_f16.hip", "skinny_bf16.hip", "ops_misc.hip", "ops_outer.hip",
            "ops_gated_f16.hip", "ops_gated_bf16.hip", "ops_gated_grad_f16.hip", "ops_gated_grad_bf16.hip",
-           "skinny_gated.hip", "ops_distill.hip"]
+           "skinny_gated.hip", "ops_distill.hip", "ops_logprobs.hip"]
 ARCH = "gfx950"
 
 # Packed FP32 instructions are kept out of all generated code.

@@ -142,4 +142,24 @@ int launch_gather_rows(const void *in, int64_t ld_in, const int *source, const i
 int launch_sum_parts(bool bf16, const float *parts, int splits, int64_t stride, int64_t ld_part, const int *place, int rows,
                      int cols, float alpha, const float *scale, void *out, int64_t ld_out, void *stream);
 
+// Log probabilities of m rows of n stored logits (ldz elements apart), each in `parts` of part_vectors
+// 16-byte vectors.
+enum LogitsType { LOGITS_F16 = 0, LOGITS_BF16 = 1, LOGITS_F32 = 2 };
+struct LogprobParams {
+    const void *Z;
+    int64_t ldz;
+    int m, n;
+    float alpha;
+    const int64_t *target;
+    float *logprob, *lse, *entropy;   // each nullptr: not asked for
+    int top;                          // 0: no alternatives
+    int64_t *top_index;
+    float *top_logprob;
+    int64_t ld_top;
+    int parts, part_vectors;
+    float *stats;                     // parts > 1: four values a part
+    uint64_t *keys;                   // and `top` keys a part
+};
+int launch_logprobs(int type, const LogprobParams &p, void *stream);
+
 }  // namespace mpg

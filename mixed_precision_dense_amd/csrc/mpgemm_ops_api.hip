@@ -482,4 +482,36 @@ mpgemm_status_t mpgemm_run_grouped_gated_grad(mpgemm_handle_t handle, mpgemm_op_
                           ldd, stride_d, workspace, stream);
 }
 
+mpgemm_status_t mpgemm_run_logprobs(mpgemm_handle_t handle, int64_t m, int64_t n, const float *alpha, const void *Z,
+                                    mpgemm_dtype_t z_type, int64_t ldz, const int64_t *target, float *logprob, float *lse,
+                                    float *entropy, int64_t top, int64_t *top_index, float *top_logprob, int64_t ld_top,
+                                    void *workspace, uint64_t workspace_bytes, void *stream) {
+    if (!handle || !handle_live(handle)) return MPGEMM_STATUS_NOT_INITIALIZED;
+    MPGEMM_TRY(mpgemm_check_logprobs(m, n, alpha, Z, z_type, ldz, target, logprob, lse, entropy, top, top_index, top_logprob, ld_top,
+                                     workspace, workspace_bytes));
+    if (m == 0 || (!logprob && !lse && !entropy && top == 0)) return MPGEMM_STATUS_SUCCESS;
+    MPGEMM_TRY(handle_on_device(handle));
+    const LogprobLayout L = logprob_layout(m, n, elem_bytes(z_type), top);
+    mpg::LogprobParams p = {};
+    p.Z = Z;
+    p.ldz = ldz;
+    p.m = (int)m;
+    p.n = (int)n;
+    p.alpha = *alpha;
+    p.target = target;
+    p.logprob = logprob;
+    p.lse = lse;
+    p.entropy = entropy;
+    p.top = (int)top;
+    p.top_index = top_index;
+    p.top_logprob = top_logprob;
+    p.ld_top = ld_top;
+    p.parts = L.parts;
+    p.part_vectors = L.part_vectors;
+    p.stats = (float *)workspace;
+    p.keys = (uint64_t *)((char *)workspace + L.off_keys);
+    const int type = z_type == MPGEMM_R_32F ? mpg::LOGITS_F32 : (z_type == MPGEMM_R_16BF ? mpg::LOGITS_BF16 : mpg::LOGITS_F16);
+    return queued(mpg::launch_logprobs(type, p, stream));
+}
+
 }  // extern "C"

@@ -227,6 +227,23 @@ bool ce_layout(int64_t m, int64_t n, int64_t k, bool train, CeLayout &L) {
     return true;
 }
 
+LogprobLayout logprob_layout(int64_t m, int64_t n, int bytes, int64_t top) {
+    const int64_t vectors = ceil_div(n, 16 / bytes);
+    // about 8192 parts in all, none below 1024 vectors (a turn of a workgroup's four waves)
+    int64_t parts = m > 0 ? ceil_div(8192, m) : 1;
+    if (parts > ceil_div(vectors, 1024)) parts = ceil_div(vectors, 1024);
+    if (parts < 1) parts = 1;
+    LogprobLayout L;
+    L.part_vectors = (int)(ceil_div(ceil_div(vectors, parts), 64) * 64);
+    L.parts = (int)(vectors > 0 ? ceil_div(vectors, L.part_vectors) : 1);
+    L.off_keys = L.total = 0;
+    if (L.parts > 1) {
+        L.off_keys = ((uint64_t)m * (uint64_t)L.parts * 16 + 255) / 256 * 256;
+        L.total = L.off_keys + (uint64_t)m * (uint64_t)L.parts * (uint64_t)top * 8;
+    }
+    return L;
+}
+
 bool distill_layout(int64_t m, int64_t n, int64_t k, bool train, DistillLayout &D) {
     if (!ce_layout(m, n, k, train, D.ce)) return false;
     D.off_level = (D.ce.total + 255) / 256 * 256;
@@ -628,6 +645,30 @@ mpgemm_status_t mpgemm_check_linear_distill_grad(int64_t m, int64_t n, int64_t k
     if (!fits || !aligned(picked, 4)) return MPGEMM_STATUS_NOT_SUPPORTED;
     MPGEMM_TRY(check_teacher_layout(teacher));
     return check_workspace(workspace, workspace_bytes, D.total);
+}
+
+uint64_t mpgemm_logprobs_workspace_size(int64_t m, int64_t n, mpgemm_dtype_t z_type, int64_t top) {
+    if (m < 1 || n < 1 || m > kOpMaxSize || n > kOpMaxSize || top < 0 || top > kMaxAlternatives) return 0;
+    if (!half_type(z_type) && z_type != MPGEMM_R_32F) return 0;
+    return logprob_layout(m, n, elem_bytes(z_type), top).total;
+}
+
+mpgemm_status_t mpgemm_check_logprobs(int64_t m, int64_t n, const float *alpha, const void *Z, mpgemm_dtype_t z_type, int64_t ldz,
+                                      const int64_t *target, const float *logprob, const float *lse, const float *entropy,
+                                      int64_t top, const int64_t *top_index, const float *top_logprob, int64_t ld_top,
+                                      const void *workspace, uint64_t workspace_bytes) {
+    if (m < 0 || n < 1 || !alpha || top < 0) return MPGEMM_STATUS_INVALID_VALUE;
+    if (!half_type(z_type) && z_type != MPGEMM_R_32F) return MPGEMM_STATUS_NOT_SUPPORTED;
+    if (!(*alpha > 0.0f) || *alpha > 1.0e30f || ldz < n || (top > 0 && ld_top < top)) return MPGEMM_STATUS_INVALID_VALUE;
+    if (m == 0) return MPGEMM_STATUS_SUCCESS;
+    if (!Z || (logprob && !target) || (top > 0 && (!top_index || !top_logprob))) return MPGEMM_STATUS_INVALID_VALUE;
+    const int64_t most = INT64_MAX / ((int64_t)1 << 36);   // (rows times a leading dimension stay 64-bit byte offsets)
+    if (m > kOpMaxSize || n > kOpMaxSize || ldz > ((int64_t)1 << 31) || top > kMaxAlternatives || (top > 0 && ld_top > most))
+        return MPGEMM_STATUS_NOT_SUPPORTED;
+    if (!aligned(Z, 16) || (ldz * elem_bytes(z_type)) % 16 || (logprob && !aligned(target, 8)) || !aligned(logprob, 4) ||
+        !aligned(lse, 4) || !aligned(entropy, 4) || (top > 0 && (!aligned(top_index, 8) || !aligned(top_logprob, 4))))
+        return MPGEMM_STATUS_NOT_SUPPORTED;
+    return check_workspace(workspace, workspace_bytes, mpgemm_logprobs_workspace_size(m, n, z_type, top));
 }
 
 }  // extern "C"

@@ -62,4 +62,12 @@ struct DistillLayout {
 bool distill_layout(int64_t m, int64_t n, int64_t k, bool train, DistillLayout &D);
 constexpr int64_t kMaxTop = 1024;   // entries of a teacher's row
 
+// Log probabilities: the parts of a row (a workgroup each) and where they are kept.
+struct LogprobLayout {
+    int parts, part_vectors;
+    uint64_t off_keys, total;
+};
+LogprobLayout logprob_layout(int64_t m, int64_t n, int bytes, int64_t top);
+constexpr int64_t kMaxAlternatives = 64;
+
 }  // namespace mpg_host
