@@ -144,6 +144,7 @@ int launch_sum_parts(bool bf16, const float *parts, int splits, int64_t stride, 
 
 // Log probabilities of m rows of n stored logits (ldz elements apart), each in `parts` of part_vectors
 // 16-byte vectors.
+constexpr int kLogprobPart = 131072;   // most elements of a part
 enum LogitsType { LOGITS_F16 = 0, LOGITS_BF16 = 1, LOGITS_F32 = 2 };
 struct LogprobParams {
     const void *Z;

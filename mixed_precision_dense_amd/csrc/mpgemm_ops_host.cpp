@@ -5,6 +5,7 @@
 
 #include "mpgemm_host.hpp"
 #include "mpgemm_kinds.hpp"
+#include "mpgemm_ops.hpp"
 
 namespace mpg_host {
 namespace {
@@ -229,10 +230,10 @@ bool ce_layout(int64_t m, int64_t n, int64_t k, bool train, CeLayout &L) {
 
 LogprobLayout logprob_layout(int64_t m, int64_t n, int bytes, int64_t top) {
     const int64_t vectors = ceil_div(n, 16 / bytes);
-    // about 8192 parts in all, none below 1024 vectors (a turn of a workgroup's four waves)
-    int64_t parts = m > 0 ? ceil_div(8192, m) : 1;
-    if (parts > ceil_div(vectors, 1024)) parts = ceil_div(vectors, 1024);
-    if (parts < 1) parts = 1;
+    // about 4096 parts in all, of 4096 to kLogprobPart elements
+    int64_t parts = m > 0 ? ceil_div(4096, m) : 1;
+    if (parts > ceil_div(n, 4096)) parts = ceil_div(n, 4096);
+    if (parts < ceil_div(n, mpg::kLogprobPart)) parts = ceil_div(n, mpg::kLogprobPart);
     LogprobLayout L;
     L.part_vectors = (int)(ceil_div(ceil_div(vectors, parts), 64) * 64);
     L.parts = (int)(vectors > 0 ? ceil_div(vectors, L.part_vectors) : 1);

@@ -8,19 +8,25 @@
 // taken before the scaling, so that rows of a type's lowest value alone (a mask that leaves nothing) come out
 // as the equal values that they are.
 //
-// The largest: a wave holds a sorted list of 64, one a lane, of keys that order values first and lower
-// indexes second (no two are alike, so that the result does not depend on the order of reading), and lets
-// in only what is above the list's last needed one.  Of a random row of n that is about top (1 + log(n /
-// 512)) elements a wave; a vector without any costs a comparison.  A few are inserted one by one; more than
-// kFew are sorted across the lanes and merged, so that rows in rising order stay within a constant
-// factor too.
+// The largest.  Keys order values first and lower indexes second, so that no two are alike and the result
+// does not depend on the order of reading.  While the logits stream by, only the maximum of every 32 elements
+// of a lane is kept (in the LDS).  The top-th largest of the 256 lanes' maxima is then a bound T that
+// at least `top` elements reach; few of the kept maxima do, and only their elements are read once more
+// (4095 x 128000 BF16 with 8: about 9 of 4096 maxima a row).  What reaches T is sorted across the lanes of
+// one wave.  Where too many do (rows of equal values) or a NaN hides the maxima, the workgroup goes
+// through its part again with lists that let in what is above their last place.  (With such lists alone,
+// kept while streaming, 4095 x 128000 BF16 took 340 us with 8 alternatives and 640 with 64, against 193
+// without any.)
 #include "mpgemm_ops_epilogue.hpp"
 
 namespace mpg {
 namespace {
 
 constexpr int kWaves = 4;
-constexpr int kFew = 6;
+constexpr int kGroup = 32;                          // elements of a lane whose maximum is kept
+constexpr int kGroups = kLogprobPart / (kGroup * 64 * kWaves);   // of a lane, in a part
+constexpr int kFound = 128;                         // elements of a wave that reach T, kept in the LDS
+constexpr int kFew = 10;                            // inserted one by one; more are sorted (28 steps)
 constexpr int64_t kMostBlocks = 65536;
 constexpr float kLn2 = 0.69314718055994531f;
 
@@ -42,12 +48,34 @@ __device__ __forceinline__ uint64_t xor_lane(uint64_t v, int d) {
     const uint32_t lo = (uint32_t)__shfl_xor((int)(uint32_t)v, d, 64), hi = (uint32_t)__shfl_xor((int)(uint32_t)(v >> 32), d, 64);
     return (uint64_t)hi << 32 | lo;
 }
+__device__ __forceinline__ uint32_t xor_lane(uint32_t v, int d) { return (uint32_t)__shfl_xor((int)v, d, 64); }
 // One step of a bitonic network: the pair (lane, lane ^ d) keeps its larger key in the lower lane, or in the
 // upper one where `up`.
-__device__ __forceinline__ uint64_t exchange(uint64_t v, int d, bool up, int lane) {
-    const uint64_t o = xor_lane(v, d);
+template <typename K>
+__device__ __forceinline__ K exchange(K v, int d, bool up, int lane) {
+    const K o = xor_lane(v, d);
     const bool larger = ((lane & d) == 0) != up;
     return (v > o) == larger ? v : o;
+}
+
+// The keys of the lanes, falling from lane 0.
+template <typename K>
+__device__ __forceinline__ K sort_lanes(K v, int lane) {
+#pragma unroll
+    for (int size = 2; size <= 64; size *= 2)
+#pragma unroll
+        for (int d = size / 2; d > 0; d /= 2) v = exchange(v, d, (lane & size) != 0 && size < 64, lane);
+    return v;
+}
+// The 64 largest of two falling sequences, falling: the larger of the one and the other reversed is
+// bitonic and holds them.
+template <typename K>
+__device__ __forceinline__ K merge_lanes(K v, K other, int lane) {
+    const K o = xor_lane(other, 63);
+    v = v > o ? v : o;
+#pragma unroll
+    for (int d = 32; d > 0; d /= 2) v = exchange(v, d, false, lane);
+    return v;
 }
 
 struct TopList {
@@ -61,22 +89,14 @@ struct TopList {
     }
     // A sorted list of another wave or part (64 keys, falling).
     __device__ __forceinline__ void merge(uint64_t other, int lane) {
-        const uint64_t o = xor_lane(other, 63);        // the larger of the list and the other one reversed
-        key = key > o ? key : o;                       // is bitonic and holds the 64 largest
-#pragma unroll
-        for (int d = 32; d > 0; d /= 2) key = exchange(key, d, false, lane);
+        key = merge_lanes(key, other, lane);
         last = lane_value(key, top - 1);
     }
     // One candidate a lane (0: none); all lanes call it.
     __device__ __forceinline__ void offer(uint64_t cand, int lane) {
         uint64_t in = __ballot(cand > last);
         if (__popcll(in) > kFew) {
-            uint64_t v = cand > last ? cand : 0;
-#pragma unroll
-            for (int size = 2; size <= 64; size *= 2)
-#pragma unroll
-                for (int d = size / 2; d > 0; d /= 2) v = exchange(v, d, (lane & size) != 0 && size < 64, lane);
-            merge(v, lane);
+            merge(sort_lanes(cand > last ? cand : 0, lane), lane);
             return;
         }
         while (in != 0) {
@@ -166,66 +186,113 @@ __device__ __forceinline__ void finish_row(const LogprobParams &p, int64_t row, 
     }
 }
 
-// The waves' statistics and lists to wave 0's, through the LDS.
+// What the waves of a workgroup share.
 struct Share {
     Stat stat[kWaves];
-    uint64_t key[kWaves][64];
+    int count[kWaves];
+    uint32_t sorted[kWaves][64];
+    uint16_t ids[kWaves][64];
+    uint64_t found[kWaves][kFound];   // (or a list of 64)
 };
-template <bool TOP>
-__device__ __forceinline__ void join_waves(Share &share, Stat &st, TopList &list, float c, int wave, int lane) {
+__device__ __forceinline__ void join_stats(Share &share, Stat &st, float c, int wave, int lane) {
     st.join_wave(c);
     if (lane == 0) share.stat[wave] = st;
-    if (TOP) share.key[wave][lane] = list.key;
     __syncthreads();
-    if (wave == 0) {
-        for (int i = 1; i < kWaves; ++i) {
-            st.join(share.stat[i], c);
-            if (TOP) list.merge(share.key[i][lane], lane);
-        }
-    }
+    if (wave == 0)
+        for (int i = 1; i < kWaves; ++i) st.join(share.stat[i], c);
+}
+__device__ __forceinline__ void join_lists(Share &share, TopList &list, int wave, int lane) {
+    __syncthreads();
+    share.found[wave][lane] = list.key;
+    __syncthreads();
+    if (wave == 0)
+        for (int i = 1; i < kWaves; ++i) list.merge(share.found[i][lane], lane);
 }
 
-// A workgroup takes a part of a row: its waves take 64 vectors of 16 bytes in turn, UN at a time.
+// A part of a row: vectors first .. end - 1, of which a wave takes 64 UN in turn.
+template <int T>
+struct Part {
+    static constexpr int E = Logits<T>::E, UN = kGroup / E;
+    const char *z;
+    int first, end, n, lane;
+
+    // Vector i of the lane's in a turn that starts at `base`, and its elements; what is not there is -inf.
+    __device__ __forceinline__ int vector(int base, int i) const { return base + 64 * i + lane; }
+    __device__ __forceinline__ u32x4 load(int v) const { return *(const u32x4 *)(z + 16 * (int64_t)min(v, end - 1)); }
+    __device__ __forceinline__ void widen(u32x4 raw, int v, bool whole, float (&x)[E]) const {
+        Logits<T>::widen(raw, x);
+        if (!whole) {
+            const int left = v < end ? n - v * E : 0;
+#pragma unroll
+            for (int e = 0; e < E; ++e) x[e] = e < left ? x[e] : -__builtin_inff();
+        }
+    }
+    // (the last vector of a row may be part-filled)
+    __device__ __forceinline__ bool whole(int base, int i) const { return base + 64 * (i + 1) < end; }
+    __device__ __forceinline__ uint64_t key(float x, int v, int e) const {
+        return v < end && v * E + e < n ? (uint64_t)order_of(x) << 32 | (0xFFFFFFFFu - (uint32_t)(v * E + e)) : 0;
+    }
+
+    // The wave's largest by its list alone, whatever the part holds.
+    __device__ __forceinline__ void list_all(TopList &list, int wave) const {
+        for (int base = first + 64 * UN * wave; base < end; base += 64 * UN * kWaves)
+#pragma unroll 1
+            for (int i = 0; i < UN && base + 64 * i < end; ++i) {
+                const int v = vector(base, i);
+                float x[E];
+                widen(load(v), v, whole(base, i), x);
+                // (bit e of `left`: element e has not been offered)
+                uint32_t left = (1u << E) - 1;
+                while (true) {
+                    uint64_t best = 0;
+                    int at = 0;
+#pragma unroll
+                    for (int e = 0; e < E; ++e) {
+                        const uint64_t k = left >> e & 1 ? key(x[e], v, e) : 0;
+                        if (k > best) {
+                            best = k;
+                            at = e;
+                        }
+                    }
+                    const bool in = best > list.last;
+                    if (!__any(in)) break;
+                    list.offer(best, lane);
+                    if (in) left &= ~(1u << at);
+                }
+            }
+    }
+};
+
+// A workgroup takes a part of a row.
 template <int T, bool ENT, bool TOP>
 __global__ __launch_bounds__(64 * kWaves) void logprobs_kernel(LogprobParams p) {
-    constexpr int E = Logits<T>::E, UN = 4;
+    constexpr int E = Part<T>::E, UN = Part<T>::UN;
     __shared__ Share share;
+    __shared__ float group_max[TOP ? kWaves : 1][TOP ? kGroups : 1][64];
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), lane = threadIdx.x % 64;
     const float c = p.alpha * kLog2e;
     const int vectors = (p.n + E - 1) / E;
     const int64_t items = (int64_t)p.m * p.parts;
     for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
         const int64_t row = item / p.parts;
-        const int part = (int)(item - row * p.parts);
-        const char *z = (const char *)p.Z + row * p.ldz * (16 / E);
-        const int first = part * p.part_vectors, end = min(vectors, first + p.part_vectors);
+        const int first = (int)(item - row * p.parts) * p.part_vectors;
+        const Part<T> part = {(const char *)p.Z + row * p.ldz * (16 / E), first, min(vectors, first + p.part_vectors), p.n, lane};
         Stat st;
         st.init();
-        TopList list;
-        list.init(TOP ? p.top : 1);
-        for (int base = first + 64 * UN * wave; base < end; base += 64 * UN * kWaves) {
+        int turns = 0;
+        for (int base = first + 64 * UN * wave; base < part.end; base += 64 * UN * kWaves, ++turns) {
             u32x4 raw[UN];
 #pragma unroll
-            for (int i = 0; i < UN; ++i) {
-                const int v = base + 64 * i + lane;
-                raw[i] = *(const u32x4 *)(z + 16 * (int64_t)min(v, end - 1));
-            }
-            float x[UN][E], most[UN], up = st.m;
+            for (int i = 0; i < UN; ++i) raw[i] = part.load(part.vector(base, i));
+            float x[UN][E], most = -__builtin_inff();
 #pragma unroll
             for (int i = 0; i < UN; ++i) {
-                const int v = base + 64 * i + lane;
-                Logits<T>::widen(raw[i], x[i]);
-                if (base + 64 * (i + 1) >= end || base + 64 * (i + 1) >= vectors) {   // (uniform) what is not there
-                    const int left = v < end ? p.n - v * E : 0;
+                part.widen(raw[i], part.vector(base, i), part.whole(base, i), x[i]);
 #pragma unroll
-                    for (int e = 0; e < E; ++e) x[i][e] = e < left ? x[i][e] : -__builtin_inff();
-                }
-                most[i] = x[i][0];
-#pragma unroll
-                for (int e = 1; e < E; ++e) most[i] = fmaxf(most[i], x[i][e]);
-                up = fmaxf(up, most[i]);
+                for (int e = 0; e < E; ++e) most = fmaxf(most, x[i][e]);
             }
-            if (__any(up > st.m)) st.rescale(up, c);
+            if (TOP) group_max[wave][turns][lane] = most;
+            if (__any(most > st.m)) st.rescale(fmaxf(st.m, most), c);
             const float m = stat_base(st.m);
 #pragma unroll
             for (int i = 0; i < UN; ++i)
@@ -235,36 +302,66 @@ __global__ __launch_bounds__(64 * kWaves) void logprobs_kernel(LogprobParams p) 
                     st.s += w;
                     if (ENT) st.t = __builtin_fmaf(fmaxf(u, -1.0e4f), w, st.t);
                 }
-            if (TOP) {
+        }
+        TopList list;
+        list.init(TOP ? p.top : 1);
+        if (TOP) {
+            // T: the top-th of all lanes' maxima (0: fewer lanes have elements)
+            const uint32_t own = part.vector(first + 64 * UN * wave, 0) < part.end ? order_of(st.m) : 0u;
+            share.sorted[wave][lane] = sort_lanes(own, lane);
+            const bool nan = __any(st.s != st.s);
+            __syncthreads();
+            uint32_t best = share.sorted[0][lane];
 #pragma unroll
-                for (int i = 0; i < UN; ++i) {
-                    const int v = base + 64 * i + lane;
-                    // (equal to the last one at a higher index is not above it)
-                    if (base + 64 * i >= end || !__any(order_of(most[i]) > (uint32_t)(list.last >> 32))) continue;
-                    uint32_t key[E];
+            for (int i = 1; i < kWaves; ++i) best = merge_lanes(best, share.sorted[i][lane], lane);
+            const uint32_t bound = (uint32_t)__builtin_amdgcn_readlane((int)best, p.top - 1);
+            // the lanes' turns that reach it, packed
+            int groups = 0;
+            for (int g = 0; g < turns; ++g) {
+                const bool in = order_of(group_max[wave][g][lane]) >= bound;
+                const uint64_t mask = __ballot(in);
+                const int at = groups + __builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0u));
+                if (in && at < 64) share.ids[wave][at] = (uint16_t)(g * 64 + lane);
+                groups += __popcll(mask);
+            }
+            int found = groups > 64 || nan ? kFound + 1 : 0;
+            // their elements that reach it
+            for (int i = lane; i - lane < groups * UN && found <= kFound; i += 64) {
+                uint64_t key[E];
 #pragma unroll
-                    for (int e = 0; e < E; ++e) key[e] = v < end && v * E + e < p.n ? order_of(x[i][e]) : 0u;
-                    while (true) {
-                        uint32_t best = 0;
-                        int at = 0;
+                for (int e = 0; e < E; ++e) key[e] = 0;
+                if (i < groups * UN) {
+                    const int id = share.ids[wave][i / UN];
+                    const int v = first + 64 * UN * (wave + kWaves * (id / 64)) + 64 * (i % UN) + id % 64;
+                    float x[E];
+                    Logits<T>::widen(part.load(v), x);
 #pragma unroll
-                        for (int e = 0; e < E; ++e)
-                            if (key[e] > best) {
-                                best = key[e];
-                                at = e;
-                            }
-                        const uint64_t cand = best == 0 ? 0 : (uint64_t)best << 32 | (0xFFFFFFFFu - (uint32_t)(v * E + at));
-                        const bool in = cand > list.last;
-                        if (!__any(in)) break;
-                        list.offer(cand, lane);
+                    for (int e = 0; e < E; ++e) key[e] = part.key(x[e], v, e);
+                }
 #pragma unroll
-                        for (int e = 0; e < E; ++e)
-                            if (in && e == at) key[e] = 0;
-                    }
+                for (int e = 0; e < E; ++e) {
+                    const bool in = key[e] != 0 && (uint32_t)(key[e] >> 32) >= bound;
+                    const uint64_t mask = __ballot(in);
+                    if (mask == 0) continue;
+                    const int at = found + __builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0u));
+                    if (in && at < kFound) share.found[wave][at] = key[e];
+                    found += __popcll(mask);
                 }
             }
+            if (lane == 0) share.count[wave] = found;
+            __syncthreads();
+            bool listed = true;
+            for (int i = 0; i < kWaves; ++i) listed &= share.count[i] <= kFound;
+            if (!listed) {
+                part.list_all(list, wave);
+                join_lists(share, list, wave, lane);
+            } else if (wave == 0) {
+                for (int i = 0; i < kWaves; ++i)
+                    for (int b = 0; b < share.count[i]; b += 64)
+                        list.offer(b + lane < share.count[i] ? share.found[i][b + lane] : 0, lane);
+            }
         }
-        join_waves<TOP>(share, st, list, c, wave, lane);
+        join_stats(share, st, c, wave, lane);
         if (wave == 0) {
             if (p.parts == 1) {
                 finish_row<T>(p, row, st, list, lane);
@@ -282,7 +379,8 @@ __global__ __launch_bounds__(64 * kWaves) void logprobs_kernel(LogprobParams p) 
     }
 }
 
-// A workgroup joins the parts of a row.
+// A workgroup joins the parts of a row.  A wave takes 64 parts at a time and their lists rank by rank: once
+// no part's key of a rank enters, none of a later one does.
 template <int T>
 __global__ __launch_bounds__(64 * kWaves) void logprobs_join_kernel(LogprobParams p) {
     __shared__ Share share;
@@ -297,10 +395,19 @@ __global__ __launch_bounds__(64 * kWaves) void logprobs_join_kernel(LogprobParam
         }
         TopList list;
         list.init(p.top > 0 ? p.top : 1);
-        const int keys = p.parts * p.top;
-        for (int i = 64 * wave; i < keys; i += 64 * kWaves)
-            list.offer(i + lane < keys ? p.keys[row * keys + i + lane] : 0, lane);
-        join_waves<true>(share, st, list, c, wave, lane);
+        for (int i = 64 * wave; p.top > 0 && i < p.parts; i += 64 * kWaves) {
+            const bool in = i + lane < p.parts;
+            const uint64_t *keys = p.keys + (row * p.parts + min(i + lane, p.parts - 1)) * p.top;
+            uint64_t next = keys[0];
+            for (int j = 0; j < p.top; ++j) {
+                const uint64_t k = in ? next : 0;
+                next = keys[min(j + 1, p.top - 1)];
+                if (!__any(k > list.last)) break;
+                list.offer(k, lane);
+            }
+        }
+        if (p.parts > 64) join_lists(share, list, wave, lane);   // (else the first wave has them all)
+        join_stats(share, st, c, wave, lane);
         if (wave == 0) finish_row<T>(p, row, st, list, lane);
         __syncthreads();   // share is written again
     }
