@@ -161,6 +161,6 @@ struct LogprobParams {
     float *stats;                     // parts > 1: four values a part
     uint64_t *keys;                   // and `top` keys a part
 };
-int launch_logprobs(int type, const LogprobParams &p, void *stream);
+int launch_logprobs(int type, int waves, const LogprobParams &p, void *stream);
 
 }  // namespace mpg

@@ -511,7 +511,7 @@ mpgemm_status_t mpgemm_run_logprobs(mpgemm_handle_t handle, int64_t m, int64_t n
     p.stats = (float *)workspace;
     p.keys = (uint64_t *)((char *)workspace + L.off_keys);
     const int type = z_type == MPGEMM_R_32F ? mpg::LOGITS_F32 : (z_type == MPGEMM_R_16BF ? mpg::LOGITS_BF16 : mpg::LOGITS_F16);
-    return queued(mpg::launch_logprobs(type, p, stream));
+    return queued(mpg::launch_logprobs(type, L.waves, p, stream));
 }
 
 }  // extern "C"

@@ -230,11 +230,24 @@ bool ce_layout(int64_t m, int64_t n, int64_t k, bool train, CeLayout &L) {
 
 LogprobLayout logprob_layout(int64_t m, int64_t n, int bytes, int64_t top) {
     const int64_t vectors = ceil_div(n, 16 / bytes);
-    // about 4096 parts in all, of 4096 to kLogprobPart elements
-    int64_t parts = m > 0 ? ceil_div(4096, m) : 1;
-    if (parts > ceil_div(n, 4096)) parts = ceil_div(n, 4096);
+    // A row in parts costs a second launch and a search in every part, so that rows are cut only where they
+    // leave CUs idle, into two workgroups a CU (us with 20 alternatives, whole / 512 / 4096 parts in all):
+    //   16 x 32000 FP32 12.8 / 17.1 / 17.9;  300 x 32000 16.6 / 24.7 / 30.9;  256 x 128000 30.3 / 37.8 / 45.3
+    //   (BF16 27.3 / 30.2 / 46.4);  64 x 128000 - / 22.1 / 28.7;  16 x 128000 - / 18.7 / 18.2
+    int64_t parts = 1;
+    if (m > 0 && m < kCus && n > 32768) {
+        parts = ceil_div(2 * kCus, m);
+        if (parts > ceil_div(n, 4096)) parts = ceil_div(n, 4096);
+    }
     if (parts < ceil_div(n, mpg::kLogprobPart)) parts = ceil_div(n, mpg::kLogprobPart);
     LogprobLayout L;
+    // A wave a row where rows are short (four would have little each and meet twice) or many (us with 20
+    // alternatives, one wave / four):
+    //   16 x 4096 FP32 8.3 / 9.1;  128 x 8192 10.2 / 9.6;  1024 x 8192 13.9 / 15.5;  1024 x 16384 BF16 17.0 / 17.5;
+    //   1024 x 32000 25.5 / 22.8;  4096 x 1000 14.0 / 34.3;  4096 x 32000 59.9 / 77.4 (FP32 107 / 103)
+    int64_t one = 8 * m < (bytes == 2 ? 32768 : 16384) ? 8 * m : (bytes == 2 ? 32768 : 16384);
+    if (one < 4096) one = 4096;
+    L.waves = n <= one ? 1 : 4;
     L.part_vectors = (int)(ceil_div(ceil_div(vectors, parts), 64) * 64);
     L.parts = (int)(vectors > 0 ? ceil_div(vectors, L.part_vectors) : 1);
     L.off_keys = L.total = 0;

@@ -65,6 +65,7 @@ constexpr int64_t kMaxTop = 1024;   // entries of a teacher's row
 // Log probabilities: the parts of a row (a workgroup each) and where they are kept.
 struct LogprobLayout {
     int parts, part_vectors;
+    int waves;   // of a workgroup
     uint64_t off_keys, total;
 };
 LogprobLayout logprob_layout(int64_t m, int64_t n, int bytes, int64_t top);

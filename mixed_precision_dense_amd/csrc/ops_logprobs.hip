@@ -14,17 +14,17 @@
 // at least `top` elements reach; few of the kept maxima do, and only their elements are read once more
 // (4095 x 128000 BF16 with 8: about 9 of 4096 maxima a row).  What reaches T is sorted across the lanes of
 // one wave.  Where too many do (rows of equal values) or a NaN hides the maxima, the workgroup goes
-// through its part again with lists that let in what is above their last place.  (With such lists alone,
-// kept while streaming, 4095 x 128000 BF16 took 340 us with 8 alternatives and 640 with 64, against 193
-// without any.)
+// through its part again with lists that let in what is above their last place.  With such lists alone,
+// kept while streaming, 4095 x 128000 BF16 took 340 us with 8 alternatives and 640 with 64; so 198 and 211
+// (5.3 and 5.0 TB/s), against 188 without any: the row's bytes bound it.  Of a short row most of the time
+// is the chain of dependent lane exchanges (16 x 4096: 8.3 us, an empty launch 4).
 #include "mpgemm_ops_epilogue.hpp"
 
 namespace mpg {
 namespace {
 
-constexpr int kWaves = 4;
 constexpr int kGroup = 32;                          // elements of a lane whose maximum is kept
-constexpr int kGroups = kLogprobPart / (kGroup * 64 * kWaves);   // of a lane, in a part
+constexpr int kGroups = kLogprobPart / (kGroup * 64 * 4);   // of a lane, in a part (a part of one wave has a fourth)
 constexpr int kFound = 128;                         // elements of a wave that reach T, kept in the LDS
 constexpr int kFew = 10;                            // inserted one by one; more are sorted (28 steps)
 constexpr int64_t kMostBlocks = 65536;
@@ -44,38 +44,63 @@ __device__ __forceinline__ uint64_t lane_value(uint64_t v, int lane) {
     const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(v >> 32), lane);
     return (uint64_t)hi << 32 | lo;
 }
-__device__ __forceinline__ uint64_t xor_lane(uint64_t v, int d) {
-    const uint32_t lo = (uint32_t)__shfl_xor((int)(uint32_t)v, d, 64), hi = (uint32_t)__shfl_xor((int)(uint32_t)(v >> 32), d, 64);
-    return (uint64_t)hi << 32 | lo;
+// The value of lane ^ D, by moves within rows of 16 lanes and swaps between them (the LDS's permutation, ten
+// times as long, would be most of the time that a short row takes).
+template <int CTRL>
+__device__ __forceinline__ uint32_t row_move(uint32_t v) {
+    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, false);
 }
-__device__ __forceinline__ uint32_t xor_lane(uint32_t v, int d) { return (uint32_t)__shfl_xor((int)v, d, 64); }
-// One step of a bitonic network: the pair (lane, lane ^ d) keeps its larger key in the lower lane, or in the
+template <int D>
+__device__ __forceinline__ uint32_t xor_lane(uint32_t v, int lane) {
+    if constexpr (D == 1) return row_move<0xB1>(v);                      // within quads: 1 0 3 2
+    if constexpr (D == 2) return row_move<0x4E>(v);                      // 2 3 0 1
+    if constexpr (D == 4) return row_move<0x1B>(row_move<0x141>(v));     // half rows reversed (^ 7), quads reversed (^ 3)
+    if constexpr (D == 8) return row_move<0x128>(v);                     // rows rotated by 8
+    if constexpr (D == 16) {   // both results hold rows 0, 0, 2, 2 and 1, 1, 3, 3
+        const auto r = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+        return lane & 16 ? r[0] : r[1];
+    }
+    if constexpr (D == 32) {
+        const auto r = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+        return lane & 32 ? r[0] : r[1];
+    }
+    if constexpr (D == 63) return xor_lane<32>(xor_lane<16>(row_move<0x140>(v), lane), lane);   // rows reversed (^ 15)
+}
+template <int D>
+__device__ __forceinline__ uint64_t xor_lane(uint64_t v, int lane) {
+    return (uint64_t)xor_lane<D>((uint32_t)(v >> 32), lane) << 32 | xor_lane<D>((uint32_t)v, lane);
+}
+// One step of a bitonic network: the pair (lane, lane ^ D) keeps its larger key in the lower lane, or in the
 // upper one where `up`.
-template <typename K>
-__device__ __forceinline__ K exchange(K v, int d, bool up, int lane) {
-    const K o = xor_lane(v, d);
-    const bool larger = ((lane & d) == 0) != up;
+template <int D, typename K>
+__device__ __forceinline__ K exchange(K v, bool up, int lane) {
+    const K o = xor_lane<D>(v, lane);
+    const bool larger = ((lane & D) == 0) != up;
     return (v > o) == larger ? v : o;
+}
+template <int D, typename K>
+__device__ __forceinline__ K exchange_down(K v, bool up, int lane) {
+    v = exchange<D>(v, up, lane);
+    if constexpr (D > 1) v = exchange_down<D / 2>(v, up, lane);
+    return v;
 }
 
 // The keys of the lanes, falling from lane 0.
 template <typename K>
 __device__ __forceinline__ K sort_lanes(K v, int lane) {
-#pragma unroll
-    for (int size = 2; size <= 64; size *= 2)
-#pragma unroll
-        for (int d = size / 2; d > 0; d /= 2) v = exchange(v, d, (lane & size) != 0 && size < 64, lane);
-    return v;
+    v = exchange_down<1>(v, (lane & 2) != 0, lane);
+    v = exchange_down<2>(v, (lane & 4) != 0, lane);
+    v = exchange_down<4>(v, (lane & 8) != 0, lane);
+    v = exchange_down<8>(v, (lane & 16) != 0, lane);
+    v = exchange_down<16>(v, (lane & 32) != 0, lane);
+    return exchange_down<32>(v, false, lane);
 }
 // The 64 largest of two falling sequences, falling: the larger of the one and the other reversed is
 // bitonic and holds them.
 template <typename K>
 __device__ __forceinline__ K merge_lanes(K v, K other, int lane) {
-    const K o = xor_lane(other, 63);
-    v = v > o ? v : o;
-#pragma unroll
-    for (int d = 32; d > 0; d /= 2) v = exchange(v, d, false, lane);
-    return v;
+    const K o = xor_lane<63>(other, lane);
+    return exchange_down<32>(v > o ? v : o, false, lane);
 }
 
 struct TopList {
@@ -186,31 +211,33 @@ __device__ __forceinline__ void finish_row(const LogprobParams &p, int64_t row, 
     }
 }
 
-// What the waves of a workgroup share.
+// What the NW waves of a workgroup share.
+template <int NW>
 struct Share {
-    Stat stat[kWaves];
-    int count[kWaves];
-    uint32_t sorted[kWaves][64];
-    uint16_t ids[kWaves][64];
-    uint64_t found[kWaves][kFound];   // (or a list of 64)
-};
-__device__ __forceinline__ void join_stats(Share &share, Stat &st, float c, int wave, int lane) {
-    st.join_wave(c);
-    if (lane == 0) share.stat[wave] = st;
-    __syncthreads();
-    if (wave == 0)
-        for (int i = 1; i < kWaves; ++i) st.join(share.stat[i], c);
-}
-__device__ __forceinline__ void join_lists(Share &share, TopList &list, int wave, int lane) {
-    __syncthreads();
-    share.found[wave][lane] = list.key;
-    __syncthreads();
-    if (wave == 0)
-        for (int i = 1; i < kWaves; ++i) list.merge(share.found[i][lane], lane);
-}
+    Stat stat[NW];
+    int count[NW];
+    uint32_t sorted[NW][64];
+    uint16_t ids[NW][64];
+    uint64_t found[NW][kFound];   // (or a list of 64)
 
-// A part of a row: vectors first .. end - 1, of which a wave takes 64 UN in turn.
-template <int T>
+    __device__ __forceinline__ void join_stats(Stat &st, float c, int wave, int lane) {
+        st.join_wave(c);
+        if (lane == 0) stat[wave] = st;
+        __syncthreads();
+        if (wave == 0)
+            for (int i = 1; i < NW; ++i) st.join(stat[i], c);
+    }
+    __device__ __forceinline__ void join_lists(TopList &list, int wave, int lane) {
+        __syncthreads();
+        found[wave][lane] = list.key;
+        __syncthreads();
+        if (wave == 0)
+            for (int i = 1; i < NW; ++i) list.merge(found[i][lane], lane);
+    }
+};
+
+// A part of a row: vectors first .. end - 1, of which each of NW waves takes 64 UN in turn.
+template <int T, int NW>
 struct Part {
     static constexpr int E = Logits<T>::E, UN = kGroup / E;
     const char *z;
@@ -235,7 +262,7 @@ struct Part {
 
     // The wave's largest by its list alone, whatever the part holds.
     __device__ __forceinline__ void list_all(TopList &list, int wave) const {
-        for (int base = first + 64 * UN * wave; base < end; base += 64 * UN * kWaves)
+        for (int base = first + 64 * UN * wave; base < end; base += 64 * UN * NW)
 #pragma unroll 1
             for (int i = 0; i < UN && base + 64 * i < end; ++i) {
                 const int v = vector(base, i);
@@ -263,12 +290,12 @@ struct Part {
     }
 };
 
-// A workgroup takes a part of a row.
-template <int T, bool ENT, bool TOP>
-__global__ __launch_bounds__(64 * kWaves) void logprobs_kernel(LogprobParams p) {
-    constexpr int E = Part<T>::E, UN = Part<T>::UN;
-    __shared__ Share share;
-    __shared__ float group_max[TOP ? kWaves : 1][TOP ? kGroups : 1][64];
+// A workgroup of NW waves takes a part of a row.
+template <int T, int NW, bool ENT, bool TOP>
+__global__ __launch_bounds__(64 * NW) void logprobs_kernel(LogprobParams p) {
+    constexpr int E = Part<T, NW>::E, UN = Part<T, NW>::UN;
+    __shared__ Share<NW> share;
+    __shared__ float group_max[TOP ? NW : 1][TOP ? kGroups : 1][64];
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), lane = threadIdx.x % 64;
     const float c = p.alpha * kLog2e;
     const int vectors = (p.n + E - 1) / E;
@@ -276,11 +303,11 @@ __global__ __launch_bounds__(64 * kWaves) void logprobs_kernel(LogprobParams p) 
     for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
         const int64_t row = item / p.parts;
         const int first = (int)(item - row * p.parts) * p.part_vectors;
-        const Part<T> part = {(const char *)p.Z + row * p.ldz * (16 / E), first, min(vectors, first + p.part_vectors), p.n, lane};
+        const Part<T, NW> part = {(const char *)p.Z + row * p.ldz * (16 / E), first, min(vectors, first + p.part_vectors), p.n, lane};
         Stat st;
         st.init();
         int turns = 0;
-        for (int base = first + 64 * UN * wave; base < part.end; base += 64 * UN * kWaves, ++turns) {
+        for (int base = first + 64 * UN * wave; base < part.end; base += 64 * UN * NW, ++turns) {
             u32x4 raw[UN];
 #pragma unroll
             for (int i = 0; i < UN; ++i) raw[i] = part.load(part.vector(base, i));
@@ -313,7 +340,7 @@ __global__ __launch_bounds__(64 * kWaves) void logprobs_kernel(LogprobParams p) 
             __syncthreads();
             uint32_t best = share.sorted[0][lane];
 #pragma unroll
-            for (int i = 1; i < kWaves; ++i) best = merge_lanes(best, share.sorted[i][lane], lane);
+            for (int i = 1; i < NW; ++i) best = merge_lanes(best, share.sorted[i][lane], lane);
             const uint32_t bound = (uint32_t)__builtin_amdgcn_readlane((int)best, p.top - 1);
             // the lanes' turns that reach it, packed
             int groups = 0;
@@ -332,7 +359,7 @@ __global__ __launch_bounds__(64 * kWaves) void logprobs_kernel(LogprobParams p) 
                 for (int e = 0; e < E; ++e) key[e] = 0;
                 if (i < groups * UN) {
                     const int id = share.ids[wave][i / UN];
-                    const int v = first + 64 * UN * (wave + kWaves * (id / 64)) + 64 * (i % UN) + id % 64;
+                    const int v = first + 64 * UN * (wave + NW * (id / 64)) + 64 * (i % UN) + id % 64;
                     float x[E];
                     Logits<T>::widen(part.load(v), x);
 #pragma unroll
@@ -351,17 +378,17 @@ __global__ __launch_bounds__(64 * kWaves) void logprobs_kernel(LogprobParams p) 
             if (lane == 0) share.count[wave] = found;
             __syncthreads();
             bool listed = true;
-            for (int i = 0; i < kWaves; ++i) listed &= share.count[i] <= kFound;
+            for (int i = 0; i < NW; ++i) listed &= share.count[i] <= kFound;
             if (!listed) {
                 part.list_all(list, wave);
-                join_lists(share, list, wave, lane);
+                share.join_lists(list, wave, lane);
             } else if (wave == 0) {
-                for (int i = 0; i < kWaves; ++i)
+                for (int i = 0; i < NW; ++i)
                     for (int b = 0; b < share.count[i]; b += 64)
                         list.offer(b + lane < share.count[i] ? share.found[i][b + lane] : 0, lane);
             }
         }
-        join_stats(share, st, c, wave, lane);
+        share.join_stats(st, c, wave, lane);
         if (wave == 0) {
             if (p.parts == 1) {
                 finish_row<T>(p, row, st, list, lane);
@@ -381,9 +408,10 @@ __global__ __launch_bounds__(64 * kWaves) void logprobs_kernel(LogprobParams p) 
 
 // A workgroup joins the parts of a row.  A wave takes 64 parts at a time and their lists rank by rank: once
 // no part's key of a rank enters, none of a later one does.
+constexpr int kWaves = 4;
 template <int T>
 __global__ __launch_bounds__(64 * kWaves) void logprobs_join_kernel(LogprobParams p) {
-    __shared__ Share share;
+    __shared__ Share<kWaves> share;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), lane = threadIdx.x % 64;
     const float c = p.alpha * kLog2e;
     for (int64_t row = blockIdx.x; row < p.m; row += gridDim.x) {
@@ -406,8 +434,8 @@ __global__ __launch_bounds__(64 * kWaves) void logprobs_join_kernel(LogprobParam
                 list.offer(k, lane);
             }
         }
-        if (p.parts > 64) join_lists(share, list, wave, lane);   // (else the first wave has them all)
-        join_stats(share, st, c, wave, lane);
+        if (p.parts > 64) share.join_lists(list, wave, lane);   // (else the first wave has them all)
+        share.join_stats(st, c, wave, lane);
         if (wave == 0) finish_row<T>(p, row, st, list, lane);
         __syncthreads();   // share is written again
     }
@@ -415,45 +443,62 @@ __global__ __launch_bounds__(64 * kWaves) void logprobs_join_kernel(LogprobParam
 
 // (instantiated explicitly: host code that only reaches a kernel through an inlined launcher does not
 // reliably emit its launch stub)
-template __global__ void logprobs_kernel<LOGITS_F16, false, false>(LogprobParams);
-template __global__ void logprobs_kernel<LOGITS_F16, false, true>(LogprobParams);
-template __global__ void logprobs_kernel<LOGITS_F16, true, false>(LogprobParams);
-template __global__ void logprobs_kernel<LOGITS_F16, true, true>(LogprobParams);
-template __global__ void logprobs_kernel<LOGITS_BF16, false, false>(LogprobParams);
-template __global__ void logprobs_kernel<LOGITS_BF16, false, true>(LogprobParams);
-template __global__ void logprobs_kernel<LOGITS_BF16, true, false>(LogprobParams);
-template __global__ void logprobs_kernel<LOGITS_BF16, true, true>(LogprobParams);
-template __global__ void logprobs_kernel<LOGITS_F32, false, false>(LogprobParams);
-template __global__ void logprobs_kernel<LOGITS_F32, false, true>(LogprobParams);
-template __global__ void logprobs_kernel<LOGITS_F32, true, false>(LogprobParams);
-template __global__ void logprobs_kernel<LOGITS_F32, true, true>(LogprobParams);
+template __global__ void logprobs_kernel<LOGITS_F16, 1, false, false>(LogprobParams);
+template __global__ void logprobs_kernel<LOGITS_F16, 1, false, true>(LogprobParams);
+template __global__ void logprobs_kernel<LOGITS_F16, 1, true, false>(LogprobParams);
+template __global__ void logprobs_kernel<LOGITS_F16, 1, true, true>(LogprobParams);
+template __global__ void logprobs_kernel<LOGITS_F16, 4, false, false>(LogprobParams);
+template __global__ void logprobs_kernel<LOGITS_F16, 4, false, true>(LogprobParams);
+template __global__ void logprobs_kernel<LOGITS_F16, 4, true, false>(LogprobParams);
+template __global__ void logprobs_kernel<LOGITS_F16, 4, true, true>(LogprobParams);
+template __global__ void logprobs_kernel<LOGITS_BF16, 1, false, false>(LogprobParams);
+template __global__ void logprobs_kernel<LOGITS_BF16, 1, false, true>(LogprobParams);
+template __global__ void logprobs_kernel<LOGITS_BF16, 1, true, false>(LogprobParams);
+template __global__ void logprobs_kernel<LOGITS_BF16, 1, true, true>(LogprobParams);
+template __global__ void logprobs_kernel<LOGITS_BF16, 4, false, false>(LogprobParams);
+template __global__ void logprobs_kernel<LOGITS_BF16, 4, false, true>(LogprobParams);
+template __global__ void logprobs_kernel<LOGITS_BF16, 4, true, false>(LogprobParams);
+template __global__ void logprobs_kernel<LOGITS_BF16, 4, true, true>(LogprobParams);
+template __global__ void logprobs_kernel<LOGITS_F32, 1, false, false>(LogprobParams);
+template __global__ void logprobs_kernel<LOGITS_F32, 1, false, true>(LogprobParams);
+template __global__ void logprobs_kernel<LOGITS_F32, 1, true, false>(LogprobParams);
+template __global__ void logprobs_kernel<LOGITS_F32, 1, true, true>(LogprobParams);
+template __global__ void logprobs_kernel<LOGITS_F32, 4, false, false>(LogprobParams);
+template __global__ void logprobs_kernel<LOGITS_F32, 4, false, true>(LogprobParams);
+template __global__ void logprobs_kernel<LOGITS_F32, 4, true, false>(LogprobParams);
+template __global__ void logprobs_kernel<LOGITS_F32, 4, true, true>(LogprobParams);
 template __global__ void logprobs_join_kernel<LOGITS_F16>(LogprobParams);
 template __global__ void logprobs_join_kernel<LOGITS_BF16>(LogprobParams);
 template __global__ void logprobs_join_kernel<LOGITS_F32>(LogprobParams);
 
-int launch(const void *kernel, int64_t blocks, const LogprobParams &p, hipStream_t stream) {
+int launch(const void *kernel, int64_t blocks, int waves, const LogprobParams &p, hipStream_t stream) {
     void *args[] = {const_cast<LogprobParams *>(&p)};
-    return (int)hipLaunchKernel(kernel, dim3((unsigned)(blocks < kMostBlocks ? blocks : kMostBlocks)), dim3(64 * kWaves), args, 0, stream);
+    return (int)hipLaunchKernel(kernel, dim3((unsigned)(blocks < kMostBlocks ? blocks : kMostBlocks)), dim3((unsigned)(64 * waves)), args, 0,
+                                stream);
+}
+
+template <int T, int NW>
+const void *kernel_of(const LogprobParams &p) {
+    if (p.entropy != nullptr)
+        return p.top > 0 ? reinterpret_cast<const void *>(&logprobs_kernel<T, NW, true, true>)
+                         : reinterpret_cast<const void *>(&logprobs_kernel<T, NW, true, false>);
+    return p.top > 0 ? reinterpret_cast<const void *>(&logprobs_kernel<T, NW, false, true>)
+                     : reinterpret_cast<const void *>(&logprobs_kernel<T, NW, false, false>);
 }
 
 template <int T>
-int launch_type(const LogprobParams &p, hipStream_t stream) {
-    const bool ent = p.entropy != nullptr, top = p.top > 0;
-    const void *first = ent ? (top ? reinterpret_cast<const void *>(&logprobs_kernel<T, true, true>)
-                                   : reinterpret_cast<const void *>(&logprobs_kernel<T, true, false>))
-                            : (top ? reinterpret_cast<const void *>(&logprobs_kernel<T, false, true>)
-                                   : reinterpret_cast<const void *>(&logprobs_kernel<T, false, false>));
-    const int e = launch(first, (int64_t)p.m * p.parts, p, stream);
+int launch_type(int waves, const LogprobParams &p, hipStream_t stream) {
+    const int e = launch(waves == 1 ? kernel_of<T, 1>(p) : kernel_of<T, 4>(p), (int64_t)p.m * p.parts, waves, p, stream);
     if (e != 0 || p.parts == 1) return e;
-    return launch(reinterpret_cast<const void *>(&logprobs_join_kernel<T>), p.m, p, stream);
+    return launch(reinterpret_cast<const void *>(&logprobs_join_kernel<T>), p.m, kWaves, p, stream);
 }
 
 }  // namespace
 
-int launch_logprobs(int type, const LogprobParams &p, void *stream) {
+int launch_logprobs(int type, int waves, const LogprobParams &p, void *stream) {
     hipStream_t s = (hipStream_t)stream;
-    if (type == LOGITS_F16) return launch_type<LOGITS_F16>(p, s);
-    return type == LOGITS_BF16 ? launch_type<LOGITS_BF16>(p, s) : launch_type<LOGITS_F32>(p, s);
+    if (type == LOGITS_F16) return launch_type<LOGITS_F16>(waves, p, s);
+    return type == LOGITS_BF16 ? launch_type<LOGITS_BF16>(waves, p, s) : launch_type<LOGITS_F32>(waves, p, s);
 }
 
 }  // namespace mpg
