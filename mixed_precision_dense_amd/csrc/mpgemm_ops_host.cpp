@@ -46,13 +46,14 @@ OpPlan skinny(int64_t tiles_m, int64_t n, int fm, int w) {
 // and one that fills the CUs, take (us)
 //   256: 18 - 22, 28 - 36, 57 - 78        128: 9, 14, 36 and 10, 21, 52
 //    64: 5, 7, 22 and 8, 17, 46
-// and in between a round grows with every 256 tiles.
-double tiles_time(int edge, int64_t tiles, int64_t k, double weight) {
+// and in between a round grows with every 256 tiles.  crowded: what an epilogue of 64-wide tiles that fill the
+// CUs costs, times one of its own (the gated products', which move two to five times as much as they compute).
+double tiles_time(int edge, int64_t tiles, int64_t k, double weight, double crowded = 1.0) {
     struct Fit { int per_cu; double alone, alone_k, full, full_k, per_weight; };
     const Fit f = edge == 256 ? Fit{1, 15.5, 0.0195, 15.5, 0.0195, 5.0}
                   : edge == 128 ? Fit{2, 6.0, 0.0098, 6.0, 0.0155, 1.7} : Fit{4, 3.2, 0.006, 4.0, 0.014, 1.0};
     const double kk = (double)ceil_div(k, 128) * 128.0, epilogue = f.per_weight * weight;
-    const double alone = f.alone + f.alone_k * kk + epilogue, full = f.full + f.full_k * kk + epilogue;
+    const double alone = f.alone + f.alone_k * kk + epilogue, full = f.full + f.full_k * kk + epilogue * (edge == 64 ? crowded : 1.0);
     const int64_t slots = f.per_cu * kCus, left = tiles % slots;
     double last = 0.0;
     if (left > 0) last = f.per_cu == 1 ? alone : alone + (full - alone) * (double)(ceil_div(left, kCus) - 1) / (double)(f.per_cu - 1);
@@ -61,10 +62,10 @@ double tiles_time(int edge, int64_t tiles, int64_t k, double weight) {
 
 // The edge with the least estimated time; tiles(edge) counts the tiles.
 template <typename Tiles>
-int best_edge(int64_t k, double weight, Tiles &&tiles) {
+int best_edge(int64_t k, double weight, Tiles &&tiles, double crowded = 1.0) {
     int best = 256;
     for (int e = 128; e >= 64; e /= 2)
-        if (tiles_time(e, tiles(e), k, weight) < tiles_time(best, tiles(best), k, weight)) best = e;
+        if (tiles_time(e, tiles(e), k, weight, crowded) < tiles_time(best, tiles(best), k, weight, crowded)) best = e;
     return best;
 }
 
@@ -124,17 +125,52 @@ OpPlan grouped_plan(int64_t rows, int64_t groups, int64_t n, int64_t k, bool tb,
 double gated_weight(int act, bool kept) { return 0.5 * forward_weight(act, false, false) + (kept ? 0.7 : 0.0); }
 double gated_grad_weight(int act, bool h) { return slope_weight(act) + 1.5 + (h ? 0.7 : 0.0); }
 
-OpPlan gated_plan(int64_t groups, int64_t rows, int64_t n, int64_t k, bool tb, double weight) {
+// The shape of the gated product's kernel for few rows.  Measured (us; rows of 16 / columns of 16 /
+// waves of a workgroup; BF16, B stored n x k unless "k x n"):
+//   few workgroups (below 384 of 16 columns): eight waves and 16 columns, and above 16 rows 32 rows each
+//     8 x 2501 x 1001 1/1/8 6.3, 1/2/8 7.1;  24 x 2501 x 1001 2/1/8 6.4, 2/2/8 8.0;  40 x 1408 x 2048 2/1/8 11.1,
+//     4/2/8 17;  64 x 2501 x 1001 2/2/8 8.2, 2/1/8 above 9.9, 4/2/8 9.9;  k x n 8 x 1408 x 2048 1/1/8 10.3, 1/2/8 11.0
+//   more of them: 1 x 8192 x 4096 1/1/4 27.3, 1/1/8 29.0;  16 x 8192 x 4096 1/2/4 31.2, 1/1/4 32.9;  8 x 14336 x 4096
+//     1/2/4 53.7, 1/1/4 above 54;  24 x 14336 x 4096 2/4/4 56.1, 64-wide tiles 58.1;  64 x 8192 x 4096 4/2/8 42.6,
+//     tiles 45.3;  k x n, whose rows come in pieces of 32 w bytes: 8 x 14336 x 4096 1/4/4 51.7, 1/2/4 70.5;
+//     24 x 14336 x 4096 2/4/4 56.1, 2/2/8 76.6;  40 x 8192 x 4096 2/4/4 42.0, 4/2/8 42.8
+//   experts, 1408 x 2048, 32 of them: 64 rows 1/1/4 60, 1/2/4 63 (k x n 1/4/4 61, 1/2/4 67);  256 rows 1/2/4 78, 1/1/4
+//     81 (66, 84);  512 rows 2/4/4 88, 64-wide tiles 87 (78, 91)
+static bool gated_few(int64_t groups, int64_t rows, int64_t n, bool tb, OpPlan &p) {
     const int64_t owners = groups < rows ? groups : rows;   // an expert's last tile may be short
     const int64_t mean = groups > 0 ? ceil_div(rows, groups) : rows;
-    auto few = [&](int fm, int w) { return skinny(groups > 0 ? rows / (16 * fm) + owners : 1, n, fm, w); };
-    if (mean <= (groups > 0 ? 10 : 16) && n <= ((int64_t)1 << 22)) return few(1, tb ? 1 : 2);
-    if (mean <= 32 && few(2, 2).tiles_m * ceil_div(n, 32) <= 384) return few(2, 2);
-    if (groups == 0 && rows <= 64 && ceil_div(n, 32) <= kCus) return few(4, 2);
+    if (mean > 64 || n > ((int64_t)1 << 22)) return false;
+    auto shape = [&](int fm, int w, int waves) {
+        p = OpPlan{true, fm, w, waves, 16 * fm, 16 * w, groups > 0 ? rows / (16 * fm) + owners : ceil_div(rows, 16 * fm), ceil_div(n, 16 * w)};
+        return true;
+    };
+    const int64_t strips = ceil_div(n, 16) * (groups > 0 ? owners : 1);
+    if (strips < 384) {
+        if (mean <= 16) return shape(1, 1, 8);
+        return mean <= 32 || strips <= 128 ? shape(2, 1, 8) : shape(2, 2, 8);
+    }
+    if (mean <= (groups > 0 ? 10 : 16)) {
+        if (!tb) return shape(1, 4, 4);
+        return mean <= (groups > 0 ? 5 : 8) && (groups > 0 || strips < 768) ? shape(1, 1, 4) : shape(1, 2, 4);
+    }
+    if (groups > 0) return mean <= 16 && shape(2, 4, 4);
+    if (mean <= 32) return strips < 640 ? shape(2, 2, 8) : shape(2, 4, 4);
+    return strips <= 512 && (tb ? shape(4, 2, 8) : shape(2, 4, 4));
+}
+
+// (us, 64 / 128 / 256: 1000 x 2048 x 512 with both kept 14.8 / 10.4 / 22.7;  its gradient 15.4 / 19.4 / 45;  gradient
+// 4096 x 1024 x 256 28 / 21.6 / 42, 4000 rows of 16 experts 704 x 1024 31 / 26 / 55;  8192 x 4096 x 2048 488 / 249 / 225,
+// gradient 354 / 190 / 164)
+constexpr double kGatedCrowded = 3.5;
+
+OpPlan gated_plan(int64_t groups, int64_t rows, int64_t n, int64_t k, bool tb, double weight) {
+    const int64_t owners = groups < rows ? groups : rows;
+    OpPlan p;
+    if (gated_few(groups, rows, n, tb, p)) return p;
     // (an edge's tile holds half as many outputs a row; half a tile per expert is lost on average)
     const int e = best_edge(k, weight, [&](int64_t t) {
         return (groups > 0 ? rows / t + owners / 2 : ceil_div(rows, t)) * ceil_div(n, t / 2);
-    });
+    }, kGatedCrowded);
     return OpPlan{false, 0, 0, 0, e, e / 2, groups > 0 ? rows / e + owners : ceil_div(rows, e), ceil_div(n, e / 2)};
 }
 
@@ -142,7 +178,7 @@ OpPlan gated_grad_plan(int64_t groups, int64_t rows, int64_t n, int64_t k, doubl
     const int64_t owners = groups < rows ? groups : rows;
     const int e = best_edge(k, weight, [&](int64_t t) {
         return (groups > 0 ? rows / t + owners / 2 : ceil_div(rows, t)) * ceil_div(n, t);
-    });
+    }, kGatedCrowded);
     OpPlan p = tiled(rows, n, e);
     if (groups > 0) p.tiles_m = rows / e + owners;
     return p;

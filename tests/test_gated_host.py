@@ -131,7 +131,7 @@ def test_backward_refusals(check):
     assert mp.mpgemm_gated_grad_workspace_size(0, 5, 5) == 0 and mp.mpgemm_gated_grad_workspace_size(1, BIG, 5) == 0
 
 
-SIZES = [1, 5, 15, 16, 17, 31, 33, 64, 65, 100, 500, 1000, 4000, 10000, 24000, 100000, 1000000]
+SIZES = [1, 5, 15, 16, 17, 31, 33, 64, 65, 100, 500, 1000, 4000, 8000, 10000, 24000, 100000, 1000000]
 KS = [1, 64, 200, 1000, 4000]
 
 
