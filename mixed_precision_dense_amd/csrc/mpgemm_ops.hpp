@@ -118,6 +118,7 @@ struct CeRows {
 int launch_ce_rows(bool bf16, int m, int n, const int64_t *target, const float *mass, const float *lse, const float *grad,
                    const CeRows &rows, void *stream);
 constexpr int64_t kNoColumn = INT64_MAX / 2;
+constexpr int kMostTop = 1024;   // entries of a teacher's row
 // A teacher's top logits, as mpgemm_teacher_t gives them.
 struct Teacher {
     int top;
@@ -127,10 +128,9 @@ struct Teacher {
     float scale;
     const float *lse;   // or nullptr
 };
-int launch_picked(bool bf16, const Teacher &t, int m, int n, int k, float alpha, const void *X, int64_t ldx, const void *W,
-                  int64_t ldw, float *picked, void *stream);
-int launch_distill_merge(const Teacher &t, const CeStat *stats, int parts, int m, int n, const float *picked, float *loss, float *lse,
-                         void *stream);
+// the loss from the statistics and the logits at the teacher's columns, which are formed and kept too
+int launch_distill_merge(bool bf16, const Teacher &t, const CeStat *stats, int parts, int m, int n, int k, float alpha, const void *X,
+                         int64_t ldx, const void *W, int64_t ldw, float *picked, float *loss, float *lse, void *stream);
 int launch_mass(const Teacher &t, int m, int n, float *level, float *mass, void *stream);
 int launch_scatter(bool bf16, const Teacher &t, int m, int n, int first, int have, const float *level, const float *mass,
                    const float *lse, const float *picked, const int *place, const float *weight, void *P, int64_t ldp, void *stream);

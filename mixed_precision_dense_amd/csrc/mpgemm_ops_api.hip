@@ -397,8 +397,8 @@ mpgemm_status_t mpgemm_run_linear_distill(mpgemm_handle_t handle, int64_t m, int
     p.stats = (mpg::CeStat *)workspace;
     p.parts = L.parts;
     MPGEMM_TRY(launch(L.logits, bf16, false, true, p, stream));
-    MPGEMM_TRY(queued(mpg::launch_picked(bf16, t, (int)m, (int)n, (int)k, *alpha, X, ldx, W, ldw, picked, stream)));
-    return queued(mpg::launch_distill_merge(t, p.stats, L.parts, (int)m, (int)n, picked, loss, lse, stream));
+    return queued(mpg::launch_distill_merge(bf16, t, p.stats, L.parts, (int)m, (int)n, (int)k, *alpha, X, ldx, W, ldw, picked, loss, lse,
+                                            stream));
 }
 
 mpgemm_status_t mpgemm_run_linear_distill_grad(mpgemm_handle_t handle, int64_t m, int64_t n, int64_t k, const float *alpha,

@@ -642,7 +642,7 @@ namespace {
 
 mpgemm_status_t check_teacher(const mpgemm_teacher_t *t) {
     if (!t || t->top < 1 || t->ld < t->top) return MPGEMM_STATUS_INVALID_VALUE;
-    return t->top <= kMaxTop && t->ld <= kOpMaxSize ? MPGEMM_STATUS_SUCCESS : MPGEMM_STATUS_NOT_SUPPORTED;
+    return t->top <= mpg::kMostTop && t->ld <= kOpMaxSize ? MPGEMM_STATUS_SUCCESS : MPGEMM_STATUS_NOT_SUPPORTED;
 }
 
 mpgemm_status_t check_teacher_layout(const mpgemm_teacher_t *t) {
@@ -653,7 +653,7 @@ mpgemm_status_t check_teacher_layout(const mpgemm_teacher_t *t) {
 
 uint64_t mpgemm_linear_distill_workspace_size(int64_t m, int64_t n, int64_t k, int64_t top, mpgemm_dtype_t type, int train) {
     DistillLayout D;
-    if (!half_type(type) || top < 1 || top > kMaxTop || !distill_layout(m, n, k, train != 0, D)) return 0;
+    if (!half_type(type) || top < 1 || top > mpg::kMostTop || !distill_layout(m, n, k, train != 0, D)) return 0;
     return m == 0 ? 0 : D.total;
 }
 

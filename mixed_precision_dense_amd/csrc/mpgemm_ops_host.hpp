@@ -60,7 +60,6 @@ struct DistillLayout {
     uint64_t off_level, off_mass, total;
 };
 bool distill_layout(int64_t m, int64_t n, int64_t k, bool train, DistillLayout &D);
-constexpr int64_t kMaxTop = 1024;   // entries of a teacher's row
 
 // Log probabilities: the parts of a row (a workgroup each) and where they are kept.
 struct LogprobLayout {

@@ -61,9 +61,49 @@ __device__ __forceinline__ void teacher_row(const Teacher &t, int64_t row, int n
     mass = t.lse != nullptr || sum == 0.0f || sum != sum ? sum : 1.0f;
 }
 
-// picked[row][j] = alpha X(row) . W(index): a wave takes kEntries entries of a row, whose columns' rows of
-// W it reads side by side (bound by those reads: top * k * 2 bytes a row, mostly from beyond the L2).
+// picked[row][j] = alpha X(row) . W(index) for the row's entries j0 .. j0 + kEntries - 1, by a wave that reads
+// their columns' rows of W side by side.  Those reads (top * k * 2 bytes a row, from beyond the L2 as a rule) bound
+// it where there are many rows (4096 rows of 64 entries, k = 4096: 7 TB/s), the chain of a wave's turns where
+// there are few.
 constexpr int kEntries = 4;
+template <int IN>
+__device__ __forceinline__ void pick(const Teacher &t, int64_t row, int j0, int n, int k, float alpha, const uint16_t *X, int64_t ldx,
+                                     const uint16_t *W, int64_t ldw, int lane, float (&out)[kEntries]) {
+    const uint16_t *x = X + row * ldx;
+    const uint16_t *w[kEntries];
+    bool counts[kEntries];
+#pragma unroll
+    for (int e = 0; e < kEntries; ++e) {
+        const int v = entry_column(t, row, j0 + e, n);
+        counts[e] = v >= 0;
+        w[e] = W + (int64_t)(counts[e] ? v : 0) * ldw;
+        out[e] = 0.0f;
+    }
+#pragma unroll 2
+    for (int c = 8 * lane; c < k; c += 512) {
+        float a[8];
+        u32x4 b[kEntries];
+        const u32x4 xa = *(const u32x4 *)(x + c);
+#pragma unroll
+        for (int e = 0; e < kEntries; ++e) b[e] = *(const u32x4 *)(w[e] + c);
+        widen8<IN>(xa, a);
+#pragma unroll
+        for (int e = 0; e < kEntries; ++e) {
+            float v[8];
+            widen8<IN>(b[e], v);
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+                if (c + q < k) out[e] = __builtin_fmaf(a[q], v[q], out[e]);
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < kEntries; ++e) {
+        const float s = wave_sum(out[e]);
+        out[e] = counts[e] ? alpha * s : 0.0f;
+    }
+}
+
+// All of a call's, a wave per kEntries of them.
 template <int IN>
 __global__ __launch_bounds__(64 * kWaves) void picked_kernel(Teacher t, int m, int n, int k, float alpha, const uint16_t *X,
                                                              int64_t ldx, const uint16_t *W, int64_t ldw, float *picked) {
@@ -73,48 +113,33 @@ __global__ __launch_bounds__(64 * kWaves) void picked_kernel(Teacher t, int m, i
     for (int64_t item = (int64_t)blockIdx.x * kWaves + wave; item < items; item += (int64_t)gridDim.x * kWaves) {
         const int64_t row = item / groups;
         const int j0 = (int)(item - row * groups) * kEntries;
-        const uint16_t *x = X + row * ldx;
-        const uint16_t *w[kEntries];
-        bool counts[kEntries];
-        float dot[kEntries];
+        float z[kEntries];
+        pick<IN>(t, row, j0, n, k, alpha, X, ldx, W, ldw, lane, z);
 #pragma unroll
-        for (int e = 0; e < kEntries; ++e) {
-            const int v = entry_column(t, row, j0 + e, n);
-            counts[e] = v >= 0;
-            w[e] = W + (int64_t)(counts[e] ? v : 0) * ldw;
-            dot[e] = 0.0f;
-        }
-#pragma unroll 2
-        for (int c = 8 * lane; c < k; c += 512) {
-            float a[8];
-            u32x4 b[kEntries];
-            const u32x4 xa = *(const u32x4 *)(x + c);
-#pragma unroll
-            for (int e = 0; e < kEntries; ++e) b[e] = *(const u32x4 *)(w[e] + c);
-            widen8<IN>(xa, a);
-#pragma unroll
-            for (int e = 0; e < kEntries; ++e) {
-                float v[8];
-                widen8<IN>(b[e], v);
-#pragma unroll
-                for (int q = 0; q < 8; ++q)
-                    if (c + q < k) dot[e] = __builtin_fmaf(a[q], v[q], dot[e]);
-            }
-        }
-#pragma unroll
-        for (int e = 0; e < kEntries; ++e) {
-            const float s = wave_sum(dot[e]);
-            if (lane == 0 && j0 + e < t.top) picked[row * t.ld + j0 + e] = counts[e] ? alpha * s : 0.0f;
-        }
+        for (int e = 0; e < kEntries; ++e)
+            if (lane == 0 && j0 + e < t.top) picked[row * t.ld + j0 + e] = z[e];
     }
 }
 
-// One workgroup per row: lse from the parts' statistics, then the loss from the picked logits.
-__global__ __launch_bounds__(64 * kWaves) void distill_merge_kernel(Teacher t, const CeStat *stats, int parts, int m, int n,
-                                                                    const float *picked, float *loss, float *lse) {
-    __shared__ float share[kWaves][2];
-    const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
+// One workgroup per row: lse from the parts' statistics, then the loss from the picked logits, which it
+// forms itself (PICK) or finds formed.
+constexpr int kMergeWaves = 8;
+template <int IN, bool PICK>
+__global__ __launch_bounds__(64 * kMergeWaves) void distill_merge_kernel(Teacher t, const CeStat *stats, int parts, int m, int n, int k,
+                                                                         float alpha, const uint16_t *X, int64_t ldx,
+                                                                         const uint16_t *W, int64_t ldw, float *picked, float *loss,
+                                                                         float *lse) {
+    __shared__ float share[kMergeWaves][2];
+    __shared__ float own_picked[PICK ? kMostTop : 1];
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), lane = threadIdx.x % 64;
     for (int64_t row = blockIdx.x; row < m; row += gridDim.x) {
+        for (int j0 = kEntries * wave; PICK && j0 < t.top; j0 += kEntries * kMergeWaves) {
+            float z[kEntries];
+            pick<IN>(t, row, j0, n, k, alpha, X, ldx, W, ldw, lane, z);
+#pragma unroll
+            for (int e = 0; e < kEntries; ++e)
+                if (lane == 0 && j0 + e < t.top) own_picked[j0 + e] = picked[row * t.ld + j0 + e] = z[e];
+        }
         const CeStat *st = stats + row * parts;
         float top = -__builtin_inff(), sum = 0.0f;
         auto join = [&](float o_top, float o_sum) {
@@ -122,12 +147,12 @@ __global__ __launch_bounds__(64 * kWaves) void distill_merge_kernel(Teacher t, c
             sum = sum * fast_exp2(top - base) + o_sum * fast_exp2(o_top - base);
             top = up;
         };
-        for (int i = threadIdx.x; i < parts; i += 4 * 64 * kWaves) {
+        for (int i = threadIdx.x; i < parts; i += 4 * 64 * kMergeWaves) {
             CeStat s[4];
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 s[q] = CeStat{-__builtin_inff(), 0.0f};
-                if (i + q * 64 * kWaves < parts) s[q] = st[i + q * 64 * kWaves];
+                if (i + q * 64 * kMergeWaves < parts) s[q] = st[i + q * 64 * kMergeWaves];
             }
 #pragma unroll
             for (int q = 0; q < 4; ++q) join(s[q].top, s[q].sum);
@@ -140,7 +165,7 @@ __global__ __launch_bounds__(64 * kWaves) void distill_merge_kernel(Teacher t, c
         }
         __syncthreads();
         if (wave == 0) {
-            for (int i = 1; i < kWaves; ++i) join(share[i][0], share[i][1]);
+            for (int i = 1; i < kMergeWaves; ++i) join(share[i][0], share[i][1]);
             const float l2 = top + __log2f(sum);
             float level2, mass;
             teacher_row(t, row, n, lane, level2, mass);
@@ -149,7 +174,7 @@ __global__ __launch_bounds__(64 * kWaves) void distill_merge_kernel(Teacher t, c
             for (int j = lane; j < t.top; j += 64) {
                 if (entry_column(t, row, j, n) < 0) continue;
                 const float y2 = f * t.logit[row * t.ld + j], q = share_of(y2, level2);
-                if (q != 0.0f) s = __builtin_fmaf(q, (y2 - level2) * kLn2 + (own - picked[row * t.ld + j]), s);
+                if (q != 0.0f) s = __builtin_fmaf(q, (y2 - level2) * kLn2 + (own - (PICK ? own_picked[j] : picked[row * t.ld + j])), s);
             }
             s = wave_sum(s);
             if (lane == 0) {
@@ -157,7 +182,7 @@ __global__ __launch_bounds__(64 * kWaves) void distill_merge_kernel(Teacher t, c
                 loss[row] = mass == 0.0f ? 0.0f : s;
             }
         }
-        __syncthreads();   // share is written again
+        __syncthreads();   // share and own_picked are written again
     }
 }
 
@@ -211,32 +236,44 @@ __global__ __launch_bounds__(64 * kWaves) void scatter_kernel(Teacher t, int m, 
     }
 }
 
-int launch(const void *kernel, int64_t blocks, void **args, void *stream) {
+int launch(const void *kernel, int64_t blocks, int waves, void **args, void *stream) {
     if (blocks == 0) return (int)hipSuccess;
-    return (int)hipLaunchKernel(kernel, dim3((unsigned)(blocks < kMostBlocks ? blocks : kMostBlocks)), dim3(64 * kWaves), args, 0,
+    return (int)hipLaunchKernel(kernel, dim3((unsigned)(blocks < kMostBlocks ? blocks : kMostBlocks)), dim3((unsigned)(64 * waves)), args, 0,
                                 (hipStream_t)stream);
 }
 int64_t by_waves(int64_t items) { return (items + kWaves - 1) / kWaves; }
 
-}  // namespace
-
-int launch_picked(bool bf16, const Teacher &t, int m, int n, int k, float alpha, const void *X, int64_t ldx, const void *W,
-                  int64_t ldw, float *picked, void *stream) {
-    const uint16_t *x = (const uint16_t *)X, *w = (const uint16_t *)W;
-    void *args[] = {const_cast<Teacher *>(&t), &m, &n, &k, &alpha, &x, &ldx, &w, &ldw, &picked};
-    return launch(bf16 ? reinterpret_cast<const void *>(&picked_kernel<IN_BF16>) : reinterpret_cast<const void *>(&picked_kernel<IN_F16>),
-                  by_waves((int64_t)m * ((t.top + kEntries - 1) / kEntries)), args, stream);
+template <int IN>
+int launch_merge_type(const Teacher &t, const CeStat *stats, int parts, int m, int n, int k, float alpha, const uint16_t *x, int64_t ldx,
+                      const uint16_t *w, int64_t ldw, float *picked, float *loss, float *lse, void *stream) {
+    // The merging kernel picks the logits itself where its waves have a turn of them at most, or rows keep all
+    // CUs busy: that saves a launch (us with the loss before it, n = 32000, k = 4096, apart / itself: 8 rows of 20
+    // entries 73 / 66, 8 of 128 72 / 86, 8 of 1000 92 / 264, 64 of 64 72 / 77; k = 2048: 512 of 64 82 / 78, 4096 of 64
+    // 563 / 551).
+    const bool itself = t.top <= kEntries * kMergeWaves || m >= 512;
+    if (!itself) {
+        void *args[] = {const_cast<Teacher *>(&t), &m, &n, &k, &alpha, &x, &ldx, &w, &ldw, &picked};
+        const int e = launch(reinterpret_cast<const void *>(&picked_kernel<IN>), by_waves((int64_t)m * ((t.top + kEntries - 1) / kEntries)),
+                             kWaves, args, stream);
+        if (e != 0) return e;
+    }
+    void *args[] = {const_cast<Teacher *>(&t), &stats, &parts, &m, &n, &k, &alpha, &x, &ldx, &w, &ldw, &picked, &loss, &lse};
+    return launch(itself ? reinterpret_cast<const void *>(&distill_merge_kernel<IN, true>)
+                         : reinterpret_cast<const void *>(&distill_merge_kernel<IN, false>),
+                  m, kMergeWaves, args, stream);
 }
 
-int launch_distill_merge(const Teacher &t, const CeStat *stats, int parts, int m, int n, const float *picked, float *loss, float *lse,
-                         void *stream) {
-    void *args[] = {const_cast<Teacher *>(&t), &stats, &parts, &m, &n, &picked, &loss, &lse};
-    return launch(reinterpret_cast<const void *>(&distill_merge_kernel), m, args, stream);
+}  // namespace
+
+int launch_distill_merge(bool bf16, const Teacher &t, const CeStat *stats, int parts, int m, int n, int k, float alpha, const void *X,
+                         int64_t ldx, const void *W, int64_t ldw, float *picked, float *loss, float *lse, void *stream) {
+    const auto f = bf16 ? launch_merge_type<IN_BF16> : launch_merge_type<IN_F16>;
+    return f(t, stats, parts, m, n, k, alpha, (const uint16_t *)X, ldx, (const uint16_t *)W, ldw, picked, loss, lse, stream);
 }
 
 int launch_mass(const Teacher &t, int m, int n, float *level, float *mass, void *stream) {
     void *args[] = {const_cast<Teacher *>(&t), &m, &n, &level, &mass};
-    return launch(reinterpret_cast<const void *>(&mass_kernel), by_waves(m), args, stream);
+    return launch(reinterpret_cast<const void *>(&mass_kernel), by_waves(m), kWaves, args, stream);
 }
 
 int launch_scatter(bool bf16, const Teacher &t, int m, int n, int first, int have, const float *level, const float *mass,
@@ -244,7 +281,7 @@ int launch_scatter(bool bf16, const Teacher &t, int m, int n, int first, int hav
     uint16_t *p = (uint16_t *)P;
     void *args[] = {const_cast<Teacher *>(&t), &m, &n, &first, &have, &level, &mass, &lse, &picked, &place, &weight, &p, &ldp};
     return launch(bf16 ? reinterpret_cast<const void *>(&scatter_kernel<IN_BF16>) : reinterpret_cast<const void *>(&scatter_kernel<IN_F16>),
-                  by_waves(m), args, stream);
+                  by_waves(m), kWaves, args, stream);
 }
 
 }  // namespace mpg
