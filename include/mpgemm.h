@@ -576,7 +576,8 @@ mpgemm_status_t mpgemm_run_gated(mpgemm_handle_t handle, mpgemm_op_t transb, int
  * of its D (A the block's output gradient, B the down projection's weights),
  *   dG = E U act'(G),  dU = E act(G),  H = act(G) U,
  * with dG and dU the pair at D, and the column sums of both, summed in FP32 before the rounding in a
- * fixed order.  m == 0 gives dbias = 0.
+ * fixed order.  D == kept is allowed when the two pairs are alike in type, leading dimension and
+ * stride: the gradients then take the factors' place.  m == 0 gives dbias = 0.
  *   workspace: mpgemm_gated_grad_workspace_size(1, m, n) bytes (none without dbias). */
 mpgemm_status_t mpgemm_run_gated_grad(mpgemm_handle_t handle, mpgemm_op_t transb, int64_t m,
                                       int64_t n, int64_t k, const float *alpha, const void *A,

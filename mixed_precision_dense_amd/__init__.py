@@ -146,6 +146,13 @@ def _ptr(x) -> Optional[int]:
     return int(x)
 
 
+def _vec(x) -> Optional[int]:
+    """_ptr of values that the library takes one after the other: a strided view (a column) is refused."""
+    if isinstance(x, torch.Tensor) and not x.is_contiguous():
+        raise ValueError(f"a vector with strides {x.stride()}: its values must follow each other in memory")
+    return _ptr(x)
+
+
 def _scalar(v, compute_type: int):
     """alpha / beta as the compute type's host scalar (float or int32_t)."""
     if compute_type == R_32I:
@@ -482,12 +489,12 @@ class Teacher:
 
     def __init__(self, top, index, logit, ld, scale=1.0, lse=None):
         self.held = (index, logit, lse)
-        self.struct = _TeacherStruct(top, _ptr(index), _ptr(logit), ld, scale, _ptr(lse))
+        self.struct = _TeacherStruct(top, _ptr(index), _ptr(logit), ld, scale, _vec(lse))
 
 
 def _linear_distill_args(m, n, k, alpha, X, dtype, ldx, W, ldw, teacher, loss, lse, picked, workspace,
                          workspace_bytes):
-    return (m, n, k, _f32(alpha), _ptr(X), _dtype(dtype), ldx, _ptr(W), ldw, _epi(teacher), _ptr(loss), _ptr(lse),
+    return (m, n, k, _f32(alpha), _ptr(X), _dtype(dtype), ldx, _ptr(W), ldw, _epi(teacher), _vec(loss), _vec(lse),
             _ptr(picked), _ptr(workspace), workspace_bytes)
 
 
@@ -505,8 +512,8 @@ def mpgemm_check_linear_distill(*args) -> int:
 
 def _linear_distill_grad_args(m, n, k, alpha, X, dtype, ldx, W, ldw, teacher, lse, picked, grad, dX, lddx, dW, lddw,
                               workspace, workspace_bytes):
-    return (m, n, k, _f32(alpha), _ptr(X), _dtype(dtype), ldx, _ptr(W), ldw, _epi(teacher), _ptr(lse), _ptr(picked),
-            _ptr(grad), _ptr(dX), lddx, _ptr(dW), lddw, _ptr(workspace), workspace_bytes)
+    return (m, n, k, _f32(alpha), _ptr(X), _dtype(dtype), ldx, _ptr(W), ldw, _epi(teacher), _vec(lse), _ptr(picked),
+            _vec(grad), _ptr(dX), lddx, _ptr(dW), lddw, _ptr(workspace), workspace_bytes)
 
 
 def mpgemm_run_linear_distill_grad(handle, m, n, k, alpha, X, dtype, ldx, W, ldw, teacher, lse, picked, grad, dX, lddx,
@@ -528,7 +535,7 @@ def mpgemm_linear_distill_workspace_size(m: int, n: int, k: int, top: int, dtype
 
 def _logprobs_args(m, n, alpha, Z, z_type, ldz, target, logprob, lse, entropy, top, top_index, top_logprob, ld_top,
                    workspace, workspace_bytes):
-    return (m, n, _f32(alpha), _ptr(Z), _dtype(z_type), ldz, _ptr(target), _ptr(logprob), _ptr(lse), _ptr(entropy), top,
+    return (m, n, _f32(alpha), _ptr(Z), _dtype(z_type), ldz, _vec(target), _vec(logprob), _vec(lse), _vec(entropy), top,
             _ptr(top_index), _ptr(top_logprob), ld_top, _ptr(workspace), workspace_bytes)
 
 
@@ -582,7 +589,7 @@ class GatedGrad:
 
     def __init__(self, act="none", kept=None, ld_kept=0, stride_kept=0, H=None, ldh=0, dbias=None):
         self.held = (kept, H, dbias)
-        self.struct = _GatedGradStruct(_act(act), _ptr(kept), ld_kept, stride_kept, _ptr(H), ldh, _ptr(dbias))
+        self.struct = _GatedGradStruct(_act(act), _ptr(kept), ld_kept, stride_kept, _ptr(H), ldh, _vec(dbias))
 
 
 def _gated_args(transb, m, n, k, alpha, A, a_type, lda, B, b_type, ldb, stride_up, gated, D, d_type, ldd):
