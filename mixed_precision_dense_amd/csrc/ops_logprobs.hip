@@ -158,15 +158,28 @@ struct Stat {
         s += o.s;
         t += o.t;
     }
-    __device__ __forceinline__ void join_wave(float c) {
-#pragma unroll
-        for (int d = 1; d < 64; d *= 2) {
-            const Stat o = {__shfl_xor(m, d, 64), __shfl_xor(s, d, 64), __shfl_xor(t, d, 64)};
-            // (the lower lane's first, so that both halves of a pair come to the same bits)
-            Stat a = threadIdx.x & d ? o : *this, b = threadIdx.x & d ? *this : o;
-            a.join(b, c);
-            *this = a;
-        }
+    // The wave's in every lane: the maximum first, so that a lane rescales once.
+    __device__ __forceinline__ void join_wave(float c, int lane) {
+        float to = m;
+        over_lanes(lane, [&](auto d) { to = fmaxf(to, other_lane<decltype(d)::value>(to, lane)); });
+        rescale(to, c);
+        over_lanes(lane, [&](auto d) {
+            s += other_lane<decltype(d)::value>(s, lane);
+            t += other_lane<decltype(d)::value>(t, lane);
+        });
+    }
+    template <int D>
+    static __device__ __forceinline__ float other_lane(float v, int lane) {
+        return __builtin_bit_cast(float, xor_lane<D>(__builtin_bit_cast(uint32_t, v), lane));
+    }
+    template <typename F>
+    static __device__ __forceinline__ void over_lanes(int lane, F &&f) {
+        f(std::integral_constant<int, 1>{});
+        f(std::integral_constant<int, 2>{});
+        f(std::integral_constant<int, 4>{});
+        f(std::integral_constant<int, 8>{});
+        f(std::integral_constant<int, 16>{});
+        f(std::integral_constant<int, 32>{});
     }
 };
 
@@ -221,11 +234,37 @@ struct Share {
     uint64_t found[NW][kFound];   // (or a list of 64)
 
     __device__ __forceinline__ void join_stats(Stat &st, float c, int wave, int lane) {
-        st.join_wave(c);
+        st.join_wave(c, lane);
         if (lane == 0) stat[wave] = st;
         __syncthreads();
         if (wave == 0)
             for (int i = 1; i < NW; ++i) st.join(stat[i], c);
+    }
+    // The list of all waves' found keys, by wave 0.  Up to 64 of them (as a rule little more than `top`) are put
+    // in order by how many are above each; more are offered to the list.
+    __device__ __forceinline__ void order_found(TopList &list, int lane) {
+        int all = 0, from = 0, at = lane;
+#pragma unroll
+        for (int i = 0; i < NW; ++i) {
+            if (lane >= all) {
+                from = i;
+                at = lane - all;
+            }
+            all += __builtin_amdgcn_readfirstlane(count[i]);
+        }
+        if (all <= 64) {
+            const uint64_t k = lane < all ? found[from][at] : 0;
+            int above = 0;
+            for (int j = 0; j < all; ++j) above += lane_value(k, j) > k ? 1 : 0;
+            // (every key has been read: found is free)
+            if (lane < all) found[0][above] = k;
+            __builtin_amdgcn_wave_barrier();
+            list.key = lane < all ? found[0][lane] : 0;
+            list.last = lane_value(list.key, list.top - 1);
+            return;
+        }
+        for (int i = 0; i < NW; ++i)
+            for (int b = 0; b < count[i]; b += 64) list.offer(b + lane < count[i] ? found[i][b + lane] : 0, lane);
     }
     __device__ __forceinline__ void join_lists(TopList &list, int wave, int lane) {
         __syncthreads();
@@ -383,9 +422,7 @@ __global__ __launch_bounds__(64 * NW) void logprobs_kernel(LogprobParams p) {
                 part.list_all(list, wave);
                 share.join_lists(list, wave, lane);
             } else if (wave == 0) {
-                for (int i = 0; i < NW; ++i)
-                    for (int b = 0; b < share.count[i]; b += 64)
-                        list.offer(b + lane < share.count[i] ? share.found[i][b + lane] : 0, lane);
+                share.order_found(list, lane);
             }
         }
         share.join_stats(st, c, wave, lane);
