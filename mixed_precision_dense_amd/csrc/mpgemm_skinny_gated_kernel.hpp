@@ -1,4 +1,4 @@
-// mpgemm_gated_skinny_kernel.hpp -- the gated product for few rows: 16 FM rows by 16 W outputs per
+// mpgemm_skinny_gated_kernel.hpp -- the gated product for few rows: 16 FM rows by 16 W outputs per
 // workgroup, D = act(alpha A op(Bg) + bg) * (alpha A op(Bu) + bu).
 //
 // Both weights are read once and everything else is small, so that the bytes of the weights bound it.

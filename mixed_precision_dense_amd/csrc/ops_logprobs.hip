@@ -12,9 +12,11 @@
 // does not depend on the order of reading.  While the logits stream by, only the maximum of every 32 elements
 // of a lane is kept (in the LDS).  The top-th largest of the 256 lanes' maxima is then a bound T that
 // at least `top` elements reach; few of the kept maxima do, and only their elements are read once more
-// (4095 x 128000 BF16 with 8: about 9 of 4096 maxima a row).  What reaches T is sorted across the lanes of
-// one wave.  Where too many do (rows of equal values) or a NaN hides the maxima, the workgroup goes
-// through its part again with lists that let in what is above their last place.  With such lists alone,
+// (4095 x 128000 BF16 with 8: about 9 of 4096 maxima a row).  What reaches T is put
+// in order by one wave.  Where too many do, as equal values, those above T are taken and then the first that
+// equal it; where even these are too many (rising rows) or a NaN hides the maxima, the workgroup goes through
+// its part again with lists that let in what is above their last place (4095 x 128000 BF16: constant rows and
+// rows masked but for ten as random ones; rising rows so with 20, but 4.3 ms with 64).  With such lists alone,
 // kept while streaming, 4095 x 128000 BF16 took 340 us with 8 alternatives and 640 with 64; so 198 and 211
 // (5.3 and 5.0 TB/s), against 188 without any: the row's bytes bound it.  Of a short row most of the time
 // is the chain of dependent lane exchanges (16 x 4096: 8.3 us, an empty launch 4).
@@ -299,33 +301,77 @@ struct Part {
         return v < end && v * E + e < n ? (uint64_t)order_of(x) << 32 | (0xFFFFFFFFu - (uint32_t)(v * E + e)) : 0;
     }
 
+    // Offers the elements of 64 vectors, or those of one order.
+    __device__ __forceinline__ void offer_vectors(TopList &list, int v, uint32_t only) const {
+        float x[E];
+        Logits<T>::widen(load(v), x);
+        uint32_t left = (1u << E) - 1;     // bit e: element e has not been offered
+        while (true) {
+            uint64_t best = 0;
+            int at = 0;
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                const uint64_t k = left >> e & 1 ? key(x[e], v, e) : 0;
+                if (k > best && (only == 0 || (uint32_t)(k >> 32) == only)) {
+                    best = k;
+                    at = e;
+                }
+            }
+            const bool in = best > list.last;
+            if (!__any(in)) return;
+            list.offer(best, lane);
+            if (in) left &= ~(1u << at);
+        }
+    }
     // The wave's largest by its list alone, whatever the part holds.
     __device__ __forceinline__ void list_all(TopList &list, int wave) const {
         for (int base = first + 64 * UN * wave; base < end; base += 64 * UN * NW)
 #pragma unroll 1
-            for (int i = 0; i < UN && base + 64 * i < end; ++i) {
-                const int v = vector(base, i);
-                float x[E];
-                widen(load(v), v, whole(base, i), x);
-                // (bit e of `left`: element e has not been offered)
-                uint32_t left = (1u << E) - 1;
-                while (true) {
-                    uint64_t best = 0;
-                    int at = 0;
+            for (int i = 0; i < UN && base + 64 * i < end; ++i) offer_vectors(list, vector(base, i), 0);
+    }
+    // Fills a list that holds all above `bound` with the first elements that equal it (there are enough: the
+    // maxima that make the bound).
+    __device__ __forceinline__ void list_equal(TopList &list, uint32_t bound) const {
+        for (int base = first; base < end && list.last == 0; base += 64) offer_vectors(list, vector(base, 0), bound);
+    }
+    // The wave's elements of order `least` and more, found by the maxima of its turns; returns how many, or
+    // more than kFound where there is no room for them.
+    __device__ __forceinline__ int find(const float (*group_max)[64], int turns, uint32_t least, uint16_t *ids, uint64_t *found, int wave) const {
+        // the lanes' turns that reach it, packed
+        int groups = 0;
+        for (int g = 0; g < turns; ++g) {
+            const bool in = order_of(group_max[g][lane]) >= least;
+            const uint64_t mask = __ballot(in);
+            const int at = groups + __builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0u));
+            if (in && at < 64) ids[at] = (uint16_t)(g * 64 + lane);
+            groups += __popcll(mask);
+        }
+        if (groups > 64) return kFound + 1;
+        // their elements that reach it
+        int count = 0;
+        for (int i = lane; i - lane < groups * UN && count <= kFound; i += 64) {
+            uint64_t k[E];
 #pragma unroll
-                    for (int e = 0; e < E; ++e) {
-                        const uint64_t k = left >> e & 1 ? key(x[e], v, e) : 0;
-                        if (k > best) {
-                            best = k;
-                            at = e;
-                        }
-                    }
-                    const bool in = best > list.last;
-                    if (!__any(in)) break;
-                    list.offer(best, lane);
-                    if (in) left &= ~(1u << at);
-                }
+            for (int e = 0; e < E; ++e) k[e] = 0;
+            if (i < groups * UN) {
+                const int id = ids[i / UN];
+                const int v = first + 64 * UN * (wave + NW * (id / 64)) + 64 * (i % UN) + id % 64;
+                float x[E];
+                Logits<T>::widen(load(v), x);
+#pragma unroll
+                for (int e = 0; e < E; ++e) k[e] = key(x[e], v, e);
             }
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                const bool in = k[e] != 0 && (uint32_t)(k[e] >> 32) >= least;
+                const uint64_t mask = __ballot(in);
+                if (mask == 0) continue;
+                const int at = count + __builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0u));
+                if (in && at < kFound) found[at] = k[e];
+                count += __popcll(mask);
+            }
+        }
+        return count;
     }
 };
 
@@ -381,48 +427,24 @@ __global__ __launch_bounds__(64 * NW) void logprobs_kernel(LogprobParams p) {
 #pragma unroll
             for (int i = 1; i < NW; ++i) best = merge_lanes(best, share.sorted[i][lane], lane);
             const uint32_t bound = (uint32_t)__builtin_amdgcn_readlane((int)best, p.top - 1);
-            // the lanes' turns that reach it, packed
-            int groups = 0;
-            for (int g = 0; g < turns; ++g) {
-                const bool in = order_of(group_max[wave][g][lane]) >= bound;
-                const uint64_t mask = __ballot(in);
-                const int at = groups + __builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0u));
-                if (in && at < 64) share.ids[wave][at] = (uint16_t)(g * 64 + lane);
-                groups += __popcll(mask);
-            }
-            int found = groups > 64 || nan ? kFound + 1 : 0;
-            // their elements that reach it
-            for (int i = lane; i - lane < groups * UN && found <= kFound; i += 64) {
-                uint64_t key[E];
-#pragma unroll
-                for (int e = 0; e < E; ++e) key[e] = 0;
-                if (i < groups * UN) {
-                    const int id = share.ids[wave][i / UN];
-                    const int v = first + 64 * UN * (wave + NW * (id / 64)) + 64 * (i % UN) + id % 64;
-                    float x[E];
-                    Logits<T>::widen(part.load(v), x);
-#pragma unroll
-                    for (int e = 0; e < E; ++e) key[e] = part.key(x[e], v, e);
+            // All that reach T; or, where too many do, those above it, and then the first ones that equal it (masks and
+            // other equal values); or everything again (rising values: the maxima say too little; NaN).
+            bool listed = false;
+            for (int turn = 0; turn < 2 && !listed; ++turn) {
+                const int found = nan ? kFound + 1 : part.find(group_max[wave], turns, bound + turn, share.ids[wave], share.found[wave], wave);
+                if (lane == 0) share.count[wave] = found;
+                __syncthreads();
+                listed = true;
+                for (int i = 0; i < NW; ++i) listed &= share.count[i] <= kFound;
+                if (listed && wave == 0) {
+                    share.order_found(list, lane);
+                    if (turn == 1 && list.last == 0) part.list_equal(list, bound);
                 }
-#pragma unroll
-                for (int e = 0; e < E; ++e) {
-                    const bool in = key[e] != 0 && (uint32_t)(key[e] >> 32) >= bound;
-                    const uint64_t mask = __ballot(in);
-                    if (mask == 0) continue;
-                    const int at = found + __builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0u));
-                    if (in && at < kFound) share.found[wave][at] = key[e];
-                    found += __popcll(mask);
-                }
+                __syncthreads();   // share is written again
             }
-            if (lane == 0) share.count[wave] = found;
-            __syncthreads();
-            bool listed = true;
-            for (int i = 0; i < NW; ++i) listed &= share.count[i] <= kFound;
             if (!listed) {
                 part.list_all(list, wave);
                 share.join_lists(list, wave, lane);
-            } else if (wave == 0) {
-                share.order_found(list, lane);
             }
         }
         share.join_stats(st, c, wave, lane);

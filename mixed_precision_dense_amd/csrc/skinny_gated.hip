@@ -1,6 +1,6 @@
 // Instances of the gated product's kernel for few rows (instantiated explicitly: host code that only
 // reaches a kernel through an inlined launcher does not reliably emit its launch stub).
-#include "mpgemm_gated_skinny_kernel.hpp"
+#include "mpgemm_skinny_gated_kernel.hpp"
 
 namespace mpg {
 
