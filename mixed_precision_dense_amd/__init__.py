@@ -148,8 +148,13 @@ def _ptr(x) -> Optional[int]:
 
 def _vec(x) -> Optional[int]:
     """_ptr of values that the library takes one after the other: a strided view (a column) is refused."""
-    if isinstance(x, torch.Tensor) and not x.is_contiguous():
-        raise ValueError(f"a vector with strides {x.stride()}: its values must follow each other in memory")
+    if x is None:
+        return None
+    if isinstance(x, torch.Tensor):
+        if not x.is_contiguous():
+            raise ValueError(f"a vector with strides {x.stride()}: its values must follow each other in memory")
+        if x.is_cuda:
+            return x.data_ptr()
     return _ptr(x)
 
 
@@ -323,9 +328,17 @@ def _act(act: Union[str, int]) -> int:
 
 
 def _f32(v):
-    """A scalar argument: the library reads it before the call returns and never writes it."""
+    """A scalar argument: the library reads it before the call returns and never writes it.  The first few
+    numbers that a program uses (temperatures, scales) are kept: making one takes 2 us, looking it up 0.1.
+    (Plain floats only: anything else could change its value under the same key.)"""
+    if type(v) is not float:
+        v = float(v)
     known = _F32.get(v)
-    return ctypes.byref(ctypes.c_float(v)) if known is None else known
+    if known is None:
+        known = ctypes.byref(ctypes.c_float(v))
+        if len(_F32) < 64:
+            _F32[v] = known
+    return known
 
 
 _F32 = {v: ctypes.byref(ctypes.c_float(v)) for v in (1.0, 0.0)}   # (equal keys: 0.0 stands for -0.0 too)

@@ -47,3 +47,14 @@ def test_workspaces(m, n):
     assert check(m=m, n=100, z_type="f32", ldz=100, workspace=None, workspace_bytes=0) == OK
     for bad in ((0, n, "f32", 20), (m, 0, "f32", 20), (m, n, "i8", 20), (m, n, "f32", 65), (m, n, "f32", -1), (BIG, n, "f32", 1)):
         assert mp.mpgemm_logprobs_workspace_size(*bad) == 0
+
+
+def test_scalars_that_change_their_value():
+    """A scalar is taken by its value at the call: a tensor that holds another one the next time is taken anew."""
+    import torch
+    alpha = torch.tensor(1.0)
+    assert check(alpha=alpha) == OK
+    alpha.fill_(-1.0)
+    assert check(alpha=alpha) == BAD
+    for i in range(200):                                     # more values than are kept
+        assert check(alpha=0.5 + i) == OK and check(alpha=-0.5 - i) == BAD
