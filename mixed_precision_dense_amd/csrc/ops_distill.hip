@@ -250,7 +250,7 @@ int launch_merge_type(const Teacher &t, const CeStat *stats, int parts, int m, i
     // CUs busy: that saves a launch (us with the loss before it, n = 32000, k = 4096, apart / itself: 8 rows of 20
     // entries 73 / 66, 8 of 128 72 / 86, 8 of 1000 92 / 264, 64 of 64 72 / 77; k = 2048: 512 of 64 82 / 78, 4096 of 64
     // 563 / 551).
-    const bool itself = t.top <= kEntries * kMergeWaves || m >= 512;
+    const bool itself = t.top <= kEntries * kMergeWaves || (int64_t)m * t.top * k >= ((int64_t)1 << 25);
     if (!itself) {
         void *args[] = {const_cast<Teacher *>(&t), &m, &n, &k, &alpha, &x, &ldx, &w, &ldw, &picked};
         const int e = launch(reinterpret_cast<const void *>(&picked_kernel<IN>), by_waves((int64_t)m * ((t.top + kEntries - 1) / kEntries)),
