@@ -146,15 +146,28 @@ def _ptr(x) -> Optional[int]:
     return int(x)
 
 
-def _vec(x) -> Optional[int]:
-    """_ptr of values that the library takes one after the other: a strided view (a column) is refused."""
+def _vec(x, dtype=torch.float32) -> Optional[int]:
+    """_ptr of values that the library takes one after the other, of the one type that it takes there: a
+    strided view (a column) and a tensor of another type are refused."""
     if x is None:
         return None
     if isinstance(x, torch.Tensor):
         if not x.is_contiguous():
             raise ValueError(f"a vector with strides {x.stride()}: its values must follow each other in memory")
+        if x.dtype is not dtype:
+            raise ValueError(f"a vector of {x.dtype}: its values must be {dtype}")
         if x.is_cuda:
             return x.data_ptr()
+    return _ptr(x)
+
+
+def _rows(x, dtype=torch.float32) -> Optional[int]:
+    """The same for rows of such values, whose distance the call is told."""
+    if isinstance(x, torch.Tensor):
+        if x.dim() > 0 and x.shape[-1] > 1 and x.stride(-1) != 1:
+            raise ValueError(f"rows with strides {x.stride()}: the values of a row must follow each other in memory")
+        if x.dtype is not dtype:
+            raise ValueError(f"rows of {x.dtype}: their values must be {dtype}")
     return _ptr(x)
 
 
@@ -502,13 +515,13 @@ class Teacher:
 
     def __init__(self, top, index, logit, ld, scale=1.0, lse=None):
         self.held = (index, logit, lse)
-        self.struct = _TeacherStruct(top, _ptr(index), _ptr(logit), ld, scale, _vec(lse))
+        self.struct = _TeacherStruct(top, _rows(index, torch.int64), _rows(logit), ld, scale, _vec(lse))
 
 
 def _linear_distill_args(m, n, k, alpha, X, dtype, ldx, W, ldw, teacher, loss, lse, picked, workspace,
                          workspace_bytes):
     return (m, n, k, _f32(alpha), _ptr(X), _dtype(dtype), ldx, _ptr(W), ldw, _epi(teacher), _vec(loss), _vec(lse),
-            _ptr(picked), _ptr(workspace), workspace_bytes)
+            _rows(picked), _ptr(workspace), workspace_bytes)
 
 
 def mpgemm_run_linear_distill(handle, m, n, k, alpha, X, dtype, ldx, W, ldw, teacher, loss, lse, picked, workspace,
@@ -525,7 +538,7 @@ def mpgemm_check_linear_distill(*args) -> int:
 
 def _linear_distill_grad_args(m, n, k, alpha, X, dtype, ldx, W, ldw, teacher, lse, picked, grad, dX, lddx, dW, lddw,
                               workspace, workspace_bytes):
-    return (m, n, k, _f32(alpha), _ptr(X), _dtype(dtype), ldx, _ptr(W), ldw, _epi(teacher), _vec(lse), _ptr(picked),
+    return (m, n, k, _f32(alpha), _ptr(X), _dtype(dtype), ldx, _ptr(W), ldw, _epi(teacher), _vec(lse), _rows(picked),
             _vec(grad), _ptr(dX), lddx, _ptr(dW), lddw, _ptr(workspace), workspace_bytes)
 
 
@@ -548,8 +561,8 @@ def mpgemm_linear_distill_workspace_size(m: int, n: int, k: int, top: int, dtype
 
 def _logprobs_args(m, n, alpha, Z, z_type, ldz, target, logprob, lse, entropy, top, top_index, top_logprob, ld_top,
                    workspace, workspace_bytes):
-    return (m, n, _f32(alpha), _ptr(Z), _dtype(z_type), ldz, _vec(target), _vec(logprob), _vec(lse), _vec(entropy), top,
-            _ptr(top_index), _ptr(top_logprob), ld_top, _ptr(workspace), workspace_bytes)
+    return (m, n, _f32(alpha), _ptr(Z), _dtype(z_type), ldz, _vec(target, torch.int64), _vec(logprob), _vec(lse),
+            _vec(entropy), top, _rows(top_index, torch.int64), _rows(top_logprob), ld_top, _ptr(workspace), workspace_bytes)
 
 
 def mpgemm_run_logprobs(handle, m, n, alpha, Z, z_type, ldz, target, logprob, lse, entropy, top, top_index, top_logprob,
@@ -590,8 +603,9 @@ class Gated:
     def __init__(self, act="none", bias_gate=None, bias_up=None, bias_type="f32", bias_stride=0, kept=None,
                  ld_kept=0, stride_kept=0):
         self.held = (bias_gate, bias_up, kept)
-        self.struct = _GatedStruct(_act(act), _ptr(bias_gate), _ptr(bias_up), _dtype(bias_type), bias_stride,
-                                   _ptr(kept), ld_kept, stride_kept)
+        gate, up = (_rows(x, getattr(x, "dtype", None)) for x in (bias_gate, bias_up))
+        self.struct = _GatedStruct(_act(act), gate, up, _dtype(bias_type), bias_stride, _ptr(kept), ld_kept,
+                                   stride_kept)
 
 
 class GatedGrad:
@@ -644,7 +658,7 @@ def mpgemm_check_gated_grad(*args) -> int:
 
 def _grouped_gated_args(transb, groups, rows, n, k, alpha, A, a_type, lda, offsets, B, b_type, ldb, stride_b,
                         stride_up, gated, D, d_type, ldd):
-    return (_op(transb), groups, rows, n, k, _f32(alpha), _ptr(A), _dtype(a_type), lda, _ptr(offsets), _ptr(B),
+    return (_op(transb), groups, rows, n, k, _f32(alpha), _ptr(A), _dtype(a_type), lda, _vec(offsets, torch.int32), _ptr(B),
             _dtype(b_type), ldb, stride_b, stride_up, _epi(gated), _ptr(D), _dtype(d_type), ldd)
 
 
@@ -662,7 +676,7 @@ def mpgemm_check_grouped_gated(*args) -> int:
 
 def _grouped_gated_grad_args(transb, groups, rows, n, k, alpha, A, a_type, lda, offsets, B, b_type, ldb, stride_b,
                              grad, D, d_type, ldd, stride_d, workspace, workspace_bytes):
-    return (_op(transb), groups, rows, n, k, _f32(alpha), _ptr(A), _dtype(a_type), lda, _ptr(offsets), _ptr(B),
+    return (_op(transb), groups, rows, n, k, _f32(alpha), _ptr(A), _dtype(a_type), lda, _vec(offsets, torch.int32), _ptr(B),
             _dtype(b_type), ldb, stride_b, _epi(grad), _ptr(D), _dtype(d_type), ldd, stride_d, _ptr(workspace),
             workspace_bytes)
 
