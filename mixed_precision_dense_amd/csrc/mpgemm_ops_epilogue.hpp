@@ -523,6 +523,39 @@ __device__ __forceinline__ void expert_tiles(const OpParams &p, int tile_rows, i
     }
 }
 
+// tile_coords without a last group of one or two tile rows: of five tile rows (517 rows), in groups of four, the fifth
+// would read op(B) once more with nothing beside it to share it (517 x 50021 x 1000, loss alone: 94 us so, 88
+// together).  Of more than two rounds of tiles (65536 / BM a round) up to seven a group (its gradients, where dW has 391 x
+// 8 tiles: 383 us with four, 363 with eight, 350 with seven), of fewer four (4925 x 1264 x 3411: 71.5 us, 77 with six to
+// eight; 6160 rows of 350 gated outputs over 3618 in tiles of 64: 64.3, 70.8 with seven).
+template <int BM>
+__device__ __forceinline__ void op_tile_coords(int wg, int tiles_m, int tiles_n, int &tm, int &tn) {
+    const int total = tiles_m * tiles_n, run = total / 8;
+    const int id = wg < run * 8 ? (wg % 8) * run + wg / 8 : wg;
+    if (tiles_m <= kGroupM + 2) {
+        tn = tiles_m == 1 ? id : id / tiles_m;
+        tm = id - tn * tiles_m;
+        return;
+    }
+    if (tiles_m % 16 == 0 && tiles_n % 16 == 0) return tile_coords(wg, tiles_m, tiles_n, tm, tn);
+    int rows, cut, rows_after;   // tile rows of a group, and from tile row `cut` on
+    if (total > 2 * (65536 / BM)) {
+        const int groups = (tiles_m + 6) / 7;
+        rows = tiles_m / groups;
+        rows_after = rows + 1;
+        cut = (groups - tiles_m % groups) * rows;
+    } else {
+        rows = kGroupM;
+        cut = ((tiles_m + 1) / kGroupM - 1) * kGroupM;
+        rows_after = tiles_m - cut;
+    }
+    const int before = id < cut * tiles_n ? 0 : cut;
+    if (before > 0) rows = rows_after;
+    const int group = (id - before * tiles_n) / (rows * tiles_n), in = id - (before + group * rows) * tiles_n;
+    tm = before + group * rows + in % rows;
+    tn = in / rows;
+}
+
 // The tile of workgroup `wg`; false: none is left for it.  Every wave of a workgroup finds it for
 // itself.  The experts' tiles follow each other, an expert's own by columns of tiles (which share
 // its weights); each XCD gets a contiguous run of them.
@@ -585,29 +618,36 @@ __device__ __forceinline__ bool locate(const OpParams &p, int wg, int split, int
         w.d_off = (int64_t)w.expert * p.stride_d;
         return true;
     }
-    if (p.splits > 1) {
-        // Ranges of k share nothing, the tiles of one range all of its rows and columns: each XCD gets a contiguous
-        // run over (range, tile), so that a range's operands come to one or two L2s and not to all eight
-        // (466 x 1000 over 50021 in 12 ranges of 40 tiles: 232 MB read, 62 us; tile by tile over the XCDs 541 MB, 102 us).
-        const int per = p.tiles_m * p.tiles_n, total = per * p.splits, run = total / 8, l = split * per + wg;
-        const int id = l < run * 8 ? (l % 8) * run + l / 8 : l;
-        w.split = split = id / per;
-        const int local = id - split * per;
-        w.tm = local % p.tiles_m;
-        w.tn = local / p.tiles_m;
-    } else {
-        tile_coords(wg, p.tiles_m, p.tiles_n, w.tm, w.tn);
-    }
-    w.tile = w.tm;
+    // Only the tiles of rows that take part are laid out: the workgroups of the others leave from the end of the
+    // grid and not from one XCD's run (2650 rows, half of them ignored, over 12305 columns, k = 2168, loss and gradients:
+    // 564 us, 635 with them in).
+    int tiles_m = p.tiles_m;
     if (p.count != nullptr) {
         const int count = max(uniform(p.count[0]), 0);
         if (p.count_k) {
             w.k = min(p.k, count);
         } else {
             w.m = min(p.m, count);
-            if (w.tm * BM >= w.m) return false;
+            tiles_m = (w.m + BM - 1) / BM;
         }
     }
+    const int per = tiles_m * p.tiles_n;
+    if (p.splits > 1) {
+        // Ranges of k share nothing, the tiles of one range all of its rows and columns: each XCD gets a contiguous
+        // run over (range, tile), so that a range's operands come to one or two L2s and not to all eight
+        // (466 x 1000 over 50021 in 12 ranges of 40 tiles: 232 MB read, 62 us; tile by tile over the XCDs 541 MB, 102 us).
+        const int total = per * p.splits, run = total / 8, l = split * p.tiles_m * p.tiles_n + wg;
+        if (l >= total) return false;
+        const int id = l < run * 8 ? (l % 8) * run + l / 8 : l;
+        w.split = split = id / per;
+        const int local = id - split * per;
+        w.tm = local % tiles_m;
+        w.tn = local / tiles_m;
+    } else {
+        if (wg >= per) return false;
+        op_tile_coords<BM>(wg, tiles_m, p.tiles_n, w.tm, w.tn);
+    }
+    w.tile = w.tm;
     if (p.splits > 1) {
         w.k = min(p.k_split, p.k - split * p.k_split);
         w.d_off = (int64_t)split * p.stride_split;
