@@ -162,12 +162,16 @@ def _vec(x, dtype=torch.float32) -> Optional[int]:
 
 
 def _rows(x, dtype=torch.float32) -> Optional[int]:
-    """The same for rows of such values, whose distance the call is told."""
+    """The same for rows of such values, whose distance the call is told.  (dtype None: any.)"""
+    if x is None:
+        return None
     if isinstance(x, torch.Tensor):
-        if x.dim() > 0 and x.shape[-1] > 1 and x.stride(-1) != 1:
+        if not x.is_contiguous() and x.dim() > 0 and x.shape[-1] > 1 and x.stride(-1) != 1:
             raise ValueError(f"rows with strides {x.stride()}: the values of a row must follow each other in memory")
-        if x.dtype is not dtype:
+        if dtype is not None and x.dtype is not dtype:
             raise ValueError(f"rows of {x.dtype}: their values must be {dtype}")
+        if x.is_cuda:
+            return x.data_ptr()
     return _ptr(x)
 
 
@@ -603,9 +607,8 @@ class Gated:
     def __init__(self, act="none", bias_gate=None, bias_up=None, bias_type="f32", bias_stride=0, kept=None,
                  ld_kept=0, stride_kept=0):
         self.held = (bias_gate, bias_up, kept)
-        gate, up = (_rows(x, getattr(x, "dtype", None)) for x in (bias_gate, bias_up))
-        self.struct = _GatedStruct(_act(act), gate, up, _dtype(bias_type), bias_stride, _ptr(kept), ld_kept,
-                                   stride_kept)
+        self.struct = _GatedStruct(_act(act), _rows(bias_gate, None), _rows(bias_up, None), _dtype(bias_type),
+                                   bias_stride, _ptr(kept), ld_kept, stride_kept)
 
 
 class GatedGrad:
