@@ -54,6 +54,7 @@ struct OpParams {
     int d_f32;                   // else the inputs' type
     int64_t ldd;
     int lines;                   // D's (and aux's) rows are whole 128-byte lines
+    int wide;                    // D's rows are a multiple of 32 KB apart
     float *colsum;               // OP_SLOPE: two rows of partial sums per row tile, or nullptr
     int64_t ld_colsum;
     int groups_kind, groups;

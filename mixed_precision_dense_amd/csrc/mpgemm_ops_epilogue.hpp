@@ -528,13 +528,25 @@ __device__ __forceinline__ void expert_tiles(const OpParams &p, int tile_rows, i
 // together).  Of more than two rounds of tiles (65536 / BM a round) up to seven a group (its gradients, where dW has 391 x
 // 8 tiles: 383 us with four, 363 with eight, 350 with seven), of fewer four (4925 x 1264 x 3411: 71.5 us, 77 with six to
 // eight; 6160 rows of 350 gated outputs over 3618 in tiles of 64: 64.3, 70.8 with seven).
+//
+// wide: D's rows lie a multiple of 32 KB apart, over which the memory's channels (128 of 256 bytes) repeat: at the end of
+// a round of equal tiles, the columns of 16 of them meet in a part of the channels, whatever the row.  There the regions
+// of tile_coords become 8 x 32 tiles (gradient of a gated product, 4096 x 8192, D side by side: over 4096 268 -> 251 us,
+// over 1024 140 -> 119; 4096 x 16384 x 4096, BF16 D 415 -> 404.  With other distances the two come to the same).
 template <int BM>
-__device__ __forceinline__ void op_tile_coords(int wg, int tiles_m, int tiles_n, int &tm, int &tn) {
+__device__ __forceinline__ void op_tile_coords(bool wide, int wg, int tiles_m, int tiles_n, int &tm, int &tn) {
     const int total = tiles_m * tiles_n, run = total / 8;
     const int id = wg < run * 8 ? (wg % 8) * run + wg / 8 : wg;
     if (tiles_m <= kGroupM + 2) {
         tn = tiles_m == 1 ? id : id / tiles_m;
         tm = id - tn * tiles_m;
+        return;
+    }
+    if (BM == 256 && wide && tiles_m % 8 == 0 && tiles_n % 32 == 0) {
+        const int xcd = wg % 8, i = wg / 8 % 32, round = wg / 256, regions = tiles_n / 32;
+        const int ra = round / regions, rb = round % regions;
+        tm = 8 * ra + 4 * (xcd % 2) + i % 4;
+        tn = 32 * (ra % 2 == 0 ? rb : regions - 1 - rb) + 8 * (xcd / 2) + i / 4;
         return;
     }
     if (tiles_m % 16 == 0 && tiles_n % 16 == 0) return tile_coords(wg, tiles_m, tiles_n, tm, tn);
@@ -645,7 +657,7 @@ __device__ __forceinline__ bool locate(const OpParams &p, int wg, int split, int
         w.tn = local / tiles_m;
     } else {
         if (wg >= per) return false;
-        op_tile_coords<BM>(wg, tiles_m, p.tiles_n, w.tm, w.tn);
+        op_tile_coords<BM>(p.wide, wg, tiles_m, p.tiles_n, w.tm, w.tn);
     }
     w.tile = w.tm;
     if (p.splits > 1) {

@@ -59,3 +59,20 @@ def test_gradients_with_rows_that_do_not_count(m, n, k, share, t):
     ref.assert_within(got[3], dx, dx_err, "dX")
     ref.assert_within(got[4], dw, dw_err, "dW")
     assert bool((got[3][ignored] == 0).all())
+
+
+@pytest.mark.parametrize("m", [2000, 4096, 6144])
+def test_rows_of_a_multiple_of_32_kb(m):
+    """Where D's rows are that far apart a round of 256-wide tiles is laid out differently."""
+    n, k = 8192, 1000
+    g = rng(m)
+    a, b = (torch.randint(-3, 4, (r, k), generator=g).bfloat16().cuda() for r in (m, n))
+    want = a.float() @ b.float().t()
+    for out in ("f32", "bf16"):
+        ld = n if out == "f32" else 2 * n
+        d = torch.full((m + 1, ld), ref.SENTINEL, dtype=ref.TYPES[out], device="cuda")
+        mp.mpgemm_run_epilogue(handle().h, False, True, m, n, k, 1.0, a, "bf16", k, b, "bf16", k, mp.Epilogue(), 0.0, None, out, ld, d, out,
+                               ld)
+        torch.cuda.synchronize()
+        assert torch.equal(d[:m, :n], want.to(ref.TYPES[out])), (m, out)
+        assert bool((d[m] == ref.SENTINEL).all()) and bool((d[:, n:] == ref.SENTINEL).all())
