@@ -526,7 +526,9 @@ __device__ __forceinline__ void expert_tiles(const OpParams &p, int tile_rows, i
 // tile_coords without a last group of one or two tile rows: of five tile rows (517 rows), in groups of four, the fifth
 // would read op(B) once more with nothing beside it to share it (517 x 50021 x 1000, loss alone: 94 us so, 88
 // together).  Of more than two rounds of tiles (65536 / BM a round) up to seven a group (its gradients, where dW has 391 x
-// 8 tiles: 383 us with four, 363 with eight, 350 with seven), of fewer four (4925 x 1264 x 3411: 71.5 us, 77 with six to
+// 8 tiles: 383 us with four, 363 with eight, 350 with seven), of 256-wide ones eight where that leaves none over, since an XCD
+// has 32 at once (2047 x 50021 x 1000, loss alone: 236 us with four to seven, 232 with eight; but 31 x 20 tiles, 7868 x
+// 5016 x 1880, 221 with six and seven, 240 with seven and eight), of fewer four (4925 x 1264 x 3411: 71.5 us, 77 with six to
 // eight; 6160 rows of 350 gated outputs over 3618 in tiles of 64: 64.3, 70.8 with seven).
 //
 // wide: D's rows lie a multiple of 32 KB apart, over which the memory's channels (128 of 256 bytes) repeat: at the end of
@@ -552,7 +554,7 @@ __device__ __forceinline__ void op_tile_coords(bool wide, int wg, int tiles_m, i
     if (tiles_m % 16 == 0 && tiles_n % 16 == 0) return tile_coords(wg, tiles_m, tiles_n, tm, tn);
     int rows, cut, rows_after;   // tile rows of a group, and from tile row `cut` on
     if (total > 2 * (65536 / BM)) {
-        const int groups = (tiles_m + 6) / 7;
+        const int groups = BM == 256 && tiles_m % 8 == 0 ? tiles_m / 8 : (tiles_m + 6) / 7;
         rows = tiles_m / groups;
         rows_after = rows + 1;
         cut = (groups - tiles_m % groups) * rows;
