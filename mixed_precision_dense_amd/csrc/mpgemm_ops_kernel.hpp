@@ -20,7 +20,7 @@
 // 128: each wave holds both factors of 64 columns, which meet in its staged rows.  8192 x 4096 outputs over 2048 with
 // SiLU 212 us, where one plain product of 8192 x 8192 over 2048 takes 208: the matrix instructions and the clock that the
 // power allows them bound it.  Its gradient has the tiles of a plain product, reads G and U and stores dG, dU and H: 4096
-// x 8192 over 4096 254 us, 187 of them the product's; the rest is 335 MB that all CUs move at the end of a round.
+// x 8192 over 4096 243 us, 187 of them the product's; the rest is 335 MB that all CUs move at the end of a round.
 #pragma once
 
 #include "mpgemm_ops_epilogue.hpp"
