@@ -39,7 +39,7 @@ mpg::OpParams product(const OpPlan &plan, int64_t m, int64_t n, int64_t k, float
     p.splits = 1;
     p.k_split = (int)k;
     p.lines = lines(D, ldd, d_f32 ? 4 : 2);
-    p.wide = ldd * (d_f32 ? 4 : 2) % 32768 == 0;
+    p.wide = ldd > 0 && ldd * (d_f32 ? 4 : 2) % 32768 == 0;   // (the losses store no D)
     return p;
 }
 
