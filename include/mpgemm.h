@@ -460,7 +460,9 @@ mpgemm_status_t mpgemm_run_linear_distill(mpgemm_handle_t handle, int64_t m, int
  * 0 in rows that do not count,
  *   dX = alpha * P W,   dW = alpha * P^T X      (type's; either may be NULL and is then skipped).
  *   lse, picked: as mpgemm_run_linear_distill wrote them.  grad: m FP32 values.
- *   What is said of P and of rows that do not count at mpgemm_run_linear_ce_grad holds here.
+ *   What is said of P and of rows that do not count at mpgemm_run_linear_ce_grad holds here.  P's rounding to
+ *   the inputs' type adds about as much to the error of dX and dW as their own rounding: in norm 1.4 times
+ *   what dX and dW rounded from exact sums would have.
  *   workspace: mpgemm_linear_distill_workspace_size(m, n, k, top, type, 1) bytes, which is also
  *   enough for mpgemm_run_linear_distill. */
 mpgemm_status_t mpgemm_run_linear_distill_grad(mpgemm_handle_t handle, int64_t m, int64_t n, int64_t k,

@@ -7,6 +7,12 @@
 // The first term of P is the cross entropy's, with log Q taken from lse and no target; at the teacher's
 // columns, where a trained student's two terms all but cancel, P is formed in FP32 from the logits that
 // the forward call kept, and rounded once.
+//
+// P is held in the inputs' type: the matrix instructions take both factors in one type, and a second term of P
+// (what its rounding left) would double both products.  No entry stands out as a target's p - 1 does in the cross
+// entropy, where it is a power of two and exact, so that here the rounding of P is as much of the gradients'
+// error as their own: dX and dW of 4096 x 128000 x 4096 in BF16 are 2.34e-3 and 2.35e-3 off in norm, 1.66e-3 with P in FP32,
+// those of 517 x 50021 x 1000 in FP16 2.9e-4, 2.1e-4 with P in FP32.
 #include "mpgemm_ops_epilogue.hpp"
 
 namespace mpg {
