@@ -433,7 +433,8 @@ typedef struct {
                                  0 .. n - 1 (-1, as a rule) does not count */
     const float *logit;       /* m x top (ld): the teacher's logits there */
     int64_t ld;               /* >= top; picked's too */
-    float scale;              /* of the teacher's logits: 1 / its temperature */
+    float scale;              /* of the teacher's logits, -1e30 .. 1e30: 1 / its temperature, as a rule;
+                                 0 gives all entries the same share */
     const float *lse;         /* m log-sum-exps of the teacher's scaled logits over all columns; NULL:
                                  over the entries that count */
 } mpgemm_teacher_t;
@@ -444,7 +445,7 @@ typedef struct {
  * A temperature of the student is part of alpha.  Without the teacher's lse the q of a row sum to 1
  * and the loss is the divergence of the student from the teacher's top entries; with it, the part of
  * that divergence that lies in them.  Entries of the same column add up as they stand.  A logit of
- * -infinity has no mass; a row none of whose entries has any does not count and has loss 0.
+ * -infinity has no mass, whatever the scale; a row none of whose entries has any does not count and has loss 0.
  *   loss, lse: m FP32 values each.  picked: m x top (teacher->ld) FP32 values, z at the entries'
  *   columns (0 where an entry does not count), which the gradient takes.
  *   workspace: mpgemm_linear_distill_workspace_size(m, n, k, top, type, 0) bytes. */

@@ -642,6 +642,7 @@ namespace {
 
 mpgemm_status_t check_teacher(const mpgemm_teacher_t *t) {
     if (!t || t->top < 1 || t->ld < t->top) return MPGEMM_STATUS_INVALID_VALUE;
+    if (!(t->scale >= -1.0e30f && t->scale <= 1.0e30f)) return MPGEMM_STATUS_INVALID_VALUE;   // (NaN too)
     return t->top <= mpg::kMostTop && t->ld <= kOpMaxSize ? MPGEMM_STATUS_SUCCESS : MPGEMM_STATUS_NOT_SUPPORTED;
 }
 

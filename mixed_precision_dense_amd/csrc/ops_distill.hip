@@ -38,6 +38,9 @@ __device__ __forceinline__ float wave_max(float v) {
     for (int d = 1; d < 64; d *= 2) v = fmaxf(v, __shfl_xor(v, d, 64));
     return v;
 }
+// y in units of log 2; f = scale / log 2.  A logit of -infinity has no mass whatever the scale is: 0 times it would be
+// NaN, and a negative number +infinity.
+__device__ __forceinline__ float scaled(float f, float logit) { return logit == -__builtin_inff() ? logit : f * logit; }
 // exp(y - level) from the value in units of log 2; an entry without mass is exactly 0.
 __device__ __forceinline__ float share_of(float y2, float level2) {
     return y2 == -__builtin_inff() ? 0.0f : fast_exp2(y2 - level2);
@@ -52,7 +55,7 @@ __device__ __forceinline__ void teacher_row(const Teacher &t, int64_t row, int n
     bool nan = false;
     for (int j = lane; j < t.top; j += 64)
         if (entry_column(t, row, j, n) >= 0) {
-            const float y = f * logit[j];
+            const float y = scaled(f, logit[j]);
             top = fmaxf(top, y);
             nan |= y != y;
         }
@@ -61,7 +64,7 @@ __device__ __forceinline__ void teacher_row(const Teacher &t, int64_t row, int n
     const float base = t.lse != nullptr ? t.lse[row] * kLog2e : stat_base(top);
     float sum = 0.0f;
     for (int j = lane; j < t.top; j += 64)
-        if (entry_column(t, row, j, n) >= 0) sum += share_of(f * logit[j], base);
+        if (entry_column(t, row, j, n) >= 0) sum += share_of(scaled(f, logit[j]), base);
     sum = wave_sum(sum);
     level2 = t.lse != nullptr ? base : base + __log2f(sum);
     mass = t.lse != nullptr || sum == 0.0f || sum != sum ? sum : 1.0f;
@@ -179,7 +182,7 @@ __global__ __launch_bounds__(64 * kMergeWaves) void distill_merge_kernel(Teacher
             float s = 0.0f;
             for (int j = lane; j < t.top; j += 64) {
                 if (entry_column(t, row, j, n) < 0) continue;
-                const float y2 = f * t.logit[row * t.ld + j], q = share_of(y2, level2);
+                const float y2 = scaled(f, t.logit[row * t.ld + j]), q = share_of(y2, level2);
                 if (q != 0.0f) s = __builtin_fmaf(q, (y2 - level2) * kLn2 + (own - (PICK ? own_picked[j] : picked[row * t.ld + j])), s);
             }
             s = wave_sum(s);
@@ -225,7 +228,7 @@ __global__ __launch_bounds__(64 * kWaves) void scatter_kernel(Teacher t, int m, 
             float q = 0.0f;
             for (int i0 = 0; i0 < t.top; i0 += 64) {
                 const int o = i0 == j - lane ? v : entry_column(t, row, i0 + lane, n);
-                const float s = o < 0 ? 0.0f : share_of(f * t.logit[row * t.ld + i0 + lane], l2);
+                const float s = o < 0 ? 0.0f : share_of(scaled(f, t.logit[row * t.ld + i0 + lane]), l2);
                 const int most = min(64, t.top - i0);
                 for (int i = 0; i < most; ++i) {
                     const int other = __builtin_amdgcn_readlane(o, i);
