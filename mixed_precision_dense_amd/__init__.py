@@ -347,9 +347,10 @@ def _act(act: Union[str, int]) -> int:
 def _f32(v):
     """A scalar argument: the library reads it before the call returns and never writes it.  The first few
     numbers that a program uses (temperatures, scales) are kept: making one takes 2 us, looking it up 0.1.
-    (Plain floats only: anything else could change its value under the same key.)"""
+    (Plain floats only: anything else could change its value under the same key, and only ctypes says what a
+    number is: float() would take text.)"""
     if type(v) is not float:
-        v = float(v)
+        return ctypes.byref(ctypes.c_float(v))
     known = _F32.get(v)
     if known is None:
         known = ctypes.byref(ctypes.c_float(v))
