@@ -129,9 +129,11 @@ struct Teacher {
     float scale;
     const float *lse;   // or nullptr
 };
-// the loss from the statistics and the logits at the teacher's columns, which are formed and kept too
+// the loss from the statistics and the logits at the teacher's columns, which are formed and kept too: by the
+// kernel that joins the statistics (itself) or by one before it
+constexpr int kMergePicks = 32;   // entries of a row that the joining kernel's waves form in one turn
 int launch_distill_merge(bool bf16, const Teacher &t, const CeStat *stats, int parts, int m, int n, int k, float alpha, const void *X,
-                         int64_t ldx, const void *W, int64_t ldw, float *picked, float *loss, float *lse, void *stream);
+                         int64_t ldx, const void *W, int64_t ldw, float *picked, float *loss, float *lse, bool itself, void *stream);
 int launch_mass(const Teacher &t, int m, int n, float *level, float *mass, void *stream);
 int launch_scatter(bool bf16, const Teacher &t, int m, int n, int first, int have, const float *level, const float *mass,
                    const float *lse, const float *picked, const int *place, const float *weight, void *P, int64_t ldp, void *stream);

@@ -399,7 +399,7 @@ mpgemm_status_t mpgemm_run_linear_distill(mpgemm_handle_t handle, int64_t m, int
     p.parts = L.parts;
     MPGEMM_TRY(launch(L.logits, bf16, false, true, p, stream));
     return queued(mpg::launch_distill_merge(bf16, t, p.stats, L.parts, (int)m, (int)n, (int)k, *alpha, X, ldx, W, ldw, picked, loss, lse,
-                                            stream));
+                                            merge_picks(m, t.top, k), stream));
 }
 
 mpgemm_status_t mpgemm_run_linear_distill_grad(mpgemm_handle_t handle, int64_t m, int64_t n, int64_t k, const float *alpha,

@@ -302,6 +302,18 @@ bool distill_layout(int64_t m, int64_t n, int64_t k, bool train, DistillLayout &
     return true;
 }
 
+// That saves a launch where a workgroup's waves have a turn of entries at most, or where there is a row for every CU, work
+// that outweighs the launch, and k enough for the lanes of a wave.  Below 256 rows the others idle.  Measured (us of
+// the loss, apart / itself):
+//   n = 32000, k = 4096: 8 rows of 20 entries 73 / 66, 8 of 128 72 / 86
+//   n = 8192, k = 4096: 8 of 1024 53 / 196, 16 of 512 46 / 113, 64 of 64 41 / 44, 64 of 128 46 / 56, 128 of 64 47 / 47, 128 of 512
+//     114 / 132, 256 of 48 52.7 / 51.5, 256 of 128 77 / 73, 512 of 128 122 / 115, 1024 of 64 142 / 135;  k = 8192: 8 of 1024 73 / 344
+//   k = 2048: 256 of 512 99.5 / 97.6, 4096 of 64 255 / 236;  k = 1024: 512 of 1000 147 / 142, 2048 of 64 74.5 / 74.9
+//   k = 512: 1024 of 48 29.9 / 29.9;  k = 256: 4096 of 40 71 / 85
+bool merge_picks(int64_t m, int64_t top, int64_t k) {
+    return top <= mpg::kMergePicks || (m >= kCus && k >= 512 && m * top >= ((int64_t)1 << 25) / k);
+}
+
 }  // namespace mpg_host
 
 using namespace mpg_host;

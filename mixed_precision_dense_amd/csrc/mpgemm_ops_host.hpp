@@ -60,6 +60,8 @@ struct DistillLayout {
     uint64_t off_level, off_mass, total;
 };
 bool distill_layout(int64_t m, int64_t n, int64_t k, bool train, DistillLayout &D);
+// Whether the kernel that joins the statistics forms the logits at the teacher's columns itself.
+bool merge_picks(int64_t m, int64_t top, int64_t k);
 
 // Log probabilities: the parts of a row (a workgroup each) and where they are kept.
 struct LogprobLayout {

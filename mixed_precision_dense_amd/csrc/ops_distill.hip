@@ -133,6 +133,7 @@ __global__ __launch_bounds__(64 * kWaves) void picked_kernel(Teacher t, int m, i
 // One workgroup per row: lse from the parts' statistics, then the loss from the picked logits, which it
 // forms itself (PICK) or finds formed.
 constexpr int kMergeWaves = 8;
+static_assert(kEntries * kMergeWaves == kMergePicks, "a turn of the merging kernel's waves, as the rule counts it");
 template <int IN, bool PICK>
 __global__ __launch_bounds__(64 * kMergeWaves) void distill_merge_kernel(Teacher t, const CeStat *stats, int parts, int m, int n, int k,
                                                                          float alpha, const uint16_t *X, int64_t ldx,
@@ -254,12 +255,7 @@ int64_t by_waves(int64_t items) { return (items + kWaves - 1) / kWaves; }
 
 template <int IN>
 int launch_merge_type(const Teacher &t, const CeStat *stats, int parts, int m, int n, int k, float alpha, const uint16_t *x, int64_t ldx,
-                      const uint16_t *w, int64_t ldw, float *picked, float *loss, float *lse, void *stream) {
-    // The merging kernel picks the logits itself where its waves have a turn of them at most, or rows keep all
-    // CUs busy: that saves a launch (us with the loss before it, n = 32000, k = 4096, apart / itself: 8 rows of 20
-    // entries 73 / 66, 8 of 128 72 / 86, 8 of 1000 92 / 264, 64 of 64 72 / 77; k = 2048: 512 of 64 82 / 78, 4096 of 64
-    // 563 / 551).
-    const bool itself = t.top <= kEntries * kMergeWaves || (int64_t)m * t.top * k >= ((int64_t)1 << 25);
+                      const uint16_t *w, int64_t ldw, float *picked, float *loss, float *lse, bool itself, void *stream) {
     if (!itself) {
         void *args[] = {const_cast<Teacher *>(&t), &m, &n, &k, &alpha, &x, &ldx, &w, &ldw, &picked};
         const int e = launch(reinterpret_cast<const void *>(&picked_kernel<IN>), by_waves((int64_t)m * ((t.top + kEntries - 1) / kEntries)),
@@ -275,9 +271,9 @@ int launch_merge_type(const Teacher &t, const CeStat *stats, int parts, int m, i
 }  // namespace
 
 int launch_distill_merge(bool bf16, const Teacher &t, const CeStat *stats, int parts, int m, int n, int k, float alpha, const void *X,
-                         int64_t ldx, const void *W, int64_t ldw, float *picked, float *loss, float *lse, void *stream) {
+                         int64_t ldx, const void *W, int64_t ldw, float *picked, float *loss, float *lse, bool itself, void *stream) {
     const auto f = bf16 ? launch_merge_type<IN_BF16> : launch_merge_type<IN_F16>;
-    return f(t, stats, parts, m, n, k, alpha, (const uint16_t *)X, ldx, (const uint16_t *)W, ldw, picked, loss, lse, stream);
+    return f(t, stats, parts, m, n, k, alpha, (const uint16_t *)X, ldx, (const uint16_t *)W, ldw, picked, loss, lse, itself, stream);
 }
 
 int launch_mass(const Teacher &t, int m, int n, float *level, float *mass, void *stream) {
