@@ -10,13 +10,16 @@
 //
 // The largest.  Keys order values first and lower indexes second, so that no two are alike and the result
 // does not depend on the order of reading.  While the logits stream by, only the maximum of every 32 elements
-// of a lane is kept (in the LDS).  The top-th largest of the 256 lanes' maxima is then a bound T that
-// at least `top` elements reach; few of the kept maxima do, and only their elements are read once more
+// of a lane is kept (in the LDS).  The top-th largest of the workgroup's lanes' maxima (256, or 64 where a wave has
+// a row) is then a bound T that at least `top` elements reach; few of the kept maxima do, and only their elements are read once more
 // (4095 x 128000 BF16 with 8: about 9 of 4096 maxima a row).  What reaches T is put
 // in order by one wave.  Where too many do, as equal values, those above T are taken and then the first that
-// equal it; where even these are too many (rising rows) or a NaN hides the maxima, the workgroup goes through
-// its part again with lists that let in what is above their last place (4095 x 128000 BF16: constant rows and
-// rows masked but for ten as random ones; rising rows so with 20, but 4.3 ms with 64).  With such lists alone,
+// equal it; where even these are too many or a NaN hides the maxima, the workgroup goes through its part again with
+// lists that let in what is above their last place.  That is the way of rising rows, and of random ones with so
+// many alternatives that T is near the least of the lanes' maxima: beyond about 48 below 2560 columns (4096 x 2048 BF16 23 us with
+// 48, 40 with 64), elsewhere such rows get four waves.  (4095 x 128000 BF16: constant rows and
+// rows masked but for ten as random ones; rising rows so with 20, but 4.1 ms with 64, where random ones take 0.22; 4096 x
+// 32000 1.1 ms and 0.075; 4096 x 4096 with 20 0.12 and 0.018.)  With such lists alone,
 // kept while streaming, 4095 x 128000 BF16 took 340 us with 8 alternatives and 640 with 64; so 198 and 211
 // (5.3 and 5.0 TB/s), against 188 without any: the row's bytes bound it.  Of a short row most of the time
 // is the chain of dependent lane exchanges (16 x 4096: 8.3 us, an empty launch 4).
