@@ -88,6 +88,7 @@ def test_forward_sizes(m, n, k, tb, layout):
 
 
 # one size for each kernel that the rules can choose; (groups' mean rows, n, k) with both storages
+# (of few rows and many columns, and tiles of 256, in tests/gated_cases.py: no size here reaches those)
 KERNELS = [(0, 9, 100, 200), (0, 9, 24600, 72), (0, 30, 100, 200), (0, 30, 12000, 72), (0, 60, 100, 200), (0, 200, 100, 70),
            (0, 900, 1100, 130), (0, 2100, 2200, 72), (3, 12, 100, 200), (40, 300, 500, 72), (3, 60, 200, 136), (3, 600, 300, 72)]
 
