@@ -41,9 +41,15 @@ __device__ __forceinline__ float wave_max(float v) {
 // y in units of log 2; f = scale / log 2.  A logit of -infinity has no mass whatever the scale is: 0 times it would be
 // NaN, and a negative number +infinity.
 __device__ __forceinline__ float scaled(float f, float logit) { return logit == -__builtin_inff() ? logit : f * logit; }
-// exp(y - level) from the value in units of log 2; an entry without mass is exactly 0.
-__device__ __forceinline__ float share_of(float y2, float level2) {
-    return y2 == -__builtin_inff() ? 0.0f : fast_exp2(y2 - level2);
+// y - level in units of log 2, rounded once; -infinity for an entry without mass.
+__device__ __forceinline__ float log_share(float f, float logit, float level2) {
+    const float y2 = scaled(f, logit);
+    return y2 == -__builtin_inff() ? y2 : __builtin_fmaf(f, logit, -level2);
+}
+// exp of it; an entry without mass is exactly 0.
+__device__ __forceinline__ float share_of(float f, float logit, float level2) {
+    const float d = log_share(f, logit, level2);
+    return d == -__builtin_inff() ? 0.0f : fast_exp2(d);
 }
 
 // L (in units of log 2) and Q of a row, by a whole wave.  Q is 0 where no entry has mass: the row does
@@ -64,7 +70,7 @@ __device__ __forceinline__ void teacher_row(const Teacher &t, int64_t row, int n
     const float base = t.lse != nullptr ? t.lse[row] * kLog2e : stat_base(top);
     float sum = 0.0f;
     for (int j = lane; j < t.top; j += 64)
-        if (entry_column(t, row, j, n) >= 0) sum += share_of(scaled(f, logit[j]), base);
+        if (entry_column(t, row, j, n) >= 0) sum += share_of(f, logit[j], base);
     sum = wave_sum(sum);
     level2 = t.lse != nullptr ? base : base + __log2f(sum);
     mass = t.lse != nullptr || sum == 0.0f || sum != sum ? sum : 1.0f;
@@ -183,8 +189,8 @@ __global__ __launch_bounds__(64 * kMergeWaves) void distill_merge_kernel(Teacher
             float s = 0.0f;
             for (int j = lane; j < t.top; j += 64) {
                 if (entry_column(t, row, j, n) < 0) continue;
-                const float y2 = scaled(f, t.logit[row * t.ld + j]), q = share_of(y2, level2);
-                if (q != 0.0f) s = __builtin_fmaf(q, (y2 - level2) * kLn2 + (own - (PICK ? own_picked[j] : picked[row * t.ld + j])), s);
+                const float d = log_share(f, t.logit[row * t.ld + j], level2), q = share_of(f, t.logit[row * t.ld + j], level2);
+                if (q != 0.0f) s = __builtin_fmaf(q, d * kLn2 + (own - (PICK ? own_picked[j] : picked[row * t.ld + j])), s);
             }
             s = wave_sum(s);
             if (lane == 0) {
@@ -229,7 +235,7 @@ __global__ __launch_bounds__(64 * kWaves) void scatter_kernel(Teacher t, int m, 
             float q = 0.0f;
             for (int i0 = 0; i0 < t.top; i0 += 64) {
                 const int o = i0 == j - lane ? v : entry_column(t, row, i0 + lane, n);
-                const float s = o < 0 ? 0.0f : share_of(scaled(f, t.logit[row * t.ld + i0 + lane]), l2);
+                const float s = o < 0 ? 0.0f : share_of(f, t.logit[row * t.ld + i0 + lane], l2);
                 const int most = min(64, t.top - i0);
                 for (int i = 0; i < most; ++i) {
                     const int other = __builtin_amdgcn_readlane(o, i);
