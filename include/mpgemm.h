@@ -511,6 +511,8 @@ mpgemm_status_t mpgemm_check_linear_distill_grad(int64_t m, int64_t n, int64_t k
  *   A logit of -infinity has probability 0.  A row of nothing else has no distribution: lse, logprob and
  *   top_logprob are -infinity, the entropy 0.  A NaN or +infinity makes the row's numbers NaN (its
  *   top_index are columns in no particular order).
+ *   The time depends on the values where there are many alternatives: rows that rise along the columns take up
+ *   to 20 times as long as random ones (4095 x 128000 BF16 with 64: 4.1 ms and 0.22), masked and constant rows no longer.
  *   ldz goes up to 2^31.  workspace: mpgemm_logprobs_workspace_size(m, n, z_type, top) bytes. */
 mpgemm_status_t mpgemm_run_logprobs(mpgemm_handle_t handle, int64_t m, int64_t n, const float *alpha,
                                     const void *Z, mpgemm_dtype_t z_type, int64_t ldz,

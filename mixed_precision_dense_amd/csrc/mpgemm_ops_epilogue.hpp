@@ -534,7 +534,8 @@ __device__ __forceinline__ void expert_tiles(const OpParams &p, int tile_rows, i
 // wide: D's rows lie a multiple of 32 KB apart, over which the memory's channels (128 of 256 bytes) repeat: at the end of
 // a round of equal tiles, the columns of 16 of them meet in a part of the channels, whatever the row.  There the regions
 // of tile_coords become 8 x 32 tiles (gradient of a gated product, 4096 x 8192, D side by side: over 4096 268 -> 251 us,
-// over 1024 140 -> 119; 4096 x 16384 x 4096, BF16 D 415 -> 404.  With other distances the two come to the same).
+// over 1024 140 -> 119; 4096 x 16384 x 4096, BF16 D 415 -> 404.  With other distances the two come to the same).  Only whole
+// rounds are laid out so, 2048 rows by 8192 columns.
 template <int BM>
 __device__ __forceinline__ void op_tile_coords(bool wide, int wg, int tiles_m, int tiles_n, int &tm, int &tn) {
     const int total = tiles_m * tiles_n, run = total / 8;
