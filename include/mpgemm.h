@@ -462,8 +462,8 @@ mpgemm_status_t mpgemm_run_linear_distill(mpgemm_handle_t handle, int64_t m, int
  *   dX = alpha * P W,   dW = alpha * P^T X      (type's; either may be NULL and is then skipped).
  *   lse, picked: as mpgemm_run_linear_distill wrote them.  grad: m FP32 values.
  *   What is said of P and of rows that do not count at mpgemm_run_linear_ce_grad holds here.  P's rounding to
- *   the inputs' type adds about as much to the error of dX and dW as their own rounding: in norm 1.4 times
- *   what dX and dW rounded from exact sums would have.
+ *   the inputs' type adds about as much to the error of dX and dW as their own rounding: in norm about
+ *   1.4 times what dX and dW rounded from exact sums would have, more where the sums cancel.
  *   workspace: mpgemm_linear_distill_workspace_size(m, n, k, top, type, 1) bytes, which is also
  *   enough for mpgemm_run_linear_distill. */
 mpgemm_status_t mpgemm_run_linear_distill_grad(mpgemm_handle_t handle, int64_t m, int64_t n, int64_t k,
@@ -512,7 +512,7 @@ mpgemm_status_t mpgemm_check_linear_distill_grad(int64_t m, int64_t n, int64_t k
  *   top_logprob are -infinity, the entropy 0.  A NaN or +infinity makes the row's numbers NaN (its
  *   top_index are columns in no particular order).
  *   The time depends on the values where there are many alternatives: rows that rise along the columns take up
- *   to 20 times as long as random ones (4095 x 128000 BF16 with 64: 4.1 ms and 0.22), masked and constant rows no longer.
+ *   to 20 times as long as random ones (4095 x 128000 BF16 with 64: 4.1 ms and 0.22); masked and constant rows do not.
  *   ldz goes up to 2^31.  workspace: mpgemm_logprobs_workspace_size(m, n, z_type, top) bytes. */
 mpgemm_status_t mpgemm_run_logprobs(mpgemm_handle_t handle, int64_t m, int64_t n, const float *alpha,
                                     const void *Z, mpgemm_dtype_t z_type, int64_t ldz,

@@ -283,8 +283,8 @@ LogprobLayout logprob_layout(int64_t m, int64_t n, int bytes, int64_t top) {
     //   1024 x 32000 25.5 / 22.8;  4096 x 1000 14.0 / 34.3;  4096 x 32000 59.9 / 77.4 (FP32 107 / 103)
     // But with many alternatives 64 lanes' maxima bound them too loosely: of random rows about 64 log(64 / (64 - top))
     // elements reach the bound (44 for 32, 75 for 44, 266 and more for 64), and where these lie in more than 64 of the
-    // lanes' turns (2 a lane at 4096 columns, 16 at 32768) the row is gone through again with lists.  With 256 lanes all
-    // but the longest find them; below 2560 columns most of these have nothing to read (BF16, one wave / four):
+    // lanes' turns (2 a lane at 4096 columns, 16 at 32768) the row is gone through again with lists.  256 lanes' maxima
+    // bound any number of them well enough; below 2560 columns most of these have nothing to read (BF16, one wave / four):
     //   4096 x 2048, 48 alternatives 23 / 43, 64 40 / 91;  4096 x 2560, 64 39 / 49 (FP32 48 / 44, 64 rows 22 / 14)
     //   4096 x 3504, 44 30 / 39, 48 38 / 40, 56 45 / 42;  64 x 3504, 48 22 / 12;  4096 x 4096, 40 21 / 38, 48 42 / 40, 64 50 / 42
     //   (FP32 28 / 34, 54 / 37, 61 / 38);  4096 x 6000, 36 24 / 36, 40 38 / 38, 48 58 / 40;  1024 x 8192, 36 15 / 14, 40 32 / 14
